@@ -245,6 +245,49 @@ TEMX_API te_mx_status te_mx_layernorm_quantize(const void* x, int64_t rows, int6
                                                uint8_t* q_col, uint8_t* s_col, int64_t ld_s_col,
                                                float* mu, float* rsigma, void* stream);
 
+/* Element types of the LayerNorm entry points below. */
+typedef enum te_mx_dtype { TE_MX_BF16 = 0, TE_MX_FP16 = 1, TE_MX_FP32 = 2 } te_mx_dtype;
+
+/* te_mx_layernorm — LayerNorm whose output keeps the activations' type (the
+ * norm in front of what is not an MXFP8 GEMM; te_mx_layernorm_quantize feeds
+ * those).  Per row r of x: mu, var, rsigma and y as defined there (biased
+ * variance, eps > 0 and finite), all in fp32, y rounded once to its type.
+ *   x     [rows x hidden] of `dtype`, row pitch ld_x elements (device);
+ *   gamma [hidden] of `param_dtype`, which is `dtype` or TE_MX_FP32;
+ *   beta  [hidden] of `param_dtype`, or NULL (no shift);
+ *   y     [rows x hidden] of `dtype`, pitch ld_y; y = x in place is allowed
+ *         (the same pointer and pitch);
+ *   mu, rsigma  fp32 [rows], for the backward pass; both NULL: not written.
+ * Pointers aligned to their elements; any hidden <= 2^24 and any pitches >=
+ * hidden (rows that start on 16-byte boundaries are read and written 16 bytes
+ * at a time); rows == 0 or hidden == 0 is a no-op.  Deterministic. */
+TEMX_API te_mx_status te_mx_layernorm(const void* x, int64_t rows, int64_t hidden, int64_t ld_x, int32_t dtype,
+                                      const void* gamma, const void* beta, int32_t param_dtype, float eps,
+                                      void* y, int64_t ld_y, float* mu, float* rsigma, void* stream);
+
+/* te_mx_layernorm_backward — gradients of te_mx_layernorm (and of the
+ * normalisation in te_mx_layernorm_quantize, which saves the same mu and
+ * rsigma).  With xh = (x - mu) rsigma and g = dy gamma:
+ *   dx = rsigma (g - mean(g) - xh mean(g xh))   per row,
+ *   dgamma[c] = sum_r dy[r][c] xh[r][c],  dbeta[c] = sum_r dy[r][c],
+ * in fp32, each result rounded once.
+ *   dy, x, dx  [rows x hidden] of `dtype`, pitches ld_dy, ld_x, ld_dx; dx may
+ *              be NULL (not computed) or dy itself (the same pointer and pitch);
+ *   dgamma, dbeta  [hidden] of `param_dtype`; dbeta may be NULL, or both (not
+ *              computed).  With rows == 0 they are set to zero;
+ *   workspace  device scratch of te_mx_layernorm_backward_workspace_size(rows,
+ *              hidden) bytes, 16-byte aligned, for dgamma / dbeta (else NULL);
+ *              its contents on entry do not matter and it is clobbered.
+ * Types, alignment and sizes as te_mx_layernorm.  The column sums are taken in
+ * a fixed order (deterministic).  TE_MX_ERR_WORKSPACE_TOO_SMALL if
+ * workspace_bytes is short. */
+TEMX_API size_t te_mx_layernorm_backward_workspace_size(int64_t rows, int64_t hidden);
+TEMX_API te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t rows,
+                                               int64_t hidden, int32_t dtype, const void* gamma, int32_t param_dtype,
+                                               const float* mu, const float* rsigma, void* dx, int64_t ld_dx,
+                                               void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                                               void* stream);
+
 /* te_mx_gemm — MXFP8 TN GEMM with fused epilogue (HipKittens MXFP8 GEMM
  * Support, PR description: MXFP8 GEMM with BIAS and GELU AUX epilogues; the
  * review thread's TN layout and its K % 128 rule for MXFP8 scaling):

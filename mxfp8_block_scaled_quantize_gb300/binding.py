@@ -19,6 +19,7 @@ TE_MX_OK = 0
 STATUS_NAMES = {0: "TE_MX_OK", 1: "TE_MX_ERR_INVALID_ARG", 2: "TE_MX_ERR_UNSUPPORTED_SHAPE",
                 3: "TE_MX_ERR_MISALIGNED", 4: "TE_MX_ERR_WORKSPACE_TOO_SMALL", 5: "TE_MX_ERR_CUDA",
                 6: "TE_MX_ERR_DEVICE_TIMEOUT", 7: "TE_MX_ERR_ARCH"}
+BF16, FP16, FP32 = 0, 1, 2                       # te_mx_dtype
 EPI_NONE, EPI_BIAS, EPI_GELU_AUX, EPI_BIAS_GELU_AUX, EPI_DGELU, EPI_ACCUMULATE_F32 = 0, 1, 2, 3, 4, 5
 
 # (name, restype, argtypes) for every function declared in include/temx.h
@@ -31,6 +32,10 @@ SIGNATURES = {
     "te_mx_block_quantize_fp32": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _P, _I64, _P]),
     "te_mx_layernorm_quantize": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _I64, _P,
                                                 _P, _I64, _P, _P, _P]),
+    "te_mx_layernorm": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, ctypes.c_float, _P, _I64, _P, _P, _P]),
+    "te_mx_layernorm_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "te_mx_layernorm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _P, _P, _P, _I64, _P,
+                                                _P, _P, _SZ, _P]),
     "te_mx_grouped_code_width": (_I64, [_I64, _I32]),
     "te_mx_grouped_scale_width": (_I64, [_I64, _I32]),
     "te_mx_quantize_colwise_grouped": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _I64, _P]),
@@ -101,6 +106,21 @@ def te_mx_layernorm_quantize(x, rows, hidden, ld_x, gamma, beta, eps, q_row, s_r
                              ld_s_col, mu, rsigma, stream) -> None:
     _check(lib().te_mx_layernorm_quantize(x, rows, hidden, ld_x, gamma, beta, eps, q_row, s_row, ld_s_row, q_col,
                                           s_col, ld_s_col, mu, rsigma, stream))
+
+
+def te_mx_layernorm(x, rows, hidden, ld_x, dtype, gamma, beta, param_dtype, eps, y, ld_y, mu, rsigma, stream) -> None:
+    _check(lib().te_mx_layernorm(x, rows, hidden, ld_x, dtype, gamma, beta, param_dtype, eps, y, ld_y, mu, rsigma,
+                                 stream))
+
+
+def te_mx_layernorm_backward_workspace_size(rows, hidden) -> int:
+    return lib().te_mx_layernorm_backward_workspace_size(rows, hidden)
+
+
+def te_mx_layernorm_backward(dy, ld_dy, x, ld_x, rows, hidden, dtype, gamma, param_dtype, mu, rsigma, dx, ld_dx,
+                             dgamma, dbeta, workspace, workspace_bytes, stream) -> None:
+    _check(lib().te_mx_layernorm_backward(dy, ld_dy, x, ld_x, rows, hidden, dtype, gamma, param_dtype, mu, rsigma, dx,
+                                          ld_dx, dgamma, dbeta, workspace, workspace_bytes, stream))
 
 
 def te_mx_grouped_code_width(total_m, num_groups) -> int:
@@ -292,6 +312,72 @@ def layernorm_quantize(x, gamma, beta, eps: float = 1e-5, rowwise: bool = True, 
                              _ptr(o.get("q_row")), _ptr(o.get("s_row")), o["s_row"].stride(0) if "s_row" in o else 0,
                              _ptr(o.get("q_col")), _ptr(o.get("s_col")), o["s_col"].stride(0) if "s_col" in o else 0,
                              _ptr(o.get("mu")), _ptr(o.get("rsigma")), _stream_ptr(stream))
+    return o
+
+
+def _dtype_code(t) -> int:
+    import torch
+    return {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}[t.dtype]
+
+
+def _pitch(t) -> int:
+    """Row pitch of a 2-D tensor (a single row has no next one, whatever its stride says)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream=None, out=None):
+    """LayerNorm over the last axis of a 2-D bf16, fp16 or fp32 CUDA tensor;
+    gamma and beta (None: no shift) have its type or fp32.  Returns a dict with
+    "y" (the type of x) and, with ``stats``, "mu" and "rsigma" (fp32 [rows])
+    for ``layernorm_backward``."""
+    import torch
+    assert x.dim() == 2 and x.is_cuda and x.stride(1) == 1
+    rows, hidden = x.shape
+    assert gamma.numel() == hidden and gamma.is_contiguous() and gamma.is_cuda
+    assert beta is None or (beta.dtype == gamma.dtype and beta.numel() == hidden and beta.is_contiguous())
+    o = dict(out or {})
+    if "y" not in o:
+        o["y"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+    if stats and "mu" not in o:
+        o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+        o["rsigma"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+    y = o["y"]
+    assert y.shape == x.shape and y.dtype == x.dtype and y.stride(1) == 1
+    te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), _ptr(beta),
+                    _dtype_code(gamma), eps, y.data_ptr(), _pitch(y), _ptr(o.get("mu")), _ptr(o.get("rsigma")),
+                    _stream_ptr(stream))
+    return o
+
+
+def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=None, out=None, workspace=None):
+    """Gradients of ``layernorm`` (or of the normalisation in
+    ``layernorm_quantize``): dy and x [rows, hidden] of one type, mu and rsigma
+    from the forward pass.  Returns a dict with "dx" and, with ``dparams``,
+    "dgamma" and "dbeta" (the type of gamma); their scratch is ``workspace``
+    (uint8 CUDA tensor) or allocated here."""
+    import torch
+    assert x.dim() == 2 and x.is_cuda and x.stride(1) == 1
+    assert dy.shape == x.shape and dy.dtype == x.dtype and dy.stride(1) == 1
+    rows, hidden = x.shape
+    assert gamma.numel() == hidden and gamma.is_contiguous()
+    assert mu.dtype == rsigma.dtype == torch.float32 and mu.numel() == rsigma.numel() == rows
+    o = dict(out or {})
+    if "dx" not in o:
+        o["dx"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+    need = 0
+    if dparams:
+        if "dgamma" not in o:
+            o["dgamma"] = torch.empty(hidden, dtype=gamma.dtype, device=x.device)
+            o["dbeta"] = torch.empty(hidden, dtype=gamma.dtype, device=x.device)
+        need = te_mx_layernorm_backward_workspace_size(rows, hidden)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    dx = o["dx"]
+    assert dx.shape == x.shape and dx.dtype == x.dtype and dx.stride(1) == 1
+    te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, _dtype_code(x),
+                             gamma.data_ptr(), _dtype_code(gamma), mu.data_ptr(), rsigma.data_ptr(), dx.data_ptr(),
+                             _pitch(dx), _ptr(o.get("dgamma")), _ptr(o.get("dbeta")), _ptr(workspace),
+                             workspace.numel() if workspace is not None else 0, _stream_ptr(stream))
     return o
 
 

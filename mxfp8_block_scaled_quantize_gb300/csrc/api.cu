@@ -307,6 +307,82 @@ te_mx_status te_mx_layernorm_quantize(const void* x, int64_t rows, int64_t hidde
     return ln_quantize_launch(a, static_cast<cudaStream_t>(stream));
 }
 
+// Checks shared by the LayerNorm entry points: sizes and types; a matrix's
+// pitch and its alignment to its elements.
+static te_mx_status validate_layernorm(int64_t rows, int64_t hidden, int32_t dtype, int32_t param_dtype) {
+    if (rows < 0 || hidden < 0) return set_error(TE_MX_ERR_INVALID_ARG, "negative size %lld x %lld", (long long)rows, (long long)hidden);
+    if (dtype < TE_MX_BF16 || dtype > TE_MX_FP32) return set_error(TE_MX_ERR_INVALID_ARG, "unknown dtype %d", int(dtype));
+    if (param_dtype != dtype && param_dtype != TE_MX_FP32)
+        return set_error(TE_MX_ERR_INVALID_ARG, "param_dtype=%d must be the activations' type or TE_MX_FP32", int(param_dtype));
+    if (rows > (int64_t(1) << 31) - 64 || hidden > (int64_t(1) << 24))
+        return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "rows=%lld exceeds 2^31 - 64 or hidden=%lld exceeds 2^24", (long long)rows,
+                         (long long)hidden);
+    return TE_MX_OK;
+}
+
+static te_mx_status validate_ln_matrix(const void* p, int64_t ld, int64_t hidden, int32_t dtype, const char* name) {
+    if (!p) return set_error(TE_MX_ERR_INVALID_ARG, "%s is NULL", name);
+    if (ld < hidden) return set_error(TE_MX_ERR_MISALIGNED, "ld_%s=%lld is less than hidden=%lld", name, (long long)ld, (long long)hidden);
+    if (!aligned(p, dtype == TE_MX_FP32 ? 4 : 2)) return set_error(TE_MX_ERR_MISALIGNED, "%s is not aligned to its elements", name);
+    return TE_MX_OK;
+}
+
+te_mx_status te_mx_layernorm(const void* x, int64_t rows, int64_t hidden, int64_t ld_x, int32_t dtype,
+                             const void* gamma, const void* beta, int32_t param_dtype, float eps,
+                             void* y, int64_t ld_y, float* mu, float* rsigma, void* stream) {
+    t_last_error[0] = '\0';
+    te_mx_status st = validate_layernorm(rows, hidden, dtype, param_dtype);
+    if (st != TE_MX_OK) return st;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return set_error(TE_MX_ERR_INVALID_ARG, "eps must be positive and finite");
+    if ((mu == nullptr) != (rsigma == nullptr))
+        return set_error(TE_MX_ERR_INVALID_ARG, "mu and rsigma must both be given or both be NULL");
+    if (rows == 0 || hidden == 0) return TE_MX_OK;
+    const uintptr_t pa = param_dtype == TE_MX_FP32 ? 4 : 2;
+    if (!gamma) return set_error(TE_MX_ERR_INVALID_ARG, "gamma is NULL");
+    if (!aligned(gamma, pa) || !aligned(beta, pa) || !aligned(mu, 4) || !aligned(rsigma, 4))
+        return set_error(TE_MX_ERR_MISALIGNED, "gamma, beta, mu or rsigma is not aligned to its elements");
+    if ((st = validate_ln_matrix(x, ld_x, hidden, dtype, "x")) != TE_MX_OK) return st;
+    if ((st = validate_ln_matrix(y, ld_y, hidden, dtype, "y")) != TE_MX_OK) return st;
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    LnArgs a{x, rows, hidden, ld_x, dtype, param_dtype, gamma, beta, eps, y, ld_y, mu, rsigma};
+    return ln_forward_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t te_mx_layernorm_backward_workspace_size(int64_t rows, int64_t hidden) {
+    if (rows <= 0 || hidden <= 0) return 0;
+    return size_t(ln_backward_parts(rows)) * 2 * size_t(hidden) * sizeof(float);
+}
+
+te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t rows,
+                                      int64_t hidden, int32_t dtype, const void* gamma, int32_t param_dtype,
+                                      const float* mu, const float* rsigma, void* dx, int64_t ld_dx,
+                                      void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+    t_last_error[0] = '\0';
+    te_mx_status st = validate_layernorm(rows, hidden, dtype, param_dtype);
+    if (st != TE_MX_OK) return st;
+    if (dbeta && !dgamma) return set_error(TE_MX_ERR_INVALID_ARG, "dbeta is given without dgamma");
+    if (!dx && !dgamma) return set_error(TE_MX_ERR_INVALID_ARG, "dx and dgamma are both NULL");
+    if (hidden == 0 || (rows == 0 && !dgamma)) return TE_MX_OK;
+    const uintptr_t pa = param_dtype == TE_MX_FP32 ? 4 : 2;
+    if (!aligned(gamma, pa) || !aligned(dgamma, pa) || !aligned(dbeta, pa) || !aligned(mu, 4) || !aligned(rsigma, 4))
+        return set_error(TE_MX_ERR_MISALIGNED, "gamma, dgamma, dbeta, mu or rsigma is not aligned to its elements");
+    if (rows > 0) {
+        if (!mu || !rsigma || !gamma) return set_error(TE_MX_ERR_INVALID_ARG, "gamma, mu and rsigma are required");
+        if ((st = validate_ln_matrix(dy, ld_dy, hidden, dtype, "dy")) != TE_MX_OK) return st;
+        if ((st = validate_ln_matrix(x, ld_x, hidden, dtype, "x")) != TE_MX_OK) return st;
+        if (dx && (st = validate_ln_matrix(dx, ld_dx, hidden, dtype, "dx")) != TE_MX_OK) return st;
+        const size_t need = dgamma ? te_mx_layernorm_backward_workspace_size(rows, hidden) : 0;
+        if (need && (!workspace || workspace_bytes < need))
+            return set_error(TE_MX_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+        if (need && !aligned(workspace, 16)) return set_error(TE_MX_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+    }
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    LnBackwardArgs a{dy, ld_dy, x, rows, hidden, ld_x, dtype, param_dtype, gamma, mu, rsigma, dx, ld_dx, dgamma, dbeta,
+                     static_cast<float*>(workspace)};
+    return ln_backward_launch(a, static_cast<cudaStream_t>(stream));
+}
+
 int64_t te_mx_grouped_code_width(int64_t total_m, int32_t num_groups) {
     if (total_m < 0 || num_groups < 0) return 0;
     return grouped_code_width(total_m, num_groups);

@@ -67,6 +67,39 @@ struct LnQuantizeArgs {
 };
 te_mx_status ln_quantize_launch(const LnQuantizeArgs& a, cudaStream_t stream);
 
+struct LnArgs {
+    const void* x;           // [rows x hidden] of `dtype`, pitch ld_x
+    int64_t rows, hidden, ld_x;
+    int32_t dtype, param_dtype;      // te_mx_dtype
+    const void* gamma;       // [hidden]
+    const void* beta;        // [hidden] or null
+    float eps;
+    void* y;                 // [rows x hidden], pitch ld_y
+    int64_t ld_y;
+    float* mu;               // fp32 [rows], both or neither
+    float* rsigma;
+};
+te_mx_status ln_forward_launch(const LnArgs& a, cudaStream_t stream);
+
+struct LnBackwardArgs {
+    const void* dy;          // [rows x hidden] of `dtype`, pitch ld_dy
+    int64_t ld_dy;
+    const void* x;
+    int64_t rows, hidden, ld_x;
+    int32_t dtype, param_dtype;
+    const void* gamma;
+    const float* mu;
+    const float* rsigma;
+    void* dx;                // [rows x hidden], pitch ld_dx, or null
+    int64_t ld_dx;
+    void* dgamma;            // [hidden] of `param_dtype`, or null (then dbeta is null too)
+    void* dbeta;             // [hidden] or null
+    float* partial;          // fp32 [parts][2][hidden] (with dgamma)
+};
+constexpr int kLnMaxParts = 304;                 // partial sums per column, at most (two per SM)
+int ln_backward_parts(int64_t rows);
+te_mx_status ln_backward_launch(const LnBackwardArgs& a, cudaStream_t stream);
+
 struct GroupedColwiseArgs {
     const void* x;           // bf16 [total_m x cols], pitch ld_x (token-major)
     int64_t total_m, cols, ld_x;
