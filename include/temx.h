@@ -313,6 +313,42 @@ TEMX_API te_mx_status te_mx_gemm(const uint8_t* A, const uint8_t* sA, int64_t ld
                         void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* Activations of the gated feed-forward: silu(x) = x / (1 + e^-x) (SwiGLU),
+ * the tanh form of GELU (GeGLU), max(x, 0) (ReGLU). */
+typedef enum te_mx_activation { TE_MX_ACT_SILU = 0, TE_MX_ACT_GELU = 1, TE_MX_ACT_RELU = 2 } te_mx_activation;
+
+/* te_mx_gated_gemm — both projections of a gated feed-forward, its activation
+ * and its product in one launch (the first half of a LayerNormMLP, leeroopedia
+ * "FP8 Training Quickstart", with a gated activation).  W holds the gate
+ * weight's F rows, then the up weight's F rows:
+ *   pre[m][n] = sum_k deq(A)[m][k] deq(W)[n][k] (+ bias[n]),  0 <= n < 2F, fp32,
+ *   D[m][n] = bf16(act(pre[m][n]) pre[m][F + n]),             0 <= n < F,
+ *   aux = bf16(pre) if given (te_mx_gated_backward reads it).
+ *   A  uint8 E4M3 [M x K], sA uint8 [M x ld_sA];
+ *   W  uint8 E4M3 [2F x K], sW uint8 [2F x ld_sW]  (te_mx_quantize's row-wise copies);
+ *   bias  bf16 [2F] or NULL;  activation: a te_mx_activation;
+ *   D  bf16 [M x F];  aux  bf16 [M x 2F] or NULL.
+ * Any M, one token included; K % 128 == 0, F % 16 == 0; alignment and errors
+ * as te_mx_gemm (M == 0 is a no-op).  pre is as accurate as te_mx_gemm's
+ * accumulator: within 1e-5 sum_k |a_k w_k| before it is rounded.
+ * Deterministic: equal inputs give equal bits. */
+TEMX_API te_mx_status te_mx_gated_gemm(const uint8_t* A, const uint8_t* sA, int64_t ld_sA,
+                                       const uint8_t* W, const uint8_t* sW, int64_t ld_sW,
+                                       int64_t M, int64_t F, int64_t K, const void* bias, int32_t activation,
+                                       void* D, void* aux, void* stream);
+
+/* te_mx_grouped_gated_gemm — te_mx_gated_gemm for the experts of a mixture in
+ * one launch.  group_m, total_m and the row ranges as te_mx_grouped_gemm;
+ *   W  uint8 [G x 2F x K], sW uint8 [G*2F x ld_sW] (per group: gate rows, then
+ *   up rows);  bias bf16 [G x 2F] or NULL;  D bf16 [total_m x F];
+ *   aux bf16 [total_m x 2F] or NULL.
+ * Rows past sum m_g are not written; device-side errors as te_mx_grouped_gemm. */
+TEMX_API te_mx_status te_mx_grouped_gated_gemm(int32_t num_groups, const int32_t* group_m, int64_t total_m,
+                                               const uint8_t* X, const uint8_t* sX, int64_t ld_sX,
+                                               const uint8_t* W, const uint8_t* sW, int64_t ld_sW,
+                                               int64_t F, int64_t K, const void* bias, int32_t activation,
+                                               void* D, void* aux, void* stream);
+
 /* te_mx_gemm_fp32_scales — the Float8BlockScaling TN GEMM computed with the
  * FP32 scales directly (ROCm/TransformerEngine README, "Blockwise FP8 GEMM
  * support on ROCm", second mode), on te_mx_block_quantize_fp32 output:

@@ -20,6 +20,8 @@ STATUS_NAMES = {0: "TE_MX_OK", 1: "TE_MX_ERR_INVALID_ARG", 2: "TE_MX_ERR_UNSUPPO
                 3: "TE_MX_ERR_MISALIGNED", 4: "TE_MX_ERR_WORKSPACE_TOO_SMALL", 5: "TE_MX_ERR_CUDA",
                 6: "TE_MX_ERR_DEVICE_TIMEOUT", 7: "TE_MX_ERR_ARCH"}
 BF16, FP16, FP32 = 0, 1, 2                       # te_mx_dtype
+ACT_SILU, ACT_GELU, ACT_RELU = 0, 1, 2           # te_mx_activation
+ACTIVATIONS = {"silu": ACT_SILU, "gelu": ACT_GELU, "relu": ACT_RELU}
 EPI_NONE, EPI_BIAS, EPI_GELU_AUX, EPI_BIAS_GELU_AUX, EPI_DGELU, EPI_ACCUMULATE_F32 = 0, 1, 2, 3, 4, 5
 
 # (name, restype, argtypes) for every function declared in include/temx.h
@@ -45,6 +47,9 @@ SIGNATURES = {
     "te_mx_quantize_dbias": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P, _SZ, _P]),
     "te_mx_quantize_dbias_noalloc": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P]),
     "te_mx_gemm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "te_mx_gated_gemm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _I32, _P, _P, _P]),
+    "te_mx_grouped_gated_gemm": (ctypes.c_int, [_I32, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _P,
+                                                _P]),
     "te_mx_gemm_fp32_scales": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I32, _I64, _I64, _I64, _P, _I32, _P, _P,
                                               _P]),
     "te_mx_grouped_gemm": (ctypes.c_int, [_I32, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32,
@@ -170,6 +175,16 @@ def te_mx_grouped_gemm(num_groups, group_m, total_m, X, sX, ld_sX, W, sW, ld_sW,
                        workspace, workspace_bytes, stream) -> None:
     _check(lib().te_mx_grouped_gemm(num_groups, group_m, total_m, X, sX, ld_sX, W, sW, ld_sW, N, K, bias,
                                     epilogue, D, aux, workspace, workspace_bytes, stream))
+
+
+def te_mx_gated_gemm(A, sA, ld_sA, W, sW, ld_sW, M, F, K, bias, activation, D, aux, stream) -> None:
+    _check(lib().te_mx_gated_gemm(A, sA, ld_sA, W, sW, ld_sW, M, F, K, bias, activation, D, aux, stream))
+
+
+def te_mx_grouped_gated_gemm(num_groups, group_m, total_m, X, sX, ld_sX, W, sW, ld_sW, F, K, bias, activation, D, aux,
+                             stream) -> None:
+    _check(lib().te_mx_grouped_gated_gemm(num_groups, group_m, total_m, X, sX, ld_sX, W, sW, ld_sW, F, K, bias,
+                                          activation, D, aux, stream))
 
 
 def te_mx_gemm_workspace_size(M, N, K, num_groups=0) -> int:
@@ -508,3 +523,45 @@ def grouped_gemm(group_m, qx, sx, qw, sw, bias=None, gelu: bool = False, stream=
                        qw.data_ptr(), sw2.data_ptr(), sw2.stride(0), N, K, _ptr(bias), epi,
                        d.data_ptr(), _ptr(aux), 0, 0, _stream_ptr(stream))
     return d, aux
+
+
+def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = False, stream=None, out=None):
+    """Gated feed-forward of MXFP8 operands: qx [M, K] and qw [2F, K] (the gate
+    weight's rows, then the up weight's; ``quantize``'s row-wise copies), bias
+    bf16 [2F] or None, activation "silu", "gelu" (tanh form) or "relu".
+    Returns (h, pre): h = act(gate) * up in bf16 [M, F], and with ``aux`` the
+    pre-activations [gate | up] in bf16 [M, 2F] for ``gated_backward``, else None."""
+    import torch
+    M, K = qx.shape
+    F = qw.shape[0] // 2
+    assert qw.shape == (2 * F, K) and (bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == 2 * F))
+    if out is None:
+        h = torch.empty(M, F, dtype=torch.bfloat16, device=qx.device)
+        pre = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=qx.device) if aux else None
+    else:
+        h, pre = out
+    te_mx_gated_gemm(qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(), sw.data_ptr(), _pitch(sw), M, F, K,
+                     _ptr(bias), ACTIVATIONS[activation], h.data_ptr(), _ptr(pre), _stream_ptr(stream))
+    return h, pre
+
+
+def grouped_gated_gemm(group_m, qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = False, stream=None,
+                       out=None):
+    """``gated_gemm`` over the experts of a mixture: group_m int32 [G] on the
+    device, qx [total_m, K] (the experts' rows in order), qw [G, 2F, K], sw
+    [G*2F, pitch], bias bf16 [G, 2F] or None.  Returns (h [total_m, F], pre
+    [total_m, 2F] or None)."""
+    import torch
+    total_m, K = qx.shape
+    G, N, _ = qw.shape
+    assert group_m.dtype == torch.int32 and group_m.numel() == G and N % 2 == 0 and qw.shape[2] == K
+    if out is None:
+        h = torch.empty(total_m, N // 2, dtype=torch.bfloat16, device=qx.device)
+        pre = torch.empty(total_m, N, dtype=torch.bfloat16, device=qx.device) if aux else None
+    else:
+        h, pre = out
+    sw2 = sw.reshape(G * N, -1)
+    te_mx_grouped_gated_gemm(G, group_m.data_ptr(), total_m, qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(),
+                             sw2.data_ptr(), _pitch(sw2), N // 2, K, _ptr(bias), ACTIVATIONS[activation], h.data_ptr(),
+                             _ptr(pre), _stream_ptr(stream))
+    return h, pre

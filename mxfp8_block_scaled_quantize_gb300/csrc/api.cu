@@ -524,6 +524,63 @@ te_mx_status te_mx_gemm(const uint8_t* A, const uint8_t* sA, int64_t ld_sA,
     return gemm_launch(a, static_cast<cudaStream_t>(stream));
 }
 
+// Checks shared by the two gated entry points.
+static te_mx_status validate_gated(const uint8_t* A, const uint8_t* sA, int64_t ld_sA, const uint8_t* W, const uint8_t* sW,
+                                   int64_t ld_sW, int64_t F, int64_t K, const void* bias, int32_t activation, void* D,
+                                   void* aux) {
+    if (activation < TE_MX_ACT_SILU || activation > TE_MX_ACT_RELU)
+        return set_error(TE_MX_ERR_INVALID_ARG, "unknown activation %d", int(activation));
+    if (F > (int64_t(1) << 29)) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "F too large");
+    te_mx_status st = validate_gemm_common(A, sA, ld_sA, W, sW, ld_sW, F, K, bias,
+                                           bias ? TE_MX_EPI_BIAS : TE_MX_EPI_NONE, D, nullptr);
+    if (st != TE_MX_OK) return st;
+    if (!aligned(aux, 16)) return set_error(TE_MX_ERR_MISALIGNED, "aux is not 16-byte aligned");
+    return TE_MX_OK;
+}
+
+te_mx_status te_mx_gated_gemm(const uint8_t* A, const uint8_t* sA, int64_t ld_sA, const uint8_t* W, const uint8_t* sW,
+                              int64_t ld_sW, int64_t M, int64_t F, int64_t K, const void* bias, int32_t activation,
+                              void* D, void* aux, void* stream) {
+    t_last_error[0] = '\0';
+    if (M < 0) return set_error(TE_MX_ERR_INVALID_ARG, "negative M");
+    if (M == 0) return TE_MX_OK;
+    if (M > (int64_t(1) << 31) - 256) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "M too large");
+    te_mx_status st = validate_gated(A, sA, ld_sA, W, sW, ld_sW, F, K, bias, activation, D, aux);
+    if (st != TE_MX_OK) return st;
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    GemmArgs a{};
+    a.A = A; a.sA = sA; a.ld_sA = ld_sA; a.B = W; a.sB = sW; a.ld_sB = ld_sW;
+    a.M = M; a.N = F; a.K = K; a.bias = bias; a.has_bias = bias != nullptr;
+    a.D = D; a.aux = aux;
+    a.gated = true;
+    a.act = activation;
+    return gemm_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+te_mx_status te_mx_grouped_gated_gemm(int32_t num_groups, const int32_t* group_m, int64_t total_m, const uint8_t* X,
+                                      const uint8_t* sX, int64_t ld_sX, const uint8_t* W, const uint8_t* sW,
+                                      int64_t ld_sW, int64_t F, int64_t K, const void* bias, int32_t activation,
+                                      void* D, void* aux, void* stream) {
+    t_last_error[0] = '\0';
+    if (num_groups < 1 || num_groups > 1024) return set_error(TE_MX_ERR_INVALID_ARG, "num_groups=%d must be in [1, 1024]", num_groups);
+    if (!group_m) return set_error(TE_MX_ERR_INVALID_ARG, "group_m is NULL");
+    if (!aligned(group_m, 4)) return set_error(TE_MX_ERR_MISALIGNED, "group_m is not 4-byte aligned");
+    if (total_m < 0) return set_error(TE_MX_ERR_INVALID_ARG, "negative total_m");
+    if (total_m == 0) return TE_MX_OK;
+    if (total_m > (int64_t(1) << 31) - 256) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "total_m too large");
+    te_mx_status st = validate_gated(X, sX, ld_sX, W, sW, ld_sW, F, K, bias, activation, D, aux);
+    if (st != TE_MX_OK) return st;
+    if (int64_t(num_groups) * 2 * F > (int64_t(1) << 31) - 256) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "2 G F too large");
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    GemmArgs a{};
+    a.A = X; a.sA = sX; a.ld_sA = ld_sX; a.B = W; a.sB = sW; a.ld_sB = ld_sW;
+    a.M = total_m; a.N = F; a.K = K; a.bias = bias; a.has_bias = bias != nullptr;
+    a.D = D; a.aux = aux; a.groups = num_groups; a.group_m = group_m;
+    a.gated = true;
+    a.act = activation;
+    return gemm_launch(a, static_cast<cudaStream_t>(stream));
+}
+
 te_mx_status te_mx_gemm_fp32_scales(const uint8_t* A, const float* sA, int64_t ld_sA,
                                     const uint8_t* B, const float* sB, int64_t ld_sB, int32_t b_blocks_2d,
                                     int64_t M, int64_t N, int64_t K, const void* bias, int32_t epilogue,

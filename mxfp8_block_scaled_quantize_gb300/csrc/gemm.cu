@@ -43,6 +43,13 @@
 // (raised to 216): every K-step's product lands in one of two 256-column TMEM
 // buffers and each epilogue thread adds it, scaled, to the 128 accumulator
 // columns of its row that it keeps in registers.
+// The gated GEMM (te_mx_gated_gemm) uses the same tiles for two projections at
+// once: B's 256 tile rows are 128 rows of the gate weight and the 128 rows of
+// the up weight that belong to the same output columns (for a pair: the even
+// CTA loads the gate rows, the odd CTA the up rows), so the accumulator holds
+// gate in columns 0..127 and up in columns 128..255, an epilogue thread has
+// both projections of 64 output columns of its row in registers, and act(gate)
+// * up needs no exchange and no interleaved copy of the weights.
 // Every mbarrier wait is bounded; a wait that gives up aborts the CTA cleanly
 // and sets the device status word.
 #include <cuda_runtime.h>
@@ -132,9 +139,9 @@ static_assert(4 * kRegsRoles + 8 * kRegsEpi <= 12 * 168, "FP32-scale register sp
 
 struct GemmParams {
     int64_t M;               // dense: rows of A/D; grouped: total_m (rows of X/D)
-    int32_t N, K;
+    int32_t N, K;            // (gated: N = output columns, half of W's rows)
     int32_t k_iters;         // K / 128
-    int32_t n_tiles;         // ceil(N / 256)
+    int32_t n_tiles;         // ceil(N / 256) (gated: ceil(N / 128))
     int32_t m_tiles;         // dense: ceil(M / tile rows)
     int64_t total_tiles;     // dense only
     int32_t groups;          // 0: dense
@@ -149,6 +156,7 @@ struct GemmParams {
     int64_t total_m;                     // wgrad: bound on the token counts' sum
     int64_t ld_code, ld_sfa, ld_sfb;     // wgrad: operand pitches (capacities)
     unsigned int* status;
+    int32_t act;                         // gated: te_mx_activation
 };
 
 __device__ __forceinline__ int64_t imin64(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -193,7 +201,7 @@ struct __align__(16) SharedState {
 // column-bands in L2.  Grouped: group-major, then n-major over the group's
 // m-tiles.  Wgrad: group-major, every group the full M x N output over its
 // own K range.  `hint` carries the group found last time (tiles increase).
-template <int kTileM, int kTileN, bool kWgrad, typename SH>
+template <int kTileM, int kTileN, bool kWgrad, bool kGated, typename SH>
 __device__ __forceinline__ Tile map_tile(const GemmParams& p, const SH& sh, int64_t t, int32_t& hint) {
     Tile tl;
     tl.k0 = 0;
@@ -239,7 +247,7 @@ __device__ __forceinline__ Tile map_tile(const GemmParams& p, const SH& sh, int6
         tl.d_row = tl.a_row;
         tl.row_end = min(sh.row_start[g + 1], tl.a_row + kTileM);
         tl.n0 = nt * kTileN;
-        tl.b_row = g * p.N + tl.n0;
+        tl.b_row = (kGated ? 2 * g : g) * p.N + tl.n0;      // (gated: the first gate row; its up rows are N further)
         tl.group = g;
     }
     return tl;
@@ -625,6 +633,148 @@ __device__ __forceinline__ void store_64_staged(uint32_t* acc, const GemmParams&
     }
 }
 
+// ---------------------------------------------------------------- gated epilogue
+
+// act(x) of two gate values.  SiLU is x / (1 + 2^t) with t = -log2(e) x; GELU
+// the same quotient with its own t (gelu_tanh_f2); ReLU keeps NaN.
+__device__ __forceinline__ void gate_act_f2(float& x0, float& x1, int32_t act) {
+    if (act == TE_MX_ACT_GELU) {
+        gelu_tanh_f2(x0, x1);
+    } else if (act == TE_MX_ACT_SILU) {
+        constexpr float kNegLog2e = -1.4426950408889634f;
+        const uint64_t x = f2_pack(x0, x1);
+        float t0, t1, e0, e1, d0, d1, r0, r1;
+        f2_unpack(f2_mul(x, f2_pack(kNegLog2e, kNegLog2e)), t0, t1);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+        f2_unpack(f2_add(f2_pack(e0, e1), f2_pack(1.0f, 1.0f)), d0, d1);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
+        f2_unpack(f2_mul(x, f2_pack(r0, r1)), x0, x1);
+    } else {
+        asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x0));
+        asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x1));
+    }
+}
+
+// 16 output columns of one row: gate and up accumulators -> bias, [gate | up]
+// kept for the backward pass (aux, if given), D = act(gate) * up.
+__device__ __forceinline__ void store_gated_chunk(const uint32_t* gate, const uint32_t* up, const GemmParams& p,
+                                                  int32_t group, int64_t row, int32_t n) {
+    float v[2][16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[0][i] = __uint_as_float(gate[i]);
+        v[1][i] = __uint_as_float(up[i]);
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if (p.has_bias) {
+            const uint16_t* bias = p.bias + (2 * int64_t(group) + half) * p.N + n;
+            const uint4 b0 = __ldg(reinterpret_cast<const uint4*>(bias)), b1 = __ldg(reinterpret_cast<const uint4*>(bias + 8));
+            const uint32_t bw[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[half][2 * i] += __uint_as_float(bw[i] << 16);
+                v[half][2 * i + 1] += __uint_as_float(bw[i] & 0xFFFF0000u);
+            }
+        }
+        if (p.aux) {
+            uint16_t* aux = p.aux + (2 * row + half) * p.N + n;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(v[half][2 * i], v[half][2 * i + 1]);
+            st_global_v4(aux, o[0], o[1], o[2], o[3]);
+            st_global_v4(aux + 8, o[4], o[5], o[6], o[7]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        gate_act_f2(v[0][i], v[0][i + 1], p.act);
+        o[i / 2] = pack_bf16x2(v[0][i] * v[1][i], v[0][i + 1] * v[1][i + 1]);
+    }
+    uint16_t* d = p.D + row * p.N + n;
+    st_global_v4(d, o[0], o[1], o[2], o[3]);
+    st_global_v4(d + 8, o[4], o[5], o[6], o[7]);
+}
+
+// 64 output columns of one row per lane (32 rows per warp), through the warp's
+// staging tile as store_64_staged: gate and up (if kept), then D.  bias_sm: the
+// gate's 64 bf16 biases, then the up projection's.  map_aux is three-
+// dimensional, [rows][gate, up][N], so that a box past column N is clipped and
+// does not run from the gate half into the up half.
+__device__ __forceinline__ void store_gated_staged(uint32_t* gate, uint32_t* up, const GemmParams& p, uint32_t bias_sm,
+                                                   int64_t row0, int64_t row_end, int32_t n, uint32_t stage, int lane,
+                                                   const CUtensorMap* map_d, const CUtensorMap* map_aux, bool tma) {
+    float* v[2] = {reinterpret_cast<float*>(gate), reinterpret_cast<float*>(up)};
+    if (p.has_bias) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint4 b = lds128(bias_sm + 128 * half + 16 * c);
+                const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float& x0 = v[half][8 * c + 2 * i];
+                    float& x1 = v[half][8 * c + 2 * i + 1];
+                    f2_unpack(f2_add(f2_pack(x0, x1), f2_pack(__uint_as_float(bw[i] << 16),
+                                                              __uint_as_float(bw[i] & 0xFFFF0000u))), x0, x1);
+                }
+            }
+    }
+    // one 32 x 64 bf16 tile of `x` through the staging tile
+    auto store = [&](const float* x, int half) {             // half: 0 gate, 1 up, 2 the output
+        // the staging tile is free once this warp's previous TMA store has read it
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            sts128(stage + lane * 128 + ((c ^ (lane & 7)) << 4), pack_bf16x2(x[8 * c], x[8 * c + 1]),
+                   pack_bf16x2(x[8 * c + 2], x[8 * c + 3]), pack_bf16x2(x[8 * c + 4], x[8 * c + 5]),
+                   pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
+        if (tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                // (the L2 policies of store_64_staged: evict-first for dense GEMMs)
+                if (half < 2) {
+                    if (p.groups > 0) tma_store_3d(map_aux, stage, n, half, int32_t(row0));
+                    else tma_store_3d_evict_first(map_aux, stage, n, half, int32_t(row0));
+                } else {
+                    if (p.groups > 0) tma_store_2d(map_d, stage, n, int32_t(row0));
+                    else tma_store_2d_evict_first(map_d, stage, n, int32_t(row0));
+                }
+                bulk_commit();
+            }
+            __syncwarp();
+            return;
+        }
+        __syncwarp();
+        uint16_t* out = half < 2 ? p.aux + half * int64_t(p.N) : p.D;
+        const int64_t ld = half < 2 ? 2 * int64_t(p.N) : int64_t(p.N);
+        const int c = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            const uint4 w = lds128(stage + r * 128 + ((c ^ (r & 7)) << 4));
+            if (row0 + r < row_end && n + 8 * c < p.N)
+                st_global_v4(out + (row0 + r) * ld + n + 8 * c, w.x, w.y, w.z, w.w);
+        }
+        __syncwarp();
+    };
+    if (p.aux) {
+        store(v[0], 0);
+        store(v[1], 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+        gate_act_f2(v[0][i], v[0][i + 1], p.act);
+        f2_unpack(f2_mul(f2_pack(v[0][i], v[0][i + 1]), f2_pack(v[1][i], v[1][i + 1])), v[0][i], v[0][i + 1]);
+    }
+    store(v[0], 2);
+}
+
 // FP32 scales: acc[j] += v[j] * (sA sB) for 64 columns of one row.  2D weight
 // blocks: one factor f = sA sB for all of them, acc = fma(v, f, acc);
 // otherwise sB per column from the [4 K-steps][256 columns] shared table at
@@ -666,8 +816,8 @@ __device__ __forceinline__ void scale_accumulate_64(uint32_t (&acc)[64], const u
 // kAcc: fp32 D accumulated into; kWgrad: grouped wgrad; kF32: Float8BlockScaling
 // operands with FP32 scales (dense only): every K-step's product lands in one
 // of kScrBufs TMEM buffers and the epilogue warps accumulate it, scaled, in
-// registers.
-template <int kPair, bool kAcc, bool kWgrad, bool kF32>
+// registers.  kGated: B = [gate; up] rows, D = act(gate) * up (dense or grouped).
+template <int kPair, bool kAcc, bool kWgrad, bool kF32, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)   // 168 registers: 3 warps share a 16K-register sub-partition
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
@@ -675,6 +825,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const GemmParams p) {
     using C = Cfg<kPair, kF32>;
     using SH = SharedState<C::kStages>;
+    constexpr int kTileN = kGated ? C::kBN / 2 : C::kBN;    // output columns per tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ SH sh;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -688,8 +839,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     };
     // MXFP8: two MMA issuers for dense GEMMs of at least kSplitMinK K-steps;
     // otherwise (short K, or the grouped wgrad's per-expert K ranges) warp 1
-    // alone issues and commits, and the barriers count its arrivals only
-    const bool two_issuers = !kWgrad && p.k_iters >= kSplitMinK;
+    // alone issues and commits, and the barriers count its arrivals only.  The
+    // gated GEMM keeps one issuer: two reorder the fp32 additions from run to
+    // run, and it would gain 1.6 % (8192 x 36864 x 7168: 1506 against 1530 us).
+    const bool two_issuers = !kWgrad && !kGated && p.k_iters >= kSplitMinK;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -892,9 +1045,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 uint32_t stage = 0, phase = 0;
                 bool ok = true;
                 for (int64_t t = unit; t < total && ok; t += units) {
-                    const Tile tl = map_tile<C::kTileM, C::kBN, kWgrad>(p, sh, t, hint);
+                    const Tile tl = map_tile<C::kTileM, kTileN, kWgrad, kGated>(p, sh, t, hint);
                     const int32_t a_row = tl.a_row + int32_t(rank) * kBM;
-                    const int32_t b_row = tl.b_row + int32_t(rank) * C::kBRows;
+                    const int32_t b_row = tl.b_row + int32_t(rank) * (kGated ? p.N : C::kBRows);
                     for (int32_t k = 0; k < tl.nk; ++k) {
                         const int32_t kx = (tl.k0 + k) * kBK;
                         if (!wait_or_abort(smem_u32(&sh.empty[stage]), phase ^ 1u, sh, p.status)) { ok = false; break; }
@@ -909,6 +1062,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             mbar_arrive_expect_tx(full, C::kABytes + C::kBBytes);
                             tma_load_2d(smem_u32(st), &map_a, full, kx, a_row);
                             tma_load_2d(smem_u32(st + C::kABytes), &map_b, full, kx, b_row);
+                            if constexpr (kGated)        // (the gated map's box is 128 rows)
+                                tma_load_2d(smem_u32(st + C::kABytes + C::kBBytes / 2), &map_b, full, kx, b_row + p.N);
                         }
                         if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                     }
@@ -931,7 +1086,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 for (int64_t t = unit; t < total && ok; t += units, ++local) {
                     // K-steps of this tile (wgrad: the expert's own; 0 for an expert without tokens)
                     int32_t nk = p.k_iters;
-                    if constexpr (kWgrad) nk = map_tile<C::kTileM, C::kBN, kWgrad>(p, sh, t, hint).nk;
+                    if constexpr (kWgrad) nk = map_tile<C::kTileM, kTileN, kWgrad, kGated>(p, sh, t, hint).nk;
                     if (local > 0) {
                         if (!__all_sync(0xFFFFFFFFu, wait_or_abort(smem_u32(&sh.tmem_empty), uint32_t(local - 1) & 1u, sh,
                                                                    p.status)))
@@ -1006,7 +1161,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             Tile ltl{};
             auto seek = [&]() {               // the first tile from lt on that has scale groups
                 for (; lt < total; lt += units) {
-                    ltl = map_tile<C::kTileM, C::kBN, kWgrad>(p, sh, lt, lhint);
+                    ltl = map_tile<C::kTileM, kTileN, kWgrad, kGated>(p, sh, lt, lhint);
                     if (tile_groups(ltl) > 0) break;
                 }
             };
@@ -1026,6 +1181,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 mbar_arrive_expect_tx(bar, kSFABytes + C::kSFBBytes);
                 tma_load_2d(dst, &map_sfa, bar, ltl.sf0 + lg * 16, ltl.a_row + int32_t(rank) * kBM);
                 tma_load_2d(dst + kSFABytes, &map_sfb, bar, ltl.sf0 + lg * 16, ltl.b_row);
+                if constexpr (kGated)
+                    tma_load_2d(dst + kSFABytes + C::kSFBBytes / 2, &map_sfb, bar, ltl.sf0 + lg * 16, ltl.b_row + p.N);
                 ++jl;
                 if (++lg == tile_groups(ltl)) {
                     lg = 0;
@@ -1040,7 +1197,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             uint32_t j = 0;
             int32_t chint = 0;
             for (int64_t t = unit; t < total && ok; t += units) {
-                const Tile ct = map_tile<C::kTileM, C::kBN, kWgrad>(p, sh, t, chint);
+                const Tile ct = map_tile<C::kTileM, kTileN, kWgrad, kGated>(p, sh, t, chint);
                 const int32_t ngroups = tile_groups(ct);
                 for (int32_t g = 0; g < ngroups && ok; ++g, ++j) {
                     const uint32_t slot = j % kSfRing, bit = (j / kSfRing) & 1u;
@@ -1120,13 +1277,19 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         int32_t hint = 0, local = 0;
         uint32_t kg = 0, jg = 0;                 // FP32 scales: K-steps and scale groups consumed
         for (int64_t t = unit; t < total; t += units, ++local) {
-            const Tile tl = map_tile<C::kTileM, C::kBN, kWgrad>(p, sh, t, hint);
+            const Tile tl = map_tile<C::kTileM, kTileN, kWgrad, kGated>(p, sh, t, hint);
             // this warp's 128 output columns; their bias is loaded now, while
             // the tile's MMAs run
-            const int32_t nbw = tl.n0 + 128 * h;
+            // (gated: 64 columns; lanes 0..7 hold the gate's bias, lanes 8..15 the up projection's)
+            const int32_t nbw = tl.n0 + (kGated ? 64 : 128) * h;
             uint4 bias_pre = make_uint4(0u, 0u, 0u, 0u);
-            if (C::kStagedStores && p.has_bias && lane < 16 && nbw + 8 * lane < p.N)
+            if constexpr (kGated) {
+                const int32_t nb = nbw + 8 * (lane & 7);
+                if (C::kStagedStores && p.has_bias && lane < 16 && nb < p.N)
+                    bias_pre = __ldg(reinterpret_cast<const uint4*>(p.bias + (2 * int64_t(tl.group) + (lane >> 3)) * p.N + nb));
+            } else if (C::kStagedStores && p.has_bias && lane < 16 && nbw + 8 * lane < p.N) {
                 bias_pre = __ldg(reinterpret_cast<const uint4*>(p.bias + int64_t(tl.group) * p.N + nbw + 8 * lane));
+            }
             uint32_t acc0[64], acc1[64];
             if constexpr (kF32) {
                 // acc (registers: my row x the warp's 128 columns 128 h ..) +=
@@ -1185,9 +1348,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 break;                           // (all lanes together: tcgen05.ld is warp-collective)
             tc_fence_after();
             if (!kWgrad || tl.nk > 0) {
-                const uint32_t taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(128 * h);
+                const uint32_t taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t((kGated ? 64 : 128) * h);
                 tmem_ld_32x32b_x64(taddr, acc0);
-                tmem_ld_32x32b_x64(taddr + 64, acc1);
+                tmem_ld_32x32b_x64(taddr + (kGated ? 128 : 64), acc1);       // (gated: gate, then up)
                 tmem_ld_wait();
             } else {                             // no K-steps (an expert without tokens): the product is 0
 #pragma unroll
@@ -1219,6 +1382,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     // past the end of D (clipped there); per-row stores otherwise
                     const int64_t d_rows = kWgrad ? int64_t(p.groups) * p.M : p.M;
                     const bool tma = !kAcc && (row0 + 32 <= tl.row_end || tl.row_end == d_rows);
+                    if constexpr (kGated) {
+                        if (nb0 < p.N)
+                            store_gated_staged(acc0, acc1, p, bias, row0, tl.row_end, nb0, stage, lane, &map_d, &map_aux,
+                                               tma);
+                        continue;
+                    }
                     if (nb0 < p.N)
                         store_64_staged<kAcc>(acc0, p, bias, row0, tl.row_end, nb0, stage, lane, &map_d, &map_aux, tma);
                     if (nb0 + 64 < p.N)
@@ -1228,6 +1397,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             } else {
                 // (tcgen05.ld is warp-collective: the lanes' row test guards the stores only)
                 const bool live = row < tl.row_end;
+                if constexpr (kGated) {
+                    if (live) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (nbw + 16 * j < p.N)
+                                store_gated_chunk(acc0 + 16 * j, acc1 + 16 * j, p, tl.group, row, nbw + 16 * j);
+                    }
+                    continue;
+                }
                 const uint16_t* bias = p.has_bias ? p.bias + int64_t(tl.group) * p.N : nullptr;
                 const int32_t nb = tl.n0 + 128 * h;
                 // The next tile's operands stream in while these stores go out;
@@ -1263,7 +1441,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
 }
 
-template <int kPair, bool kAcc, bool kWgrad, bool kF32 = false>
+template <int kPair, bool kAcc, bool kWgrad, bool kF32 = false, bool kGated = false>
 te_mx_status launch_gemm(const GemmArgs& a, int sms, unsigned int* status, cudaStream_t stream) {
     using C = Cfg<kPair, kF32>;
     const bool grouped = a.groups > 0;
@@ -1271,7 +1449,10 @@ te_mx_status launch_gemm(const GemmArgs& a, int sms, unsigned int* status, cudaS
     // Extent and pitch of the operands along the reduction axis: K for the
     // dense and grouped GEMMs, the token capacity of the padded layout for wgrad.
     const uint64_t kext = wg ? uint64_t(a.ld_code) : uint64_t(a.K);
-    const uint64_t b_rows = (grouped && !wg) ? uint64_t(a.groups) * uint64_t(a.N) : uint64_t(a.N);
+    // (gated: a group's B rows are its N gate rows, then its N up rows; the
+    // boxes are one projection's 128 rows of a tile)
+    const uint64_t b_rows = ((grouped && !wg) ? uint64_t(a.groups) * uint64_t(a.N) : uint64_t(a.N)) * (kGated ? 2 : 1);
+    const uint32_t b_box = kGated ? 128 : C::kBRows, sfb_box = kGated ? 128 : C::kBN;
     // scale rows in bytes: E8M0, one per 32 K; FP32 scales, 4 bytes per 128 K
     const uint64_t sf_bytes = kF32 ? uint64_t(a.K / 128) * 4 : uint64_t(a.K / 32);
     const uint64_t sf_cols = sf_bytes < 16 ? 16 : sf_bytes;
@@ -1283,11 +1464,11 @@ te_mx_status launch_gemm(const GemmArgs& a, int sms, unsigned int* status, cudaS
     if ((st = encode_tensor_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, kext, uint64_t(a.M),
                                    kext, kBK, kBM, CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
     if ((st = encode_tensor_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, kext, b_rows,
-                                   kext, kBK, C::kBRows, CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
+                                   kext, kBK, b_box, CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
     if ((st = encode_tensor_map_2d(&msa, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sA, sfa_cols, uint64_t(a.M),
                                    sfa_pitch, 16, kBM, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
     if ((st = encode_tensor_map_2d(&msb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sB, sfb_cols, b_rows,
-                                   sfb_pitch, 16, C::kBN, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
+                                   sfb_pitch, 16, sfb_box, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
     // bf16 D and AUX as 32 x 64 boxes in the epilogue's 128-byte-swizzled
     // staging layout (CTA pairs store through them; unused otherwise)
     CUtensorMap md = ma, mx = ma;
@@ -1297,6 +1478,11 @@ te_mx_status launch_gemm(const GemmArgs& a, int sms, unsigned int* status, cudaS
                                        uint64_t(a.N) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK)
             return st;
         mx = md;
+        if (kGated && a.aux &&
+            (st = encode_tensor_map_3d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.aux, uint64_t(a.N), 2, d_rows,
+                                       uint64_t(a.N) * 2, uint64_t(a.N) * 4, 64, 1, 32, CU_TENSOR_MAP_SWIZZLE_128B)) !=
+                TE_MX_OK)
+            return st;
         if (a.gelu && (st = encode_tensor_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.aux, uint64_t(a.N), d_rows,
                                                  uint64_t(a.N) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK)
             return st;
@@ -1307,7 +1493,8 @@ te_mx_status launch_gemm(const GemmArgs& a, int sms, unsigned int* status, cudaS
     p.N = int32_t(a.N);
     p.K = int32_t(a.K);
     p.k_iters = wg ? 0 : int32_t(a.K / kBK);
-    p.n_tiles = int32_t((a.N + C::kBN - 1) / C::kBN);
+    constexpr int kTileN = kGated ? C::kBN / 2 : C::kBN;
+    p.n_tiles = int32_t((a.N + kTileN - 1) / kTileN);
     p.m_tiles = int32_t((a.M + C::kTileM - 1) / C::kTileM);
     p.total_tiles = grouped ? 0 : int64_t(p.m_tiles) * p.n_tiles;
     p.groups = a.groups;
@@ -1318,6 +1505,7 @@ te_mx_status launch_gemm(const GemmArgs& a, int sms, unsigned int* status, cudaS
     p.has_bias = a.has_bias;
     p.gelu = a.gelu;
     p.dgelu = a.dgelu;
+    p.act = a.act;
     p.wgrad = wg;
     p.total_m = a.total_m;
     p.ld_code = a.ld_code;
@@ -1329,7 +1517,7 @@ te_mx_status launch_gemm(const GemmArgs& a, int sms, unsigned int* status, cudaS
     const int64_t slots = sms / kPair;                     // CTAs (pairs) resident at once
     int64_t units = grouped ? slots : (p.total_tiles < slots ? p.total_tiles : slots);
     if (units < 1) units = 1;
-    auto kern = gemm_kernel<kPair, kAcc, kWgrad, kF32>;
+    auto kern = gemm_kernel<kPair, kAcc, kWgrad, kF32, kGated>;
     cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), C::kSmemDyn);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(gemm)");
     if constexpr (kF32) {
@@ -1392,6 +1580,8 @@ te_mx_status gemm_launch(const GemmArgs& a, cudaStream_t stream) {
     // are faster even when fewer tiles than pairs exist (a single-CTA split
     // would keep the same number of SMs busy).  FP32 scales: the same rule.
     const bool pair = a.wgrad ? a.M >= 256 : (a.groups > 0 ? a.M >= 256 * 8 : a.M >= 256);
+    if (a.gated) return pair ? launch_gemm<2, false, false, false, true>(a, sms, status, stream)
+                             : launch_gemm<1, false, false, false, true>(a, sms, status, stream);
     if (a.f32_scales) return pair ? launch_gemm<2, false, false, true>(a, sms, status, stream)
                                   : launch_gemm<1, false, false, true>(a, sms, status, stream);
     if (a.wgrad) {

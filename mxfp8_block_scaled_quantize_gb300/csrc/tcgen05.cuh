@@ -277,6 +277,14 @@ __device__ __forceinline__ void tma_store_2d_evict_first(const CUtensorMap* desc
                  :: "l"(reinterpret_cast<uint64_t>(desc)), "r"(src), "r"(x), "r"(y), "l"(policy) : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d_evict_first(const CUtensorMap* desc, uint32_t src, int32_t x, int32_t y,
+                                                         int32_t z) {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;"
+                 :: "l"(reinterpret_cast<uint64_t>(desc)), "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
+}
+
 // Register reallocation between warp groups (setmaxnreg; every thread of the
 // warp group executes the same one).  An increase waits until enough registers
 // are free in the block's pool, so the sum over the block's warps must not

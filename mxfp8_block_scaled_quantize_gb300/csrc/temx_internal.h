@@ -50,6 +50,10 @@ struct GemmArgs {
     // b_2d: sB constant over 128-row blocks (128x128 weight blocks).
     bool f32_scales;
     bool b_2d;
+    // Gated (dense or grouped): B = [2N x K] per group, N gate rows then N up
+    // rows; D = act(gate) * up [M x N], aux (or null) = [gate | up] [M x 2N].
+    bool gated;
+    int32_t act;             // te_mx_activation
 };
 
 te_mx_status quantize_launch(const QuantizeArgs& a, cudaStream_t stream);
