@@ -349,6 +349,33 @@ TEMX_API te_mx_status te_mx_grouped_gated_gemm(int32_t num_groups, const int32_t
                                                int64_t F, int64_t K, const void* bias, int32_t activation,
                                                void* D, void* aux, void* stream);
 
+/* te_mx_gated_backward — backward pass of the gated feed-forward's activation
+ * and product, with the quantisation that its two GEMMs need.  From dh, the
+ * gradient of D, and gate_up, the aux of te_mx_gated_gemm:
+ *   dg = dh up act'(gate),  du = dh act(gate),
+ * in fp32, each rounded once to bf16; [dg | du] is the gradient of the
+ * pre-activations, in the layout of aux.
+ *   dh       bf16 [rows x F], pitch ld_dh;  gate_up  bf16 [rows x 2F], pitch ld_gate_up;
+ *   d_gate_up  bf16 [rows x 2F], pitch ld_d, or NULL; may be gate_up itself
+ *            (the same pointer and pitch) when it is the only output;
+ *   q_row/s_row  the row-wise copy of [dg | du] (uint8 [rows x 2F], [rows x
+ *            ld_s_row]): the A operand of dX = [dg | du] W; both may be NULL;
+ *   q_col/s_col  the column-wise copy (uint8 [2F x ld_q_col], [2F x
+ *            ld_s_col]) with the tokens zero-padded to Kp = round_up(rows, 128)
+ *            (codes 0, scale bytes 0x00): the A operand of dW = [dg | du]^T X
+ *            with K = Kp = ld_q_col, and one group of the per-expert layout of
+ *            te_mx_quantize_colwise_grouped, which makes X's copy.  Both may be NULL.
+ * The copies are bit for bit what te_mx_quantize makes of the bf16 matrix [dg | du].
+ * Rules: F % 16 == 0 (F % 32 == 0 for the copies); pitches multiples of 8
+ * elements; ld_q_col a multiple of 16 >= Kp; ld_s_row, ld_s_col multiples of 16
+ * >= 2F/32 and Kp/32; every pointer 16-byte aligned; rows == 0 or F == 0 is a
+ * no-op.  Bytes of the copies past the block counts, Kp and 2F are not written. */
+TEMX_API te_mx_status te_mx_gated_backward(const void* dh, int64_t ld_dh, const void* gate_up, int64_t ld_gate_up,
+                                           int64_t rows, int64_t F, int32_t activation, void* d_gate_up, int64_t ld_d,
+                                           uint8_t* q_row, uint8_t* s_row, int64_t ld_s_row,
+                                           uint8_t* q_col, int64_t ld_q_col, uint8_t* s_col, int64_t ld_s_col,
+                                           void* stream);
+
 /* te_mx_gemm_fp32_scales — the Float8BlockScaling TN GEMM computed with the
  * FP32 scales directly (ROCm/TransformerEngine README, "Blockwise FP8 GEMM
  * support on ROCm", second mode), on te_mx_block_quantize_fp32 output:

@@ -50,6 +50,8 @@ SIGNATURES = {
     "te_mx_gated_gemm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _I32, _P, _P, _P]),
     "te_mx_grouped_gated_gemm": (ctypes.c_int, [_I32, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _P,
                                                 _P]),
+    "te_mx_gated_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _I64, _P,
+                                            _I64, _P]),
     "te_mx_gemm_fp32_scales": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I32, _I64, _I64, _I64, _P, _I32, _P, _P,
                                               _P]),
     "te_mx_grouped_gemm": (ctypes.c_int, [_I32, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32,
@@ -185,6 +187,12 @@ def te_mx_grouped_gated_gemm(num_groups, group_m, total_m, X, sX, ld_sX, W, sW, 
                              stream) -> None:
     _check(lib().te_mx_grouped_gated_gemm(num_groups, group_m, total_m, X, sX, ld_sX, W, sW, ld_sW, F, K, bias,
                                           activation, D, aux, stream))
+
+
+def te_mx_gated_backward(dh, ld_dh, gate_up, ld_gate_up, rows, F, activation, d_gate_up, ld_d, q_row, s_row, ld_s_row,
+                         q_col, ld_q_col, s_col, ld_s_col, stream) -> None:
+    _check(lib().te_mx_gated_backward(dh, ld_dh, gate_up, ld_gate_up, rows, F, activation, d_gate_up, ld_d, q_row, s_row,
+                                      ld_s_row, q_col, ld_q_col, s_col, ld_s_col, stream))
 
 
 def te_mx_gemm_workspace_size(M, N, K, num_groups=0) -> int:
@@ -565,3 +573,34 @@ def grouped_gated_gemm(group_m, qx, sx, qw, sw, activation: str = "silu", bias=N
                              sw2.data_ptr(), _pitch(sw2), N // 2, K, _ptr(bias), ACTIVATIONS[activation], h.data_ptr(),
                              _ptr(pre), _stream_ptr(stream))
     return h, pre
+
+
+def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, rowwise: bool = True, colwise: bool = True,
+                   stream=None, out=None):
+    """Gradient of the gated feed-forward's pre-activations: dh bf16 [M, F] and
+    gate_up bf16 [M, 2F] (the ``pre`` of ``gated_gemm``).  Returns a dict with
+    "d_gate_up" (bf16 [M, 2F], with ``dense``), "q_row"/"s_row" (its row-wise
+    MXFP8 copy) and "q_col"/"s_col" (its column-wise copy [2F, Kp], the tokens
+    zero-padded to Kp, M rounded up to 128), so that
+    dX = gemm(q_row, s_row, W's column-wise copy) and
+    dW = gemm(q_col, s_col, X's column-wise copy, padded likewise)."""
+    import torch
+    assert dh.dtype == gate_up.dtype == torch.bfloat16 and dh.dim() == gate_up.dim() == 2 and dh.is_cuda
+    M, F = dh.shape
+    assert gate_up.shape == (M, 2 * F) and dh.stride(1) == gate_up.stride(1) == 1
+    o = dict(out or {})
+    if dense and "d_gate_up" not in o:
+        o["d_gate_up"] = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=dh.device)
+    if rowwise and "q_row" not in o:
+        o["q_row"] = torch.empty(M, 2 * F, dtype=torch.uint8, device=dh.device)
+        o["s_row"] = torch.empty(M, te_mx_scale_pitch(2 * F), dtype=torch.uint8, device=dh.device)
+    if colwise and "q_col" not in o:
+        kp = (M + 127) // 128 * 128
+        o["q_col"] = torch.empty(2 * F, kp, dtype=torch.uint8, device=dh.device)
+        o["s_col"] = torch.empty(2 * F, te_mx_scale_pitch(kp), dtype=torch.uint8, device=dh.device)
+    ld = lambda k: _pitch(o[k]) if k in o else 0  # noqa: E731
+    te_mx_gated_backward(dh.data_ptr(), _pitch(dh), gate_up.data_ptr(), _pitch(gate_up), M, F, ACTIVATIONS[activation],
+                         _ptr(o.get("d_gate_up")), ld("d_gate_up"), _ptr(o.get("q_row")), _ptr(o.get("s_row")),
+                         ld("s_row"), _ptr(o.get("q_col")), ld("q_col"), _ptr(o.get("s_col")), ld("s_col"),
+                         _stream_ptr(stream))
+    return o

@@ -581,6 +581,43 @@ te_mx_status te_mx_grouped_gated_gemm(int32_t num_groups, const int32_t* group_m
     return gemm_launch(a, static_cast<cudaStream_t>(stream));
 }
 
+te_mx_status te_mx_gated_backward(const void* dh, int64_t ld_dh, const void* gate_up, int64_t ld_gate_up, int64_t rows,
+                                  int64_t F, int32_t activation, void* d_gate_up, int64_t ld_d, uint8_t* q_row,
+                                  uint8_t* s_row, int64_t ld_s_row, uint8_t* q_col, int64_t ld_q_col, uint8_t* s_col,
+                                  int64_t ld_s_col, void* stream) {
+    t_last_error[0] = '\0';
+    if (rows < 0 || F < 0) return set_error(TE_MX_ERR_INVALID_ARG, "negative size %lld x %lld", (long long)rows, (long long)F);
+    if (activation < TE_MX_ACT_SILU || activation > TE_MX_ACT_RELU)
+        return set_error(TE_MX_ERR_INVALID_ARG, "unknown activation %d", int(activation));
+    if ((q_row == nullptr) != (s_row == nullptr))
+        return set_error(TE_MX_ERR_INVALID_ARG, "q_row and s_row must both be given or both be NULL");
+    if ((q_col == nullptr) != (s_col == nullptr))
+        return set_error(TE_MX_ERR_INVALID_ARG, "q_col and s_col must both be given or both be NULL");
+    if (rows == 0 || F == 0 || (!d_gate_up && !q_row && !q_col)) return TE_MX_OK;
+    if (!dh || !gate_up) return set_error(TE_MX_ERR_INVALID_ARG, "dh and gate_up are required");
+    if (F % 16) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "F=%lld is not a multiple of 16", (long long)F);
+    if ((q_row || q_col) && F % 32)
+        return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "quantised output needs F %% 32 == 0 (F=%lld)", (long long)F);
+    if (rows > (int64_t(1) << 31) - 256 || F > (int64_t(1) << 29))
+        return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "rows or F too large");
+    if (ld_dh < F || ld_dh % 8 || ld_gate_up < 2 * F || ld_gate_up % 8 || (d_gate_up && (ld_d < 2 * F || ld_d % 8)))
+        return set_error(TE_MX_ERR_MISALIGNED, "pitches must be multiples of 8, ld_dh >= F, ld_gate_up and ld_d >= 2F");
+    if (!aligned(dh, 16) || !aligned(gate_up, 16) || !aligned(d_gate_up, 16) || !aligned(q_row, 16) || !aligned(q_col, 16) ||
+        !aligned(s_row, 16) || !aligned(s_col, 16))
+        return set_error(TE_MX_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    if (q_row && (ld_s_row % 16 || ld_s_row < 2 * F / 32))
+        return set_error(TE_MX_ERR_MISALIGNED, "ld_s_row=%lld must be a multiple of 16 and >= 2F/32", (long long)ld_s_row);
+    const int64_t padded = (rows + 127) / 128 * 128;
+    if (q_col && (ld_q_col % 16 || ld_q_col < padded || ld_s_col % 16 || ld_s_col < padded / 32))
+        return set_error(TE_MX_ERR_MISALIGNED, "ld_q_col=%lld and ld_s_col=%lld must be multiples of 16, >= %lld and >= %lld",
+                         (long long)ld_q_col, (long long)ld_s_col, (long long)padded, (long long)(padded / 32));
+    te_mx_status st = check_device(nullptr);
+    if (st != TE_MX_OK) return st;
+    GatedBackwardArgs a{dh, ld_dh, gate_up, ld_gate_up, rows, F, activation, d_gate_up, ld_d, q_row, s_row, ld_s_row,
+                        q_col, ld_q_col, s_col, ld_s_col};
+    return gated_backward_launch(a, static_cast<cudaStream_t>(stream));
+}
+
 te_mx_status te_mx_gemm_fp32_scales(const uint8_t* A, const float* sA, int64_t ld_sA,
                                     const uint8_t* B, const float* sB, int64_t ld_sB, int32_t b_blocks_2d,
                                     int64_t M, int64_t N, int64_t K, const void* bias, int32_t epilogue,

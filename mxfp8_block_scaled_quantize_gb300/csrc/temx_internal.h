@@ -104,6 +104,20 @@ constexpr int kLnMaxParts = 304;                 // partial sums per column, at 
 int ln_backward_parts(int64_t rows);
 te_mx_status ln_backward_launch(const LnBackwardArgs& a, cudaStream_t stream);
 
+struct GatedBackwardArgs {
+    const void* dh;          // bf16 [rows x F], pitch ld_dh
+    int64_t ld_dh;
+    const void* gate_up;     // bf16 [rows x 2F], pitch ld_gate_up
+    int64_t ld_gate_up;
+    int64_t rows, F;
+    int32_t act;             // te_mx_activation
+    void* d_gate_up;         // bf16 [rows x 2F], pitch ld_d, or null
+    int64_t ld_d;
+    uint8_t* q_row; uint8_t* s_row; int64_t ld_s_row;                       // [rows x 2F] or null
+    uint8_t* q_col; int64_t ld_q_col; uint8_t* s_col; int64_t ld_s_col;     // [2F x round_up(rows, 128)] or null
+};
+te_mx_status gated_backward_launch(const GatedBackwardArgs& a, cudaStream_t stream);
+
 struct GroupedColwiseArgs {
     const void* x;           // bf16 [total_m x cols], pitch ld_x (token-major)
     int64_t total_m, cols, ld_x;

@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from .mx_oracle import FP32_U, gelu_tanh
+from .mx_oracle import FP32_U
 
 HALF_STEP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}     # relative, at most
 # half the distance between the type's smallest subnormals (2^-133, 2^-24, 2^-149)
@@ -112,7 +112,8 @@ def act(x, kind):
         return np.maximum(x, 0.0)
     if kind == "silu":
         return x * sigmoid(x)
-    return gelu_tanh(x)
+    # (1 + tanh(z / 2)) / 2 is the logistic function of z, without the cancellation for x < 0
+    return x * sigmoid(_A * (x + 0.044715 * x ** 3))
 
 
 def act_grad(x, kind):

@@ -48,3 +48,31 @@ def test_grouped_refusals(change, error):
 def test_empty_problems():
     binding.te_mx_gated_gemm(**{**GEMM, "M": 0})
     binding.te_mx_grouped_gated_gemm(**{**GROUPED, "total_m": 0})
+
+
+BACKWARD = dict(dh=16, ld_dh=64, gate_up=16, ld_gate_up=128, rows=40, F=64, activation=0, d_gate_up=16, ld_d=128, q_row=16,
+                s_row=16, ld_s_row=16, q_col=16, ld_q_col=128, s_col=16, ld_s_col=16, stream=0)
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(rows=-1), "INVALID_ARG"), (dict(F=-32), "INVALID_ARG"), (dict(activation=3), "INVALID_ARG"),
+    (dict(q_row=0), "INVALID_ARG"), (dict(s_row=0), "INVALID_ARG"), (dict(q_col=0), "INVALID_ARG"),
+    (dict(s_col=0), "INVALID_ARG"), (dict(dh=0), "INVALID_ARG"), (dict(gate_up=0), "INVALID_ARG"),
+    (dict(F=40), "UNSUPPORTED_SHAPE"), (dict(F=48), "UNSUPPORTED_SHAPE"), (dict(rows=1 << 31), "UNSUPPORTED_SHAPE"),
+    (dict(F=1 << 30), "UNSUPPORTED_SHAPE"), (dict(ld_dh=56), "MISALIGNED"), (dict(ld_dh=68), "MISALIGNED"),
+    (dict(ld_gate_up=120), "MISALIGNED"), (dict(ld_gate_up=132), "MISALIGNED"), (dict(ld_d=64), "MISALIGNED"),
+    (dict(dh=8), "MISALIGNED"), (dict(gate_up=8), "MISALIGNED"), (dict(d_gate_up=8), "MISALIGNED"),
+    (dict(q_row=8), "MISALIGNED"), (dict(q_col=8), "MISALIGNED"), (dict(s_row=8), "MISALIGNED"),
+    (dict(s_col=8), "MISALIGNED"), (dict(ld_s_row=0), "MISALIGNED"), (dict(ld_s_row=24), "MISALIGNED"),
+    (dict(ld_q_col=64), "MISALIGNED"), (dict(ld_q_col=136), "MISALIGNED"), (dict(ld_s_col=0), "MISALIGNED"),
+    (dict(rows=4000, ld_q_col=4096), "MISALIGNED"),
+])
+def test_backward_refusals(change, error):
+    with pytest.raises(binding.TemxError, match=error):
+        binding.te_mx_gated_backward(**{**BACKWARD, **change})
+
+
+def test_backward_empty_problems():
+    binding.te_mx_gated_backward(**{**BACKWARD, "rows": 0})
+    binding.te_mx_gated_backward(**{**BACKWARD, "F": 0})
+    binding.te_mx_gated_backward(**{**BACKWARD, "d_gate_up": 0, "q_row": 0, "s_row": 0, "q_col": 0, "s_col": 0})

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 from oracle import ffn_oracle as F
+from oracle.mx_oracle import gelu_tanh
 
 H = 1e-5            # step: central differences are off by ~ H^2 f''' / 6 and 2^-53 |f| / H
 
@@ -48,6 +49,11 @@ def test_activations_at_their_limits():
         assert np.allclose(F.act(x, kind), [0, 0, 0, 100, 1e4], atol=1e-30)
         want0 = 0.0 if kind == "relu" else 0.5
         assert np.allclose(F.act_grad(x, kind), [0, 0, want0, 1, 1], atol=1e-30)
+
+
+def test_gelu_is_the_tanh_form():
+    x = np.linspace(-4, 12, 1001)
+    assert np.allclose(F.act(x, "gelu"), gelu_tanh(x), rtol=1e-12, atol=1e-15)
 
 
 def test_layernorm_of_a_constant_row_is_the_shift():
