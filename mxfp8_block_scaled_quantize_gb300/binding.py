@@ -213,10 +213,24 @@ def te_mx_version() -> str:
 
 # ---------------------------------------------------------------- torch helpers
 
+_raw_stream = None
+
+
 def _stream_ptr(stream=None) -> int:
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    """The given stream's handle, or the current device's current stream's (taken
+    without building a Stream object, which costs as much as a small launch)."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        c = torch._C
+        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+            torch.cuda.init()
+            _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
 
 
 def _ptr(t) -> int:
@@ -338,14 +352,23 @@ def layernorm_quantize(x, gamma, beta, eps: float = 1e-5, rowwise: bool = True, 
     return o
 
 
+_dtype_codes = None
+
+
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}[t.dtype]
+    global _dtype_codes
+    if _dtype_codes is None:
+        import torch
+        _dtype_codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    return _dtype_codes[t.dtype]
 
 
 def _pitch(t) -> int:
     """Row pitch of a 2-D tensor (a single row has no next one, whatever its stride says)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    assert unit == 1 or cols == 1
+    return ld if rows > 1 else max(ld, cols)
 
 
 def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream=None, out=None):
@@ -353,22 +376,25 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
     gamma and beta (None: no shift) have its type or fp32.  Returns a dict with
     "y" (the type of x) and, with ``stats``, "mu" and "rsigma" (fp32 [rows])
     for ``layernorm_backward``."""
-    import torch
-    assert x.dim() == 2 and x.is_cuda and x.stride(1) == 1
     rows, hidden = x.shape
-    assert gamma.numel() == hidden and gamma.is_contiguous() and gamma.is_cuda
-    assert beta is None or (beta.dtype == gamma.dtype and beta.numel() == hidden and beta.is_contiguous())
-    o = dict(out or {})
-    if "y" not in o:
-        o["y"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+    assert x.is_cuda and gamma.is_cuda and gamma.shape == (hidden,) and gamma.is_contiguous()
+    b = 0
+    if beta is not None:
+        assert beta.dtype == gamma.dtype and beta.shape == (hidden,) and beta.is_contiguous()
+        b = beta.data_ptr()
+    import torch
+    o = {} if out is None else dict(out)
+    y = o.get("y")
+    if y is None:
+        y = o["y"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+    else:
+        assert y.shape == x.shape and y.dtype == x.dtype
     if stats and "mu" not in o:
         o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
-        o["rsigma"] = torch.empty(rows, dtype=torch.float32, device=x.device)
-    y = o["y"]
-    assert y.shape == x.shape and y.dtype == x.dtype and y.stride(1) == 1
-    te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), _ptr(beta),
-                    _dtype_code(gamma), eps, y.data_ptr(), _pitch(y), _ptr(o.get("mu")), _ptr(o.get("rsigma")),
-                    _stream_ptr(stream))
+        o["rsigma"] = torch.empty_like(o["mu"])
+    mu, rsigma = (o["mu"].data_ptr(), o["rsigma"].data_ptr()) if "mu" in o else (0, 0)
+    te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), b, _dtype_code(gamma), eps,
+                    y.data_ptr(), _pitch(y), mu, rsigma, _stream_ptr(stream))
     return o
 
 
@@ -378,25 +404,24 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
     from the forward pass.  Returns a dict with "dx" and, with ``dparams``,
     "dgamma" and "dbeta" (the type of gamma); their scratch is ``workspace``
     (uint8 CUDA tensor) or allocated here."""
-    import torch
-    assert x.dim() == 2 and x.is_cuda and x.stride(1) == 1
-    assert dy.shape == x.shape and dy.dtype == x.dtype and dy.stride(1) == 1
     rows, hidden = x.shape
-    assert gamma.numel() == hidden and gamma.is_contiguous()
-    assert mu.dtype == rsigma.dtype == torch.float32 and mu.numel() == rsigma.numel() == rows
-    o = dict(out or {})
-    if "dx" not in o:
-        o["dx"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
-    need = 0
+    assert x.is_cuda and dy.is_cuda and dy.shape == x.shape and dy.dtype == x.dtype
+    assert gamma.shape == (hidden,) and gamma.is_contiguous() and mu.shape == rsigma.shape == (rows,)
+    assert mu.is_contiguous() and rsigma.is_contiguous() and _dtype_code(mu) == _dtype_code(rsigma) == FP32
+    import torch
+    o = {} if out is None else dict(out)
+    dx = o.get("dx")
+    if dx is None:
+        dx = o["dx"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
+    else:
+        assert dx.shape == x.shape and dx.dtype == x.dtype
     if dparams:
         if "dgamma" not in o:
-            o["dgamma"] = torch.empty(hidden, dtype=gamma.dtype, device=x.device)
-            o["dbeta"] = torch.empty(hidden, dtype=gamma.dtype, device=x.device)
-        need = te_mx_layernorm_backward_workspace_size(rows, hidden)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    dx = o["dx"]
-    assert dx.shape == x.shape and dx.dtype == x.dtype and dx.stride(1) == 1
+            o["dgamma"], o["dbeta"] = torch.empty_like(gamma), torch.empty_like(gamma)
+        if workspace is None:
+            need = te_mx_layernorm_backward_workspace_size(rows, hidden)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, _dtype_code(x),
                              gamma.data_ptr(), _dtype_code(gamma), mu.data_ptr(), rsigma.data_ptr(), dx.data_ptr(),
                              _pitch(dx), _ptr(o.get("dgamma")), _ptr(o.get("dbeta")), _ptr(workspace),

@@ -282,21 +282,32 @@ ln_backward_params_kernel(const LnBackwardArgs a, int parts) {
 }
 
 // dgamma / dbeta from `parts` partial sums per column.  A block owns 32
-// columns (lane = column); warp w adds parts w, w + 8, ... in order, then the
-// warps' sums are added in warp order.
-constexpr int kReduceWarps = 8;
+// columns (lane = column); warp w adds parts w, w + 32, ... in order, loading
+// four of them at a time (the sums come from L2 and the loads' latency is what
+// this costs), then the warps' sums are added in warp order.
+constexpr int kReduceWarps = 32;
 __global__ void __launch_bounds__(kReduceWarps * 32)
 ln_backward_reduce_kernel(const LnBackwardArgs a, int parts) {
-    __shared__ float sums[2][kReduceWarps][32];
+    __shared__ float sums[2][kReduceWarps][33];
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
     float sg = 0.0f, sb = 0.0f;
     if (c < a.hidden)
-        for (int p = warp; p < parts; p += kReduceWarps) {
-            sg += a.partial[2 * int64_t(p) * a.hidden + c];
-            sb += a.partial[(2 * int64_t(p) + 1) * a.hidden + c];
+        for (int p0 = warp; p0 < parts; p0 += 4 * kReduceWarps) {
+            float g[4], b[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t p = p0 + k * kReduceWarps;
+                g[k] = p < parts ? a.partial[2 * p * a.hidden + c] : 0.0f;
+                b[k] = p < parts ? a.partial[(2 * p + 1) * a.hidden + c] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sg += g[k];
+                sb += b[k];
+            }
         }
     sums[0][warp][lane] = sg;
     sums[1][warp][lane] = sb;
@@ -358,8 +369,26 @@ __device__ __forceinline__ void remote_store(uint32_t addr, uint64_t v, uint32_t
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
                  :: "r"(addr), "l"(v), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void group_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+// The warps' sums of a row group meet in 16 slots (zero past its warps), which
+// every thread adds in the same order, four independent chains of packed pairs.
+constexpr int kPartWarps = 16, kPartGroups = 8;
+__device__ __forceinline__ uint64_t sum_slots2(uint32_t addr) {          // 16 pairs (c1, c2)
+    uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kPartWarps / 2; ++j) {
+        uint64_t u, v;
+        lds_pairs(addr + 16 * j, u, v);
+        acc[j & 1] = f32x2::add(acc[j & 1], u);
+        acc[2 + (j & 1)] = f32x2::add(acc[2 + (j & 1)], v);
+    }
+    return f32x2::add(f32x2::add(acc[0], acc[2]), f32x2::add(acc[1], acc[3]));
 }
 
 template <typename T, bool kP32, int kV, bool kCluster>
@@ -369,11 +398,11 @@ ln_backward_vec_kernel(const LnBackwardArgs a, const LnBwdShape sh, unsigned int
     extern __shared__ __align__(128) uint8_t ring_raw[];
     __shared__ __align__(8) uint64_t full[kBwdMaxGroups][kBwdMaxStages];
     __shared__ __align__(8) uint64_t part_full[2];
-    __shared__ __align__(16) float2 warp_part[2][kBwdThreads / 32];       // by parity of the row count
+    __shared__ __align__(16) float2 warp_part[2][kPartGroups][kPartWarps];     // by parity of the row count
     __shared__ __align__(16) float2 block_part[2][kBwdMaxCluster];
 
     const int group = threadIdx.x / sh.group, t = threadIdx.x % sh.group, lane = threadIdx.x & 31;
-    const int gwarps = sh.group >> 5, gwarp0 = group * gwarps;
+    const int gwarps = sh.group >> 5;
     const uint32_t rank = kCluster ? block_rank() : 0u;
     const int unit = int(blockIdx.x) / sh.cluster, units = int(gridDim.x) / sh.cluster;
     const int vec0 = int(rank) * sh.cvec, mine = min(sh.cvec, sh.nvec - vec0);      // this block's vectors
@@ -388,6 +417,10 @@ ln_backward_vec_kernel(const LnBackwardArgs a, const LnBwdShape sh, unsigned int
         mbar_init(smem_u32(&part_full[1]), 1);
     }
     if (t == 0) fence_mbarrier_init();
+    if (threadIdx.x < kPartGroups * kPartWarps) {        // (slots past a group's warps stay 0)
+        (&warp_part[0][0][0])[threadIdx.x] = make_float2(0.0f, 0.0f);
+        (&warp_part[1][0][0])[threadIdx.x] = make_float2(0.0f, 0.0f);
+    }
     grid_dependency_wait();
     grid_launch_dependents();
     if constexpr (kCluster) all_blocks_sync();           // the barriers are ready before any remote store
@@ -458,21 +491,23 @@ ln_backward_vec_kernel(const LnBackwardArgs a, const LnBwdShape sh, unsigned int
                 }
             }
         }
-        float c1 = warp_sum(f32x2::lo(s1) + f32x2::hi(s1)), c2 = warp_sum(f32x2::lo(s2) + f32x2::hi(s2));
+        // lanes 0..15 add up the first sum, lanes 16..31 the second
+        float c1 = f32x2::lo(s1) + f32x2::hi(s1), c2 = f32x2::lo(s2) + f32x2::hi(s2);
+        float half = (lane < 16 ? c1 : c2) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? c2 : c1, 16);
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) half += __shfl_xor_sync(0xFFFFFFFFu, half, o);
         if (gwarps > 1) {
             // (a parity's slots are read before the next row's barrier, and
             // written again after it)
-            float2* part = warp_part[i & 1] + gwarp0;
-            if (lane == 0) part[t >> 5] = make_float2(c1, c2);
+            float* part = reinterpret_cast<float*>(warp_part[i & 1][group]);
+            if ((lane & 15) == 0) part[2 * (t >> 5) + (lane >> 4)] = half;
             group_barrier(1 + group, sh.group);
-            c1 = c2 = 0.0f;
-            for (int w = 0; w < gwarps; ++w) {
-                const float2 f = part[w];
-                c1 += f.x;
-                c2 += f.y;
-            }
+            const uint64_t c = sum_slots2(smem_u32(part));
+            c1 = f32x2::lo(c);
+            c2 = f32x2::hi(c);
         } else {
-            __syncwarp();                                // every lane has read the stage
+            c1 = __shfl_sync(0xFFFFFFFFu, half, 0);      // (every lane has read the stage)
+            c2 = __shfl_sync(0xFFFFFFFFu, half, 16);
         }
         if (t == 0 && ok && i + sh.stages < n_mine) load(i + sh.stages);
         if constexpr (kCluster) {
