@@ -321,29 +321,35 @@ ln_backward_reduce_kernel(const LnBackwardArgs a, int parts) {
     }
 }
 
-// Backward, rows on 16-byte boundaries, one pass over dy and x.  Persistent;
-// a group of threads owns the same columns (two vectors per thread at most) of
-// every row that it takes, so the columns' sums of dy xh and dy stay in its
-// registers from row to row.  dy and x come through a ring of rows in shared
-// memory, one bulk copy each, several rows ahead (a row's two sums are a
-// dependent chain of loads, shuffles and a barrier, which the copies of the
-// next rows cover); a row's g and xh stay in registers between its sums and
-// dx.  Rows past 16 KB are split over a cluster of blocks: each adds its part
-// of the two sums to every other's with one 8-byte remote store per row.
-// Short rows: several groups per block, joined at the end, so that every block
-// leaves one partial sum per column.
-constexpr int kBwdThreads = 512;
-constexpr int kBwdMaxStages = 8;
-constexpr int kBwdRingBytes = 200 * 1024;
+// Backward, rows on 16-byte boundaries: one pass over dy and x, persistent.  A
+// group of threads owns the same columns (kV vectors per thread) of every row
+// that it takes, so the sums of dy xh and dy over the rows stay in registers.
+// dy and x come through a ring of rows in shared memory, one bulk copy each,
+// and their words stay in registers from the row's sums to its dx.
+// Rows past a block's threads are split over a cluster of blocks, which add
+// each other's sums with remote stores.  Short rows: several groups per block,
+// joined at the end, so that every block leaves one partial sum per column.
+// Measured, 8192 x 7168 bf16 (floor 52 us; a plain copy of the bytes 58): 68 us,
+// of which 7 go to the column sums' join.  A row's two sums cross the group in
+// a dependent chain (shuffles, shared memory, a barrier) that 14 warps cannot
+// hide; two rows at a time (78 us), dx a row later (84 us), rows' sums in warps
+// of their own (113 us) and four vectors per thread in two groups (77 us) all
+// cost more, in registers first: whatever spills misses the L1, which the ring
+// leaves small.  fp32 rows take four vectors per thread, as many columns as two
+// of 16 bits: 515 x 16384 28 us (two: 44 us, in clusters of four).
 constexpr int kBwdMaxGroups = 16;
+constexpr int kBwdMaxStages = 16;
+constexpr int kBwdSmem = 200 * 1024;             // the ring
 constexpr int kBwdMaxCluster = 8;
+constexpr int kBwdThreads = 512;                 // 128 registers each
+template <typename T> constexpr int kBwdVectors = sizeof(T) == 4 ? 4 : 2;        // per thread
 
 struct LnBwdShape {
     int nvec;        // vectors of a row
     int cvec;        // vectors of a block's part of it
     int group;       // threads per group
     int groups;      // groups per block
-    int stages;
+    int stages;      // rows of a group's ring
     int cluster;     // blocks per row
 };
 
@@ -369,214 +375,196 @@ __device__ __forceinline__ void remote_store(uint32_t addr, uint64_t v, uint32_t
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
                  :: "r"(addr), "l"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
-    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
-}
 __device__ __forceinline__ void group_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
-// The warps' sums of a row group meet in 16 slots (zero past its warps), which
-// every thread adds in the same order, four independent chains of packed pairs.
-constexpr int kPartWarps = 16, kPartGroups = 8;
-__device__ __forceinline__ uint64_t sum_slots2(uint32_t addr) {          // 16 pairs (c1, c2)
-    uint64_t acc[4] = {0, 0, 0, 0};
+// Sums over the warp of two values in one butterfly: lanes 0..15 add up the
+// first, lanes 16..31 the second, and return it.
+__device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
+    float half = (lane < 16 ? a : b) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? b : a, 16);
 #pragma unroll
-    for (int j = 0; j < kPartWarps / 2; ++j) {
-        uint64_t u, v;
-        lds_pairs(addr + 16 * j, u, v);
-        acc[j & 1] = f32x2::add(acc[j & 1], u);
-        acc[2 + (j & 1)] = f32x2::add(acc[2 + (j & 1)], v);
-    }
-    return f32x2::add(f32x2::add(acc[0], acc[2]), f32x2::add(acc[1], acc[3]));
+    for (int o = 8; o >= 1; o >>= 1) half += __shfl_xor_sync(0xFFFFFFFFu, half, o);
+    return half;
 }
 
-template <typename T, bool kP32, int kV, bool kCluster>
+template <typename T, bool kP32, bool kCluster>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 ln_backward_vec_kernel(const LnBackwardArgs a, const LnBwdShape sh, unsigned int* status) {
     using V = Vec<T>;
-    extern __shared__ __align__(128) uint8_t ring_raw[];
-    __shared__ __align__(8) uint64_t full[kBwdMaxGroups][kBwdMaxStages];
-    __shared__ __align__(8) uint64_t part_full[2];
-    __shared__ __align__(16) float2 warp_part[2][kPartGroups][kPartWarps];     // by parity of the row count
-    __shared__ __align__(16) float2 block_part[2][kBwdMaxCluster];
+    constexpr int kV = kBwdVectors<T>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[kBwdMaxGroups][kBwdMaxStages];          // a row's dy and x landed
+    __shared__ __align__(8) uint64_t joined[2];                                   // every block's sums of a row are there
+    __shared__ __align__(8) float warp_part[2][kBwdThreads / 32][2];              // by parity of the row
+    __shared__ __align__(8) float block_part[2][kBwdMaxCluster][2];
 
     const int group = threadIdx.x / sh.group, t = threadIdx.x % sh.group, lane = threadIdx.x & 31;
-    const int gwarps = sh.group >> 5;
+    const int gwarps = sh.group >> 5, gwarp0 = group * gwarps;
     const uint32_t rank = kCluster ? block_rank() : 0u;
     const int unit = int(blockIdx.x) / sh.cluster, units = int(gridDim.x) / sh.cluster;
     const int vec0 = int(rank) * sh.cvec, mine = min(sh.cvec, sh.nvec - vec0);      // this block's vectors
-    const uint32_t stage_bytes = uint32_t(sh.cvec) * 32;                            // dy, then x
-    const uint32_t ring = smem_u32(ring_raw) + uint32_t(group * sh.stages) * stage_bytes;
+    const uint32_t bytes = uint32_t(mine) * 16, stage_bytes = uint32_t(sh.cvec) * 32;     // dy, then x
+    const uint32_t ring = smem_u32(smem) + uint32_t(group * sh.stages) * stage_bytes;
+    // rows first, first + step, ... of this group (every block of a cluster: the same)
     const int64_t first = int64_t(unit) * sh.groups + group, step = int64_t(units) * sh.groups;
-    const int64_t n_mine = first < a.rows ? (a.rows - first + step - 1) / step : 0;
+    const int n_mine = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
     if (t == 0)
         for (int i = 0; i < sh.stages; ++i) mbar_init(smem_u32(&full[group][i]), 1);
     if (kCluster && threadIdx.x == 0) {
-        mbar_init(smem_u32(&part_full[0]), 1);
-        mbar_init(smem_u32(&part_full[1]), 1);
+        mbar_init(smem_u32(&joined[0]), 1);
+        mbar_init(smem_u32(&joined[1]), 1);
     }
     if (t == 0) fence_mbarrier_init();
-    if (threadIdx.x < kPartGroups * kPartWarps) {        // (slots past a group's warps stay 0)
-        (&warp_part[0][0][0])[threadIdx.x] = make_float2(0.0f, 0.0f);
-        (&warp_part[1][0][0])[threadIdx.x] = make_float2(0.0f, 0.0f);
-    }
     grid_dependency_wait();
     grid_launch_dependents();
-    if constexpr (kCluster) all_blocks_sync();           // the barriers are ready before any remote store
+    if constexpr (kCluster) all_blocks_sync();             // the barriers are ready before any remote store
     else __syncthreads();
 
-    const uint32_t bytes = uint32_t(mine) * 16;
-    auto load = [&](int64_t i) {                          // row i of this group, by its thread 0
+    auto load = [&](int i, int s) {                        // row i of this group into stage s, by its thread 0
         const int64_t row = first + i * step;
-        const uint32_t bar = smem_u32(&full[group][i % sh.stages]), dst = ring + uint32_t(i % sh.stages) * stage_bytes;
+        const uint32_t bar = smem_u32(&full[group][s]), dst = ring + uint32_t(s) * stage_bytes;
         mbar_arrive_expect_tx(bar, 2 * bytes);
         bulk_load_row(dst, static_cast<const T*>(a.dy) + row * a.ld_dy + int64_t(vec0) * V::kN, bytes, bar);
         bulk_load_row(dst + stage_bytes / 2, static_cast<const T*>(a.x) + row * a.ld_x + int64_t(vec0) * V::kN, bytes, bar);
     };
     if (t == 0)
-        for (int64_t i = 0; i < sh.stages && i < n_mine; ++i) load(i);
+        for (int i = 0; i < sh.stages && i < n_mine; ++i) load(i, i);
 
+    // (threads past the row's end work on its first vector with zeros in dy and
+    // gamma, so that nothing below branches; only their stores are left out)
     uint64_t ga[kV][V::kPairs], dga[kV][V::kPairs], dbe[kV][V::kPairs];
+    bool live[kV];
+    uint32_t at[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
+        const int j = t + v * sh.group;
+        live[v] = j < mine;
+        at[v] = ring + 16u * uint32_t(live[v] ? j : 0);
         ParamVec<T, kP32> w;
-        const bool live = t + v * sh.group < mine;
-        if (live) w.load(a.gamma, vec0 + t + v * sh.group);
+        w.load(a.gamma, vec0 + (live[v] ? j : 0));
 #pragma unroll
         for (int k = 0; k < V::kPairs; ++k) {
-            ga[v][k] = live ? w.pair(k) : 0;
+            ga[v][k] = live[v] ? w.pair(k) : 0;
             dga[v][k] = dbe[v][k] = 0;
         }
     }
     const float inv_h = 1.0f / float(a.hidden);
-    float mu = 0.0f, rs = 0.0f;
-    if (n_mine > 0) {
-        mu = __ldg(a.mu + first);
-        rs = __ldg(a.rsigma + first);
-    }
-    bool ok = true;
+    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + first * a.ld_dx) + vec0 + t;
+    const int64_t out_step = step * a.ld_dx * int64_t(sizeof(T)) / 16;
+    const float* mu_p = a.mu + first;
+    const float* rs_p = a.rsigma + first;
+    float mu = n_mine > 0 ? __ldg(mu_p) : 0.0f, rs = n_mine > 0 ? __ldg(rs_p) : 0.0f;
+    bool ok = true;                                        // false once a wait gave up: no waits or copies from then on
     int stage = 0;
     uint32_t phase = 0;
-    for (int64_t i = 0; i < n_mine; ++i) {
-        const int64_t row = first + i * step;
-        const uint64_t mu2 = f32x2::both(mu), rs2 = f32x2::both(rs);
-        const float rs_now = rs;
-        if (i + 1 < n_mine) {                            // the next row's statistics, a row ahead
-            mu = __ldg(a.mu + row + step);
-            rs = __ldg(a.rsigma + row + step);
-        }
-        if (ok && !mbar_wait(smem_u32(&full[group][stage]), phase, status)) {
-            ok = false;                                  // gave up: let the copies in flight land
-            if (t == 0)
-                for (int64_t j = i; j < i + sh.stages && j < n_mine; ++j)
-                    mbar_wait(smem_u32(&full[group][j % sh.stages]), uint32_t(j / sh.stages) & 1u, status);
-        }
-        const uint32_t src = ring + uint32_t(stage) * stage_bytes;
-        uint64_t g[kV][V::kPairs], xh[kV][V::kPairs], s1 = 0, s2 = 0;
+    for (int i = 0; i < n_mine; ++i) {
+        const float r = rs;
+        const uint64_t mu2 = f32x2::both(mu), rs2 = f32x2::both(r);
+        ok = ok && mbar_wait(smem_u32(&full[group][stage]), phase, status);
+        uint4 wd[kV], wx[kV];
+        uint64_t s1 = 0, s2 = 0;
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            const int j = t + v * sh.group;
-            if (j < mine) {
-                const uint4 wd = lds128(src + 16 * j), wx = lds128(src + stage_bytes / 2 + 16 * j);
+            wd[v] = lds128(at[v] + uint32_t(stage) * stage_bytes);
+            wx[v] = lds128(at[v] + uint32_t(stage) * stage_bytes + stage_bytes / 2);
+            if (!live[v]) wd[v] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int k = 0; k < V::kPairs; ++k) {
-                    const uint64_t d = V::pair(wd, k);
-                    xh[v][k] = f32x2::mul(f32x2::sub(V::pair(wx, k), mu2), rs2);
-                    g[v][k] = f32x2::mul(d, ga[v][k]);
-                    s1 = f32x2::add(s1, g[v][k]);
-                    s2 = f32x2::fma(g[v][k], xh[v][k], s2);
-                    dga[v][k] = f32x2::fma(d, xh[v][k], dga[v][k]);
-                    dbe[v][k] = f32x2::add(dbe[v][k], d);
-                }
+            for (int k = 0; k < V::kPairs; ++k) {
+                const uint64_t d = V::pair(wd[v], k), xh = f32x2::mul(f32x2::sub(V::pair(wx[v], k), mu2), rs2);
+                const uint64_t g = f32x2::mul(d, ga[v][k]);
+                s1 = f32x2::add(s1, g);
+                s2 = f32x2::fma(g, xh, s2);
+                dga[v][k] = f32x2::fma(d, xh, dga[v][k]);
+                dbe[v][k] = f32x2::add(dbe[v][k], d);
             }
         }
-        // lanes 0..15 add up the first sum, lanes 16..31 the second
-        float c1 = f32x2::lo(s1) + f32x2::hi(s1), c2 = f32x2::lo(s2) + f32x2::hi(s2);
-        float half = (lane < 16 ? c1 : c2) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? c2 : c1, 16);
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) half += __shfl_xor_sync(0xFFFFFFFFu, half, o);
+        mu_p += step;
+        rs_p += step;
+        if (i + 1 < n_mine) {                              // the next row's statistics, a row ahead
+            mu = __ldg(mu_p);
+            rs = __ldg(rs_p);
+        }
+        // the row's sums: over the warp, then over the group's warps (every warp
+        // adds them up, lane = warp).  A parity's slots are read before the next
+        // row's barrier, and written again after it.
+        float total = warp_sum2(f32x2::lo(s1) + f32x2::hi(s1), f32x2::lo(s2) + f32x2::hi(s2), lane);
         if (gwarps > 1) {
-            // (a parity's slots are read before the next row's barrier, and
-            // written again after it)
-            float* part = reinterpret_cast<float*>(warp_part[i & 1][group]);
-            if ((lane & 15) == 0) part[2 * (t >> 5) + (lane >> 4)] = half;
+            float(*part)[2] = &warp_part[i & 1][gwarp0];
+            if (lane % 16 == 0) part[t >> 5][lane / 16] = total;
             group_barrier(1 + group, sh.group);
-            const uint64_t c = sum_slots2(smem_u32(part));
-            c1 = f32x2::lo(c);
-            c2 = f32x2::hi(c);
+            const float2 f = lane < gwarps ? *reinterpret_cast<const float2*>(part[lane]) : make_float2(0.0f, 0.0f);
+            total = warp_sum2(f.x, f.y, lane);
         } else {
-            c1 = __shfl_sync(0xFFFFFFFFu, half, 0);      // (every lane has read the stage)
-            c2 = __shfl_sync(0xFFFFFFFFu, half, 16);
+            __syncwarp();                                  // every lane has read the stage
         }
-        if (t == 0 && ok && i + sh.stages < n_mine) load(i + sh.stages);
-        if constexpr (kCluster) {
-            // every block's sums to every block; block_part[parity] is written for
-            // row i + 2 only by blocks that hold all sums of row i + 1, whose
-            // senders had read those of row i
-            const uint32_t bar = smem_u32(&part_full[i & 1]);
-            if (t == 0) mbar_arrive_expect_tx(bar, 8u * uint32_t(sh.cluster));
-            if (t < sh.cluster)
-                remote_store(remote_smem(smem_u32(&block_part[i & 1][rank]), uint32_t(t)), f32x2::pack(c1, c2),
-                             remote_smem(bar, uint32_t(t)));
-            ok = ok && mbar_wait(bar, uint32_t(i >> 1) & 1u, status);
-            c1 = c2 = 0.0f;
-            for (int r = 0; r < sh.cluster; ++r) {
-                const float2 f = block_part[i & 1][r];
-                c1 += f.x;
-                c2 += f.y;
-            }
-        }
-        if (a.dx) {
-            // dx = rs g - rs c2 xh - rs c1
-            const uint64_t m2 = f32x2::both(-rs_now * (c2 * inv_h)), m1 = f32x2::both(-rs_now * (c1 * inv_h));
-            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.ld_dx) + vec0;
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                const int j = t + v * sh.group;
-                if (j < mine) {
-                    uint64_t o[V::kPairs];
-#pragma unroll
-                    for (int k = 0; k < V::kPairs; ++k) o[k] = f32x2::fma(g[v][k], rs2, f32x2::fma(xh[v][k], m2, m1));
-                    out[j] = V::from_pairs(o);
-                }
-            }
-        }
+        if (t == 0 && ok && i + sh.stages < n_mine) load(i + sh.stages, stage);      // (every warp has read it)
         if (++stage == sh.stages) {
             stage = 0;
             phase ^= 1u;
         }
-    }
-    if (a.dgamma) {
-        // the groups' column sums meet in the ring (every copy has landed and
-        // been read) and are added in group order
-        float* sums = reinterpret_cast<float*>(ring_raw);
-        const int cols = sh.cvec * V::kN;
-        __syncthreads();
+        float c1 = __shfl_sync(0xFFFFFFFFu, total, 0), c2 = __shfl_sync(0xFFFFFFFFu, total, 16);
+        if constexpr (kCluster) {
+            // every block's sums to every block; block_part[parity] is written for
+            // row i + 2 only by blocks that hold all sums of row i + 1, which every
+            // block sent after its barrier of row i + 1, past its reads of row i
+            const uint32_t bar = smem_u32(&joined[i & 1]);
+            if (t == 0) mbar_arrive_expect_tx(bar, 8u * uint32_t(sh.cluster));
+            if (t < sh.cluster)
+                remote_store(remote_smem(smem_u32(&block_part[i & 1][rank][0]), uint32_t(t)), f32x2::pack(c1, c2),
+                             remote_smem(bar, uint32_t(t)));
+            ok = ok && mbar_wait(bar, uint32_t(i >> 1) & 1u, status);
+            c1 = c2 = 0.0f;
+            for (int b = 0; b < sh.cluster; ++b) {
+                c1 += block_part[i & 1][b][0];
+                c2 += block_part[i & 1][b][1];
+            }
+        }
+        if (a.dx) {
+            // dx = rs g - rs c2 xh - rs c1, xh = (x - mu) rs
+            const uint64_t k1 = f32x2::both(-r * (c1 * inv_h)), k2 = f32x2::both(-r * r * (c2 * inv_h));
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            const int j = t + v * sh.group;
-            if (j < mine) {
+            for (int v = 0; v < kV; ++v) {
+                uint64_t o[V::kPairs];
+#pragma unroll
+                for (int k = 0; k < V::kPairs; ++k)
+                    o[k] = f32x2::fma(f32x2::mul(V::pair(wd[v], k), ga[v][k]), rs2,
+                                      f32x2::fma(f32x2::sub(V::pair(wx[v], k), mu2), k2, k1));
+                if (live[v]) out[v * sh.group] = V::from_pairs(o);
+            }
+        }
+        out += out_step;
+    }
+    if (!ok && t == 0)                                     // gave up: let the copies in flight land
+        for (int s = 0; s < sh.stages && s < n_mine; ++s)
+            for (uint32_t q = 0; q < 2; ++q) mbar_wait(smem_u32(&full[group][s]), q, status, 1000000ull);
+    __syncthreads();                                       // (every copy has landed and been read)
+    if (a.dgamma) {
+        // the groups' column sums meet in the ring and are added in group order
+        float* sums = reinterpret_cast<float*>(smem);
+        const int cols = sh.cvec * V::kN;
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            if (live[v]) {
 #pragma unroll
                 for (int k = 0; k < V::kPairs; ++k) {
-                    const int c = j * V::kN + 2 * k;
-                    *reinterpret_cast<uint64_t*>(sums + (2 * group) * cols + c) = dga[v][k];
-                    *reinterpret_cast<uint64_t*>(sums + (2 * group + 1) * cols + c) = dbe[v][k];
+                    const int col = (t + v * sh.group) * V::kN + 2 * k;
+                    *reinterpret_cast<uint64_t*>(sums + (2 * group) * cols + col) = dga[v][k];
+                    *reinterpret_cast<uint64_t*>(sums + (2 * group + 1) * cols + col) = dbe[v][k];
                 }
             }
-        }
         __syncthreads();
-        for (int c = threadIdx.x; c < mine * V::kN; c += blockDim.x) {
+        for (int col = threadIdx.x; col < mine * V::kN; col += blockDim.x) {
             float sg = 0.0f, sb = 0.0f;
             for (int q = 0; q < sh.groups; ++q) {
-                sg += sums[(2 * q) * cols + c];
-                sb += sums[(2 * q + 1) * cols + c];
+                sg += sums[(2 * q) * cols + col];
+                sb += sums[(2 * q + 1) * cols + col];
             }
-            a.partial[(2 * int64_t(unit)) * a.hidden + vec0 * V::kN + c] = sg;
-            a.partial[(2 * int64_t(unit) + 1) * a.hidden + vec0 * V::kN + c] = sb;
+            a.partial[(2 * int64_t(unit)) * a.hidden + vec0 * V::kN + col] = sg;
+            a.partial[(2 * int64_t(unit) + 1) * a.hidden + vec0 * V::kN + col] = sb;
         }
     }
-    if constexpr (kCluster) all_blocks_sync();            // no block leaves while another may still store to it
+    if constexpr (kCluster) all_blocks_sync();             // no block leaves while another may still store to it
 }
 
 // ---------------------------------------------------------------- launches
@@ -631,13 +619,11 @@ cudaError_t forward(const LnArgs& a, cudaStream_t stream) {
     return launch_dependent(ln_forward_kernel<T>, dim3(unsigned(a.rows)), dim3(kRowThreads), stream, a);
 }
 
-template <typename T, bool kP32, int kV, bool kCluster>
-cudaError_t backward_vec_launch(const LnBackwardArgs& a, const LnBwdShape& sh, int sms, unsigned int* status, int* parts,
-                                cudaStream_t stream) {
-    auto kern = ln_backward_vec_kernel<T, kP32, kV, kCluster>;
-    const int ring = sh.groups * sh.stages * sh.cvec * 32, sums = sh.groups * sh.cvec * Vec<T>::kN * 8;
-    const int smem = ring > sums ? ring : sums;
-    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kBwdRingBytes);
+template <typename T, bool kP32, bool kCluster>
+cudaError_t backward_vec_launch(const LnBackwardArgs& a, const LnBwdShape& sh, int smem, int sms, unsigned int* status,
+                                int* parts, cudaStream_t stream) {
+    auto kern = ln_backward_vec_kernel<T, kP32, kCluster>;
+    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kBwdSmem);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.rows + sh.groups - 1) / sh.groups, most = sms / sh.cluster;
     *parts = int(want < most ? want : most);
@@ -660,29 +646,30 @@ cudaError_t backward_vec_launch(const LnBackwardArgs& a, const LnBwdShape& sh, i
 
 template <typename T, bool kP32>
 cudaError_t backward_vec(const LnBackwardArgs& a, int sms, unsigned int* status, int* parts, cudaStream_t stream) {
+    constexpr int kV = kBwdVectors<T>;
     LnBwdShape sh{};
     sh.nvec = int(a.hidden / Vec<T>::kN);
     sh.cluster = 1;
-    while (sh.nvec > 1024 * sh.cluster) sh.cluster *= 2;                   // at most 16 KB of a row per block
+    while (sh.nvec > kV * kBwdThreads * sh.cluster) sh.cluster *= 2;
     sh.cvec = (sh.nvec + sh.cluster - 1) / sh.cluster;
-    const int v = sh.cvec > 32 ? 2 : 1;
-    sh.group = ((sh.cvec + v - 1) / v + 31) / 32 * 32;
-    // as many groups as the block's threads (and named barriers) allow
+    sh.group = ((sh.cvec + kV - 1) / kV + 31) / 32 * 32;
     sh.groups = sh.cluster > 1 ? 1 : kBwdThreads / sh.group;
-    if (sh.groups > kBwdMaxGroups - 1 && sh.group > 32) sh.groups = kBwdMaxGroups - 1;
+    if (sh.groups > kBwdMaxGroups - 1 && sh.group > 32) sh.groups = kBwdMaxGroups - 1;      // (named barriers)
+    if (sh.groups > kBwdMaxGroups) sh.groups = kBwdMaxGroups;
     if (sh.groups > a.rows) sh.groups = int(a.rows);
-    sh.stages = kBwdRingBytes / (sh.groups * sh.cvec * 32);
+    sh.stages = kBwdSmem / (sh.groups * sh.cvec * 32);
     if (sh.stages > kBwdMaxStages) sh.stages = kBwdMaxStages;
-    if (v == 1) return backward_vec_launch<T, kP32, 1, false>(a, sh, sms, status, parts, stream);
-    if (sh.cluster == 1) return backward_vec_launch<T, kP32, 2, false>(a, sh, sms, status, parts, stream);
-    return backward_vec_launch<T, kP32, 2, true>(a, sh, sms, status, parts, stream);
+    const int ring = sh.groups * sh.stages * sh.cvec * 32, sums = sh.groups * sh.cvec * Vec<T>::kN * 8;
+    const int smem = ring > sums ? ring : sums;
+    if (sh.cluster == 1) return backward_vec_launch<T, kP32, false>(a, sh, smem, sms, status, parts, stream);
+    return backward_vec_launch<T, kP32, true>(a, sh, smem, sms, status, parts, stream);
 }
 
 template <typename T>
 cudaError_t backward(const LnBackwardArgs& a, int sms, unsigned int* status, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     const dim3 reduce_grid(unsigned((a.hidden + 31) / 32));
-    if (a.rows > 0 && a.hidden % Vec<T>::kN == 0 && a.hidden / Vec<T>::kN <= 1024 * kBwdMaxCluster &&
+    if (a.rows > 0 && a.hidden % Vec<T>::kN == 0 && a.hidden / Vec<T>::kN <= kBwdVectors<T> * kBwdThreads * kBwdMaxCluster &&
         rows_on16(a.x, a.ld_x, a.rows, sizeof(T)) && rows_on16(a.dy, a.ld_dy, a.rows, sizeof(T)) &&
         rows_on16(a.dx, a.ld_dx, a.rows, sizeof(T)) && on16(a.gamma)) {
         int n = 0;
