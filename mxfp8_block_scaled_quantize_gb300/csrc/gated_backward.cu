@@ -13,13 +13,15 @@
 // the two copies' codes and scales (2 bytes each).
 //   dense:      16-byte loads and stores, a thread per 8 columns.
 //   quantising: the MXFP8 quantiser's decomposition (mx_unit.cuh): units of 64
-//               rows x 64 columns of dh, g and u per warp, loaded by TMA; the
-//               warp turns g and u into dg and du in place, in shared memory,
-//               then quantises both tiles; the CTA walks strips of 8 units, so
-//               that a strip's row-wise scale bytes leave as whole words.
+//               rows x 64 columns of dh, g and u per pair of warps, loaded by
+//               TMA; the pair turns g and u into dg and du in place, in shared
+//               memory, then one warp quantises dg and the other du; the CTA
+//               walks strips of 8 units, so that a strip's row-wise scale bytes
+//               leave as whole words.
 #include <cuda_runtime.h>
 
 #include "e4m3.cuh"
+#include "f32x2.cuh"
 #include "mx_unit.cuh"
 #include "ptx.cuh"
 #include "temx_internal.h"
@@ -33,8 +35,9 @@ constexpr int kRows = 64;                    // unit height (two column-wise blo
 constexpr int kCols = 64;                    // unit width in bf16 (= 128-byte swizzle row)
 constexpr int kTileBytes = kRows * kCols * 2;
 constexpr int kUnitBytes = 3 * kTileBytes;   // dh, gate, up
-constexpr int kWarps = 8;                    // = units per strip
-constexpr int kSmemBytes = kWarps * kUnitBytes + 1024;
+constexpr int kUnits = 8;                    // units per strip: 8 x 2 scale bytes = 16 per row
+constexpr int kThreads = kUnits * 64;        // a pair of warps per unit
+constexpr int kSmemBytes = kUnits * kUnitBytes + 1024;
 
 struct GatedBwdParams {
     int64_t rows, F;
@@ -48,49 +51,60 @@ struct GatedBwdParams {
     unsigned int* status;
 };
 
-// act(x) and act'(x).  With s the logistic function of x (SiLU) or of z = 2
-// sqrt(2/pi) (x + 0.044715 x^3) (GELU's tanh form) and t = 1 - s, taken as e s
-// where that does not cancel (e = exp of minus the argument):
-//   act = x s,   act' = s + x s t dz/dx.
-__device__ __forceinline__ void act_and_grad(float x, int act, float& a, float& d) {
+// act(x) and act'(x) of a pair.  With s the logistic function of x (SiLU) or of
+// z = 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU's tanh form):
+//   act = x s,   act' = s (1 + x (1 - s) dz/dx).
+// (1 - s cancels where s is near 1; there act' is near 1 and the term's error
+// is a few units of its last place.)
+__device__ __forceinline__ void act_and_grad2(uint64_t x, int act, uint64_t& a, uint64_t& d) {
+    float x0 = f32x2::lo(x), x1 = f32x2::hi(x);
     if (act == TE_MX_ACT_RELU) {
-        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(a) : "f"(x));
-        d = x > 0.0f ? 1.0f : 0.0f;
+        float a0, a1;
+        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(a0) : "f"(x0));
+        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(a1) : "f"(x1));
+        a = f32x2::pack(a0, a1);
+        d = f32x2::pack(x0 > 0.0f ? 1.0f : 0.0f, x1 > 0.0f ? 1.0f : 0.0f);
         return;
     }
-    constexpr float kLog2e = 1.4426950408889634f;
-    float y = x, slope = 1.0f, z = x;
+    constexpr float kNegLog2e = -1.4426950408889634f, kC = 2.0f * 0.7978845608028654f;
+    uint64_t slope_x = x, t;                               // x dz/dx; -log2(e) z
     if (act == TE_MX_ACT_GELU) {
-        constexpr float kC = 2.0f * 0.7978845608028654f;
         // (beyond +-30 act' is 0 or 1 to fp32; the clamp keeps x^2 finite and NaN a NaN)
-        asm("max.NaN.f32 %0, %1, 0fC1F00000;" : "=f"(y) : "f"(x));
-        asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(y));
-        const float y2 = y * y;
-        z = y * fmaf(y2, kC * 0.044715f, kC);
-        slope = fmaf(y2, kC * 3.0f * 0.044715f, kC);
+        asm("max.NaN.f32 %0, %0, 0fC1F00000;" : "+f"(x0));
+        asm("max.NaN.f32 %0, %0, 0fC1F00000;" : "+f"(x1));
+        asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(x0));
+        asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(x1));
+        const uint64_t y = f32x2::pack(x0, x1), y2 = f32x2::mul(y, y);
+        t = f32x2::mul(y, f32x2::fma(y2, f32x2::both(kNegLog2e * kC * 0.044715f), f32x2::both(kNegLog2e * kC)));
+        slope_x = f32x2::mul(y, f32x2::fma(y2, f32x2::both(kC * 3.0f * 0.044715f), f32x2::both(kC)));
+    } else {
+        t = f32x2::mul(x, f32x2::both(kNegLog2e));
     }
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kLog2e * z));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-    const float t = e > 1.0f ? 1.0f - s : e * s;
-    a = x * s;
-    d = s * fmaf(y * slope, t, 1.0f);
+    float e0, e1, s0, s1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(f32x2::lo(t)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(f32x2::hi(t)));
+    const uint64_t one = f32x2::both(1.0f), q = f32x2::add(f32x2::pack(e0, e1), one);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(f32x2::lo(q)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(f32x2::hi(q)));
+    const uint64_t s = f32x2::pack(s0, s1);
+    a = f32x2::mul(x, s);
+    d = f32x2::mul(s, f32x2::fma(slope_x, f32x2::sub(one, s), one));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f32x2::hi(v)), "f"(f32x2::lo(v)));
     return r;
 }
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t w) { return f32x2::pack(bf16_lo(w), bf16_hi(w)); }
 
 // Two elements (a word each of dh, gate and up) -> gate becomes dg, up du.
 __device__ __forceinline__ void dgate2(uint32_t dh, uint32_t& gate, uint32_t& up, int act) {
-    float a0, d0, a1, d1;
-    act_and_grad(bf16_lo(gate), act, a0, d0);
-    act_and_grad(bf16_hi(gate), act, a1, d1);
-    const float h0 = bf16_lo(dh), h1 = bf16_hi(dh);
-    gate = pack_bf16(h0 * bf16_lo(up) * d0, h1 * bf16_hi(up) * d1);
-    up = pack_bf16(h0 * a0, h1 * a1);
+    uint64_t a, d;
+    act_and_grad2(bf16_pair(gate), act, a, d);
+    const uint64_t h = bf16_pair(dh);
+    gate = pack_bf16(f32x2::mul(f32x2::mul(h, bf16_pair(up)), d));
+    up = pack_bf16(f32x2::mul(h, a));
 }
 
 __device__ __forceinline__ void dgate8(const uint4& dh, uint4& gate, uint4& up, int act) {
@@ -128,53 +142,65 @@ gated_backward_kernel(const GatedBackwardArgs a) {
 // ---------------------------------------------------------------- quantising
 
 template <bool kDense, bool kRowwise, bool kColwise>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const __grid_constant__ CUtensorMap gu_map,
                                const __grid_constant__ CUtensorMap d_map, const __grid_constant__ CUtensorMap qrow_map,
                                const __grid_constant__ CUtensorMap qcol_map, const GatedBwdParams p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[kWarps];
+    __shared__ __align__(8) uint64_t bars[kUnits];
     // row-wise scale bytes of a strip (gate, up) x 64 rows x 16 bytes, double-buffered by round
     __shared__ __align__(16) uint8_t row_scales[2][2][kRows][16];
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pair = warp >> 1, half = warp & 1;             // the pair's unit of a strip; gate or up
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t strips_per_band = (p.col_units + kWarps - 1) / kWarps;
+    const int64_t strips_per_band = (p.col_units + kUnits - 1) / kUnits;
     const int64_t n_strips = p.bands * strips_per_band;
     if (int64_t(blockIdx.x) >= n_strips) return;                         // (uniform over the CTA)
     const int64_t n_mine = (n_strips - blockIdx.x + gridDim.x - 1) / gridDim.x;
-    const uint32_t unit = smem_u32(smem + warp * kUnitBytes);
+    const uint32_t unit = smem_u32(smem + pair * kUnitBytes), tile = unit + (1 + half) * kTileBytes;
     const UnitWalk walk(gridDim.x, strips_per_band);
     int32_t band, strip;
     walk.start(blockIdx.x, band, strip);
-    int32_t lband = band, lstrip = strip;                                // of the next load (lane 0)
-    const uint32_t bar = smem_u32(&bars[warp]);
-    auto unit_col = [&](int32_t st) { return st * kWarps + warp; };
-    auto load = [&](int32_t b, int32_t st) {
+    int32_t next_band = band, next_strip = strip;
+    const uint32_t bar = smem_u32(&bars[pair]);              // three arrivals: dh (the even warp), gate, up (each its own)
+    auto unit_col = [&](int32_t st) { return st * kUnits + pair; };
+    // lane 0: load dh, or this warp's half of [gate | up], of the strip (b, st)
+    // (past the rows' end: zeros; past the band's end: the arrival alone)
+    auto load_dh = [&](int32_t b, int32_t st) {
         if (unit_col(st) < p.col_units) {
-            const int32_t x = unit_col(st) * kCols, y = b * kRows;       // (past the rows' end: zeros)
-            mbar_arrive_expect_tx(bar, kUnitBytes);
-            tma_load_2d(unit, &dh_map, bar, x, y);
-            tma_load_3d(unit + kTileBytes, &gu_map, bar, x, 0, y);
-            tma_load_3d(unit + 2 * kTileBytes, &gu_map, bar, x, 1, y);
+            mbar_arrive_expect_tx(bar, kTileBytes);
+            tma_load_2d(unit, &dh_map, bar, unit_col(st) * kCols, b * kRows);
         } else {
             mbar_arrive(bar);
         }
     };
-    if (lane == 0) {
-        mbar_init(bar, 1);
+    auto load_half = [&](int32_t b, int32_t st) {
+        if (unit_col(st) < p.col_units) {
+            mbar_arrive_expect_tx(bar, kTileBytes);
+            tma_load_3d(tile, &gu_map, bar, unit_col(st) * kCols, half, b * kRows);
+        } else {
+            mbar_arrive(bar);
+        }
+    };
+    if (lane == 0 && half == 0) {
+        mbar_init(bar, 3);
         fence_mbarrier_init();
-        load(lband, lstrip);
-        walk.step(lband, lstrip);
+    }
+    named_barrier_sync(1 + pair, 64);
+    if (lane == 0) {
+        if (half == 0) load_dh(band, strip);
+        load_half(band, strip);
     }
     __syncwarp();
 
     bool ok = true;                      // false once a wait gave up: the warp then only keeps the barriers
     for (int64_t i = 0; i < n_mine; ++i) {
         const int32_t col = unit_col(strip);
-        const bool mine = col < p.col_units;
+        const bool mine = col < p.col_units, more = i + 1 < n_mine;
+        walk.step(next_band, next_strip);
         if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(bar, uint32_t(i & 1), p.status))) {
             ok = false;
             if (lane == 0) mbar_wait(bar, uint32_t(i & 1), p.status);   // gave up: let the loads in flight land
@@ -182,100 +208,95 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
         const int64_t r0 = int64_t(band) * kRows, c0 = int64_t(col) * kCols;
         if (ok && mine) {
 #pragma unroll 4
-            for (int k = 0; k < 16; ++k) {                     // (every tile has the same swizzle)
-                const uint32_t off = uint32_t(k * 32 + lane) * 16;
+            for (int k = 0; k < 8; ++k) {                      // (every tile has the same swizzle)
+                const uint32_t off = uint32_t(k * 64 + half * 32 + lane) * 16;
                 uint4 g = lds128(unit + kTileBytes + off), u = lds128(unit + 2 * kTileBytes + off);
                 dgate8(lds128(unit + off), g, u, p.act);
                 sts128(unit + kTileBytes + off, g.x, g.y, g.z, g.w);
                 sts128(unit + 2 * kTileBytes + off, u.x, u.y, u.z, u.w);
             }
             if (kDense) fence_proxy_async_smem();
-            __syncwarp();
+        }
+        named_barrier_sync(1 + pair, 64);         // both tiles of the unit hold the gradient, dh is read
+        if (ok && more && lane == 0 && half == 0) load_dh(next_band, next_strip);
+        if (ok && mine) {
             if (kDense && lane == 0) {
-                if (r0 < p.rows) {
-                    tma_store_3d(&d_map, unit + kTileBytes, int32_t(c0), 0, int32_t(r0));
-                    tma_store_3d(&d_map, unit + 2 * kTileBytes, int32_t(c0), 1, int32_t(r0));
-                }
+                if (r0 < p.rows) tma_store_3d(&d_map, tile, int32_t(c0), half, int32_t(r0));
                 bulk_commit();
             }
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t tile = unit + (1 + half) * kTileBytes;
-                uint32_t cc[2][2][8];             // column codes [half][column 2l / 2l+1][words]
-                uint32_t rc[2][2][8];             // row codes [row l / l+32][block][words]
-                if (kColwise) {
-                    uint32_t s_lo[2], s_hi[2];
-                    float unused = 0.0f;
-                    col_blocks(tile, 0, lane, cc[0][0], cc[0][1], s_lo[0], s_hi[0], unused, unused);
-                    col_blocks(tile, 32, lane, cc[1][0], cc[1][1], s_lo[1], s_hi[1], unused, unused);
-                    const int64_t c = c0 + 2 * lane;
-                    if (c < p.F) {                             // F % 32 == 0: c + 1 valid too
-                        uint8_t* sp = p.s_col + (half * p.F + c) * p.ld_s_col + (r0 >> 5);
-                        st_global_u16(sp, s_lo[0] | (s_lo[1] << 8));
-                        st_global_u16(sp + p.ld_s_col, s_hi[0] | (s_hi[1] << 8));
-                    }
-                }
-                if (kRowwise) {
-#pragma unroll
-                    for (int rr = 0; rr < 2; ++rr) {
-                        uint32_t sb[2];
-                        row_blocks(tile + (lane + 32 * rr) * 128, lane & 7, rc[rr], sb);
-                        sts16(smem_u32(&row_scales[i & 1][half][lane + 32 * rr][2 * warp]), sb[0] | (sb[1] << 8));
-                    }
-                }
-                if (kDense && lane == 0) bulk_wait_read_all();   // the copy out has read the tile
-                __syncwarp();                     // every lane has read the tile: reuse it for the codes
-                if (kRowwise) {
-#pragma unroll
-                    for (int rr = 0; rr < 2; ++rr) {
-                        const int r = lane + 32 * rr;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t* w = rc[rr][c >> 1] + 4 * (c & 1);
-                            sts128(tile + sw64(r, c), w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                }
-                if (kColwise) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                const uint32_t* w = cc[h][j] + 4 * t;
-                                sts128(tile + 4096 + sw64(2 * lane + j, 2 * h + t), w[0], w[1], w[2], w[3]);
-                            }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kRowwise && r0 < p.rows) tma_store_3d(&qrow_map, tile, int32_t(c0), half, int32_t(r0));
-                    if (kColwise) tma_store_3d(&qcol_map, tile + 4096, int32_t(r0), int32_t(c0), half);
-                    bulk_commit();
+            uint32_t cc[2][2][8];                 // column codes [half of the rows][column 2l / 2l+1][words]
+            uint32_t rc[2][2][8];                 // row codes [row l / l+32][block][words]
+            if (kColwise) {
+                uint32_t s_lo[2], s_hi[2];
+                float unused = 0.0f;
+                col_blocks(tile, 0, lane, cc[0][0], cc[0][1], s_lo[0], s_hi[0], unused, unused);
+                col_blocks(tile, 32, lane, cc[1][0], cc[1][1], s_lo[1], s_hi[1], unused, unused);
+                const int64_t c = c0 + 2 * lane;
+                if (c < p.F) {                                 // F % 32 == 0: c + 1 valid too
+                    uint8_t* sp = p.s_col + (half * p.F + c) * p.ld_s_col + (r0 >> 5);
+                    st_global_u16(sp, s_lo[0] | (s_lo[1] << 8));
+                    st_global_u16(sp + p.ld_s_col, s_hi[0] | (s_hi[1] << 8));
                 }
             }
+            if (kRowwise) {
+#pragma unroll
+                for (int rr = 0; rr < 2; ++rr) {
+                    uint32_t sb[2];
+                    row_blocks(tile + (lane + 32 * rr) * 128, lane & 7, rc[rr], sb);
+                    sts16(smem_u32(&row_scales[i & 1][half][lane + 32 * rr][2 * pair]), sb[0] | (sb[1] << 8));
+                }
+            }
+            if (kDense && lane == 0) bulk_wait_read_all();     // the copy out has read the tile
+            __syncwarp();                         // every lane has read the tile: reuse it for the codes
+            if (kRowwise) {
+#pragma unroll
+                for (int rr = 0; rr < 2; ++rr) {
+                    const int r = lane + 32 * rr;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t* w = rc[rr][c >> 1] + 4 * (c & 1);
+                        sts128(tile + sw64(r, c), w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (kColwise) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t* w = cc[h][j] + 4 * t;
+                            sts128(tile + 4096 + sw64(2 * lane + j, 2 * h + t), w[0], w[1], w[2], w[3]);
+                        }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (kRowwise && r0 < p.rows) tma_store_3d(&qrow_map, tile, int32_t(c0), half, int32_t(r0));
+                if (kColwise) tma_store_3d(&qcol_map, tile + 4096, int32_t(r0), int32_t(c0), half);
+                bulk_commit();
+            }
         }
-        if (ok && i + 1 < n_mine && lane == 0) {
-            bulk_wait_read_all();                 // the stores have read the tiles: refill the unit
-            load(lband, lstrip);
-            walk.step(lband, lstrip);
+        if (ok && more && lane == 0) {
+            bulk_wait_read_all();                 // the stores have read the tile: refill it
+            load_half(next_band, next_strip);
         }
         __syncwarp();
         if (kRowwise) {
-            named_barrier_sync(1, kWarps * 32);
+            named_barrier_sync(1 + kUnits, kThreads);
             if (warp < 4) {
                 // the strip's row scales of one half: lane = row; 16 bytes, or single
                 // bytes where the strip is cut by the end of F or the half does not
                 // start on a 16-byte boundary
-                const int half = warp >> 1, rl = (warp & 1) * 32 + lane;
+                const int hs = warp >> 1, rl = (warp & 1) * 32 + lane;
                 const int64_t r = r0 + rl;
-                const int64_t first = int64_t(strip) * kWarps * 2;            // the strip's first scale byte
+                const int64_t first = int64_t(strip) * kUnits * 2;            // the strip's first scale byte
                 const int64_t valid = p.F / 32 - first;                        // scale bytes of the half left
                 if (r < p.rows) {
-                    uint8_t* sp = p.s_row + r * p.ld_s_row + half * (p.F / 32) + first;
-                    const uint4 v = lds128(smem_u32(&row_scales[i & 1][half][rl][0]));
-                    if (valid >= 16 && (half == 0 || p.F % 512 == 0)) {
+                    uint8_t* sp = p.s_row + r * p.ld_s_row + hs * (p.F / 32) + first;
+                    const uint4 v = lds128(smem_u32(&row_scales[i & 1][hs][rl][0]));
+                    if (valid >= 16 && (hs == 0 || p.F % 512 == 0)) {
                         st_global_v4(sp, v.x, v.y, v.z, v.w);
                     } else {
                         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
@@ -286,7 +307,8 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
                 }
             }
         }
-        walk.step(band, strip);
+        band = next_band;
+        strip = next_strip;
     }
     if (lane == 0) bulk_wait_all();
 }
@@ -296,10 +318,10 @@ cudaError_t launch(const CUtensorMap (&m)[5], const GatedBwdParams& p, int sms, 
     auto kern = gated_backward_quantize_kernel<kDense, kRowwise, kColwise>;
     cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int64_t strips = p.bands * ((p.col_units + kWarps - 1) / kWarps);
+    const int64_t strips = p.bands * ((p.col_units + kUnits - 1) / kUnits);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(strips < sms ? strips : sms));
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
