@@ -17,7 +17,9 @@
 //               TMA; the pair turns g and u into dg and du in place, in shared
 //               memory, then one warp quantises dg and the other du; the CTA
 //               walks strips of 8 units, so that a strip's row-wise scale bytes
-//               leave as whole words.
+//               leave as whole words.  Four warps write them a round later, so
+//               that no pair waits for the others and the pairs' loads, arithmetic
+//               and stores overlap.
 #include <cuda_runtime.h>
 
 #include "e4m3.cuh"
@@ -37,6 +39,8 @@ constexpr int kTileBytes = kRows * kCols * 2;
 constexpr int kUnitBytes = 3 * kTileBytes;   // dh, gate, up
 constexpr int kUnits = 8;                    // units per strip: 8 x 2 scale bytes = 16 per row
 constexpr int kThreads = kUnits * 64;        // a pair of warps per unit
+constexpr int kScaleSlots = 4;               // rounds whose row-wise scale bytes may be in use at a time
+constexpr int kScaleWarps = 4;               // warps that write them
 constexpr int kSmemBytes = kUnits * kUnitBytes + 1024;
 
 struct GatedBwdParams {
@@ -148,8 +152,9 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
                                const __grid_constant__ CUtensorMap qcol_map, const GatedBwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kUnits];
-    // row-wise scale bytes of a strip (gate, up) x 64 rows x 16 bytes, double-buffered by round
-    __shared__ __align__(16) uint8_t row_scales[2][2][kRows][16];
+    __shared__ __align__(8) uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
+    // row-wise scale bytes of a strip: (gate, up) x 64 rows x 16 bytes
+    __shared__ __align__(16) uint8_t row_scales[kScaleSlots][2][kRows][16];
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -185,11 +190,14 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
             mbar_arrive(bar);
         }
     };
-    if (lane == 0 && half == 0) {
-        mbar_init(bar, 3);
-        fence_mbarrier_init();
-    }
-    named_barrier_sync(1 + pair, 64);
+    if (lane == 0 && half == 0) mbar_init(bar, 3);
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kScaleSlots; ++k) {
+            mbar_init(smem_u32(&scales_full[k]), kThreads / 32);
+            mbar_init(smem_u32(&scales_empty[k]), kScaleWarps);
+        }
+    if (lane == 0) fence_mbarrier_init();
+    __syncthreads();
     if (lane == 0) {
         if (half == 0) load_dh(band, strip);
         load_half(band, strip);
@@ -197,8 +205,34 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
     __syncwarp();
 
     bool ok = true;                      // false once a wait gave up: the warp then only keeps the barriers
+    // (warps 0 .. kScaleWarps - 1) write the row-wise scale bytes of round i, of
+    // the strip (b, st): lane = row of one half; 16 bytes, or single bytes where
+    // the strip is cut by the end of F or the half does not start on a 16-byte boundary
+    auto write_scales = [&](int64_t i, int32_t b, int32_t st) {
+        const int slot = int(i % kScaleSlots), hs = warp >> 1, rl = (warp & 1) * 32 + lane;
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&scales_full[slot]), uint32_t(i / kScaleSlots) & 1u, p.status));
+        const int64_t r = int64_t(b) * kRows + rl;
+        const int64_t first = int64_t(st) * kUnits * 2;                // the strip's first scale byte
+        const int64_t valid = p.F / 32 - first;                         // scale bytes of the half left
+        if (ok && r < p.rows) {
+            uint8_t* sp = p.s_row + r * p.ld_s_row + hs * (p.F / 32) + first;
+            const uint4 v = lds128(smem_u32(&row_scales[slot][hs][rl][0]));
+            if (valid >= 16 && (hs == 0 || p.F % 512 == 0)) {
+                st_global_v4(sp, v.x, v.y, v.z, v.w);
+            } else {
+                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (k < valid) st_global_u8(sp + k, (w4[k >> 2] >> (8 * (k & 3))) & 0xFFu);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&scales_empty[slot]));
+    };
+    int32_t last_band = 0, last_strip = 0;
     for (int64_t i = 0; i < n_mine; ++i) {
         const int32_t col = unit_col(strip);
+        const int slot = int(i % kScaleSlots);
         const bool mine = col < p.col_units, more = i + 1 < n_mine;
         walk.step(next_band, next_strip);
         if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(bar, uint32_t(i & 1), p.status))) {
@@ -239,11 +273,14 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
                 }
             }
             if (kRowwise) {
+                if (i >= kScaleSlots)             // the slot's bytes of four rounds ago are written
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&scales_empty[slot]), uint32_t(i / kScaleSlots - 1) & 1u,
+                                                           p.status));
 #pragma unroll
                 for (int rr = 0; rr < 2; ++rr) {
                     uint32_t sb[2];
                     row_blocks(tile + (lane + 32 * rr) * 128, lane & 7, rc[rr], sb);
-                    sts16(smem_u32(&row_scales[i & 1][half][lane + 32 * rr][2 * pair]), sb[0] | (sb[1] << 8));
+                    sts16(smem_u32(&row_scales[slot][half][lane + 32 * rr][2 * pair]), sb[0] | (sb[1] << 8));
                 }
             }
             if (kDense && lane == 0) bulk_wait_read_all();     // the copy out has read the tile
@@ -284,32 +321,15 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
         }
         __syncwarp();
         if (kRowwise) {
-            named_barrier_sync(1 + kUnits, kThreads);
-            if (warp < 4) {
-                // the strip's row scales of one half: lane = row; 16 bytes, or single
-                // bytes where the strip is cut by the end of F or the half does not
-                // start on a 16-byte boundary
-                const int hs = warp >> 1, rl = (warp & 1) * 32 + lane;
-                const int64_t r = r0 + rl;
-                const int64_t first = int64_t(strip) * kUnits * 2;            // the strip's first scale byte
-                const int64_t valid = p.F / 32 - first;                        // scale bytes of the half left
-                if (r < p.rows) {
-                    uint8_t* sp = p.s_row + r * p.ld_s_row + hs * (p.F / 32) + first;
-                    const uint4 v = lds128(smem_u32(&row_scales[i & 1][hs][rl][0]));
-                    if (valid >= 16 && (hs == 0 || p.F % 512 == 0)) {
-                        st_global_v4(sp, v.x, v.y, v.z, v.w);
-                    } else {
-                        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (k < valid) st_global_u8(sp + k, (w4[k >> 2] >> (8 * (k & 3))) & 0xFFu);
-                    }
-                }
-            }
+            if (lane == 0) mbar_arrive(smem_u32(&scales_full[slot]));
+            if (warp < kScaleWarps && i > 0) write_scales(i - 1, last_band, last_strip);
+            last_band = band;
+            last_strip = strip;
         }
         band = next_band;
         strip = next_strip;
     }
+    if (kRowwise && warp < kScaleWarps) write_scales(n_mine - 1, last_band, last_strip);
     if (lane == 0) bulk_wait_all();
 }
 
