@@ -24,6 +24,7 @@
 
 #include "e4m3.cuh"
 #include "f32x2.cuh"
+#include "gated_act.cuh"
 #include "mx_unit.cuh"
 #include "ptx.cuh"
 #include "temx_internal.h"
@@ -55,46 +56,6 @@ struct GatedBwdParams {
     unsigned int* status;
 };
 
-// act(x) and act'(x) of a pair.  With s the logistic function of x (SiLU) or of
-// z = 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU's tanh form):
-//   act = x s,   act' = s (1 + x (1 - s) dz/dx).
-// (1 - s cancels where s is near 1; there act' is near 1 and the term's error
-// is a few units of its last place.)
-__device__ __forceinline__ void act_and_grad2(uint64_t x, int act, uint64_t& a, uint64_t& d) {
-    float x0 = f32x2::lo(x), x1 = f32x2::hi(x);
-    if (act == TE_MX_ACT_RELU) {
-        float a0, a1;
-        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(a0) : "f"(x0));
-        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(a1) : "f"(x1));
-        a = f32x2::pack(a0, a1);
-        d = f32x2::pack(x0 > 0.0f ? 1.0f : 0.0f, x1 > 0.0f ? 1.0f : 0.0f);
-        return;
-    }
-    constexpr float kNegLog2e = -1.4426950408889634f, kC = 2.0f * 0.7978845608028654f;
-    uint64_t slope_x = x, t;                               // x dz/dx; -log2(e) z
-    if (act == TE_MX_ACT_GELU) {
-        // (beyond +-30 act' is 0 or 1 to fp32; the clamp keeps x^2 finite and NaN a NaN)
-        asm("max.NaN.f32 %0, %0, 0fC1F00000;" : "+f"(x0));
-        asm("max.NaN.f32 %0, %0, 0fC1F00000;" : "+f"(x1));
-        asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(x0));
-        asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(x1));
-        const uint64_t y = f32x2::pack(x0, x1), y2 = f32x2::mul(y, y);
-        t = f32x2::mul(y, f32x2::fma(y2, f32x2::both(kNegLog2e * kC * 0.044715f), f32x2::both(kNegLog2e * kC)));
-        slope_x = f32x2::mul(y, f32x2::fma(y2, f32x2::both(kC * 3.0f * 0.044715f), f32x2::both(kC)));
-    } else {
-        t = f32x2::mul(x, f32x2::both(kNegLog2e));
-    }
-    float e0, e1, s0, s1;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(f32x2::lo(t)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(f32x2::hi(t)));
-    const uint64_t one = f32x2::both(1.0f), q = f32x2::add(f32x2::pack(e0, e1), one);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(f32x2::lo(q)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(f32x2::hi(q)));
-    const uint64_t s = f32x2::pack(s0, s1);
-    a = f32x2::mul(x, s);
-    d = f32x2::mul(s, f32x2::fma(slope_x, f32x2::sub(one, s), one));
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f32x2::hi(v)), "f"(f32x2::lo(v)));
@@ -105,7 +66,7 @@ __device__ __forceinline__ uint64_t bf16_pair(uint32_t w) { return f32x2::pack(b
 // Two elements (a word each of dh, gate and up) -> gate becomes dg, up du.
 __device__ __forceinline__ void dgate2(uint32_t dh, uint32_t& gate, uint32_t& up, int act) {
     uint64_t a, d;
-    act_and_grad2(bf16_pair(gate), act, a, d);
+    gated::act_and_grad2(bf16_pair(gate), act, a, d);
     const uint64_t h = bf16_pair(dh);
     gate = pack_bf16(f32x2::mul(f32x2::mul(h, bf16_pair(up)), d));
     up = pack_bf16(f32x2::mul(h, a));

@@ -1,0 +1,406 @@
+// The gated feed-forward GEMM for few tokens (te_mx_gated_gemm with M <= 128):
+// the bytes of the weights are what it costs, so every SM streams them.
+//
+// The operands change places: the weights' rows are the MMA's M = 128 rows (64
+// gate rows and the 64 up rows of the same output columns), the tokens its N
+// columns (M rounded up to 16), so a block reads 16 KB of weights per 128 of K
+// whatever M is, and tiles of 64 output columns give four times as many blocks
+// as the 256-column tiles of gemm.cu.  Where even those leave SMs idle, K is
+// split over a cluster of up to 8 blocks, which add up their accumulators
+// through distributed shared memory in rank order (deterministic).  Two blocks
+// fit on an SM.  Measured: one token, 7168 -> 2 x 18432, 43.3 us (the bytes'
+// floor is 40.1; 56 us in the 256-column tiles); 4096 -> 2 x 1024, 6 us (17 us).
+//
+// One tile per block, 8 warps:
+//   warp 0     TMA producer: weights (128-byte swizzle) and tokens into a ring;
+//   warp 1     TMEM owner and MMA issuer (tcgen05.mma.kind::mxf8f6f4.block_scale);
+//   warp 2     scale factors: a group is 4 K-steps; row-major scale tiles are
+//              turned into the tcgen05 layout in place and copied into TMEM;
+//   warps 4-7  the accumulator's 128 lanes -> shared memory, [token][row] fp32;
+//   all        8 output columns per thread: gate and up summed over the
+//              cluster, bias, activation, product, 16-byte stores.
+// Every mbarrier wait is bounded; a wait that gives up aborts the block cleanly
+// and sets the device status word.
+#include <cuda_runtime.h>
+
+#include "e4m3.cuh"
+#include "f32x2.cuh"
+#include "gated_act.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+#include "temx_internal.h"
+
+namespace temx {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsW = 128;                  // accumulator lanes: 64 gate rows, 64 up rows
+constexpr int kCols = 64;                    // output columns per tile
+constexpr int kK = 128;                      // K per stage (bytes of E4M3)
+constexpr int kWBytes = kRowsW * kK;
+constexpr int kMaxStages = 8;
+constexpr int kSfSlots = 3;                  // scale groups in shared memory, and in TMEM
+constexpr int kSfAhead = 2;                  // groups loaded ahead of the one being prepared
+constexpr int kSfSlotBytes = 2 * kRowsW * 16;        // the weights' 128 rows, then up to 128 tokens' x 16 scale bytes
+constexpr int kSmemBytes = 112 * 1024;       // per block (two per SM)
+constexpr uint32_t kTmemCols = 256;          // accumulator [0, 128), scale factors from 128: 12 K-step slots of 8
+constexpr uint32_t kSfCol0 = 128;
+constexpr int kTilePitch = kRowsW + 4;       // floats per token of the accumulator tile in shared memory
+constexpr int kMaxSplit = 8;
+
+struct TokenParams {
+    int32_t M, F, K;
+    int32_t n;               // M rounded up to 16
+    int32_t k_iters;         // K / 128
+    int32_t split;           // blocks of a cluster, each with its part of K
+    int32_t stages;
+    const uint16_t* bias;    // bf16 [2F] or null
+    uint16_t* D;             // bf16 [M x F]
+    uint16_t* aux;           // bf16 [M x 2F] or null
+    int32_t act;
+    unsigned int* status;
+};
+
+struct __align__(16) TokenShared {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t sf_full[kSfSlots];              // a group's scale bytes landed
+    uint64_t sf_ready[kSfSlots];             // its scale factors are in TMEM
+    uint64_t grp_done[kSfSlots];             // its MMAs completed
+    uint64_t acc_full;                       // every MMA completed
+    uint32_t tmem_base;
+    int32_t abort;
+};
+
+// Bounded mbarrier wait that also returns false once another role aborted.
+__device__ __forceinline__ bool wait_or_abort(const uint64_t& b, uint32_t parity, TokenShared& sh, unsigned int* status) {
+    const uint32_t bar = smem_u32(&b);
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    volatile int32_t* abort_flag = &sh.abort;
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            set_device_status(status, kStatusTimeout);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+// Raw scale rows (row r: 16 bytes = 4 words, word c = the 4 scale bytes of
+// K-step c) of a 128-row atom -> scale-factor layout for tcgen05.cp 32x128b:
+// for K-step c 512 bytes where byte j*16 + i*4 + b is scale byte b of row 32i +
+// j.  In place; the whole warp reads before anyone writes.
+__device__ __forceinline__ void sf_layout(uint32_t sf, int lane) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lds128(sf + (32 * i + lane) * 16);
+    __syncwarp();
+    sts128(sf + 0 * 512 + lane * 16, v[0].x, v[1].x, v[2].x, v[3].x);
+    sts128(sf + 1 * 512 + lane * 16, v[0].y, v[1].y, v[2].y, v[3].y);
+    sts128(sf + 2 * 512 + lane * 16, v[0].z, v[1].z, v[2].z, v[3].z);
+    sts128(sf + 3 * 512 + lane * 16, v[0].w, v[1].w, v[2].w, v[3].w);
+}
+
+// 32 lanes x 16 consecutive 32-bit columns -> 16 registers per thread.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
+// 16 bytes of the same shared-memory variable in block `rank` of the cluster.
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(mapa_shared(addr, rank)) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f32x2::hi(v)), "f"(f32x2::lo(v)));
+    return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+gated_token_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ CUtensorMap map_sw, const __grid_constant__ CUtensorMap map_sx,
+                   const TokenParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TokenShared sh;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.split > 1 ? cluster_ctarank() : 0u;
+    const int32_t f0 = int32_t(blockIdx.x) / p.split * kCols;
+    const uint32_t stage_bytes = uint32_t(kWBytes + p.n * kK);
+    const uint32_t sf_ring = smem_u32(smem) + uint32_t(p.stages) * stage_bytes;
+    // this block's scale groups (4 K-steps each) and K-steps
+    const int32_t groups = (p.k_iters + 3) / 4;
+    const int32_t g0 = int32_t(int64_t(groups) * rank / p.split), g1 = int32_t(int64_t(groups) * (rank + 1) / p.split);
+    const int32_t k0 = 4 * g0, k1 = min(4 * g1, p.k_iters);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int s = 0; s < kSfSlots; ++s) {
+            mbar_init(smem_u32(&sh.sf_full[s]), 1);
+            mbar_init(smem_u32(&sh.sf_ready[s]), 1);
+            mbar_init(smem_u32(&sh.grp_done[s]), 1);
+        }
+        mbar_init(smem_u32(&sh.acc_full), 1);
+        sh.abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_sw);
+        tma_prefetch_desc(&map_sx);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int32_t s = 0;
+            uint32_t phase = 1;                          // (the first pass finds every stage free)
+            for (int32_t k = k0; k < k1; ++k) {
+                if (!wait_or_abort(sh.empty[s], phase, sh, p.status)) break;
+                const uint32_t dst = smem_u32(smem) + uint32_t(s) * stage_bytes, bar = smem_u32(&sh.full[s]);
+                mbar_arrive_expect_tx(bar, stage_bytes);
+                tma_load_2d(dst, &map_w, bar, k * kK, f0);                         // 64 gate rows (the box)
+                tma_load_2d(dst + kWBytes / 2, &map_w, bar, k * kK, p.F + f0);     // 64 up rows
+                tma_load_2d(dst + kWBytes, &map_x, bar, k * kK, 0);
+                if (++s == p.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (sh.abort)                                // gave up: let the loads in flight land
+                for (int i = 0; i < p.stages; ++i)
+                    for (uint32_t q = 0; q < 2; ++q) mbar_wait(smem_u32(&sh.full[i]), q, p.status, 1000000ull);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (the warp together, lane 0 issues)
+        const uint32_t issue = lane == 0 ? 1u : 0u;
+        // kind::mxf8f6f4 with block scaling: E4M3 A and B, both K-major, N >> 3 at
+        // bit 17, UE8M0 scales (bit 23), M >> 4 at bit 24; scale-factor byte ids
+        // at bits 4..5 (B) and 29..30 (A)
+        const uint32_t idesc = (uint32_t(p.n >> 3) << 17) | (1u << 23) | (uint32_t(kRowsW >> 4) << 24);
+        int32_t s = 0, j = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int32_t k = k0; k < k1; ++k) {
+            ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sh.full[s], phase, sh, p.status));
+            if (ok && ((k - k0) & 3) == 0)
+                ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sh.sf_ready[j % kSfSlots], uint32_t(j / kSfSlots) & 1u, sh, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = smem_u32(smem) + uint32_t(s) * stage_bytes;
+            const uint64_t a_desc = smem_desc(st, 16, 1024, 2), b_desc = smem_desc(st + kWBytes, 16, 1024, 2);
+            const uint32_t sf = tmem + kSfCol0 + uint32_t((j % kSfSlots) * 4 + ((k - k0) & 3)) * 8;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)               // (+32 bytes along K = +2 in the address field)
+                mma_mxf8_if(tmem, a_desc + 2 * kk, b_desc + 2 * kk, idesc | (uint32_t(kk) << 4) | (uint32_t(kk) << 29), sf,
+                            sf + 4, (k - k0) | kk ? 1u : 0u, issue);
+            tc_commit_if(smem_u32(&sh.empty[s]), issue);
+            if (((k - k0) & 3) == 3 || k == k1 - 1) {
+                tc_commit_if(smem_u32(&sh.grp_done[j % kSfSlots]), issue);
+                ++j;
+            }
+            if (++s == p.stages) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+        if (ok) tc_commit_if(smem_u32(&sh.acc_full), issue);
+    } else if (warp == 2) {
+        // ------------------------------------------------ scale factors
+        auto load = [&](int32_t j) {                     // group j (of this block), by lane 0
+            const uint32_t bar = smem_u32(&sh.sf_full[j % kSfSlots]), dst = sf_ring + uint32_t(j % kSfSlots) * kSfSlotBytes;
+            mbar_arrive_expect_tx(bar, uint32_t(16 * (kRowsW + p.n)));
+            tma_load_2d(dst, &map_sw, bar, (g0 + j) * 16, f0);
+            tma_load_2d(dst + kCols * 16, &map_sw, bar, (g0 + j) * 16, p.F + f0);
+            tma_load_2d(dst + kRowsW * 16, &map_sx, bar, (g0 + j) * 16, 0);
+        };
+        const int32_t n_groups = g1 - g0;
+        if (lane == 0)
+            for (int32_t j = 0; j < kSfAhead && j < n_groups; ++j) load(j);
+        for (int32_t j = 0; j < n_groups; ++j) {
+            const int32_t slot = j % kSfSlots;
+            const uint32_t bit = uint32_t(j / kSfSlots) & 1u;
+            bool ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sh.sf_full[slot], bit, sh, p.status));
+            if (ok) {
+                const uint32_t sf = sf_ring + uint32_t(slot) * kSfSlotBytes;
+                sf_layout(sf, lane);
+                sf_layout(sf + kRowsW * 16, lane);       // (rows past the tokens: bytes that no MMA reads)
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    // the slot's columns are free once the MMAs of the group before in it completed
+                    if (j >= kSfSlots) ok = wait_or_abort(sh.grp_done[slot], bit ^ 1u, sh, p.status);
+                    if (ok) {
+                        tc_fence_after();
+                        const int32_t steps = min(4, k1 - k0 - 4 * j);
+                        for (int32_t c = 0; c < steps; ++c) {
+                            const uint32_t col = tmem + kSfCol0 + uint32_t(slot * 4 + c) * 8;
+                            tc_cp_32x128b_warpx4(col, smem_desc(sf + c * 512, 0, 128, 0));
+                            tc_cp_32x128b_warpx4(col + 4, smem_desc(sf + kRowsW * 16 + c * 512, 0, 128, 0));
+                        }
+                        tc_commit(smem_u32(&sh.sf_ready[slot]));
+                        // group j + 2 takes the slot of group j - 1, once its copies have landed
+                        if (j + kSfAhead < n_groups) {
+                            if (j > 0) ok = wait_or_abort(sh.sf_ready[(j - 1) % kSfSlots], uint32_t((j - 1) / kSfSlots) & 1u, sh,
+                                                          p.status);
+                            if (ok) load(j + kSfAhead);
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            }
+            if (!ok) break;
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ accumulator -> [token][row] fp32
+        if (__all_sync(0xFFFFFFFFu, wait_or_abort(sh.acc_full, 0, sh, p.status))) {
+            tc_fence_after();
+            const int q = warp & 3;
+            float* tile = reinterpret_cast<float*>(smem) + 32 * q + lane;          // (every stage has been read)
+            for (int32_t c = 0; c < p.n; c += 16) {
+                uint32_t v[16];
+                tmem_ld_x16(tmem + (uint32_t(32 * q) << 16) + uint32_t(c), v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tile[(c + i) * kTilePitch] = __uint_as_float(v[i]);
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (p.split > 1) cluster_sync();                     // every block's partial accumulators are in its shared memory
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    // Items (token, 8 columns), a contiguous part of them per block of the cluster
+    // (neighbouring threads read neighbouring bytes: 128 tokens, 4096 -> 2 x 1024,
+    // 14.9 us; 19.5 us with a token per thread)
+    const int32_t items = p.M * (kCols / 8), i1 = int32_t(int64_t(items) * (rank + 1) / p.split);
+    for (int32_t i = int32_t(int64_t(items) * rank / p.split) + int32_t(threadIdx.x); i < i1; i += kThreads) {
+        const int32_t m = i / (kCols / 8), c = i % (kCols / 8) * 8, f = f0 + c;
+        if (f >= p.F) continue;                          // (F % 16 == 0: 8 columns are in or out together)
+        uint64_t v[2][4];                                // gate, up
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t addr = smem_u32(smem) + uint32_t(m * kTilePitch + half * kCols + c) * 4;
+            float4 a = make_float4(0, 0, 0, 0), b = a;
+            if (p.split == 1) {
+                a = *reinterpret_cast<const float4*>(smem + (addr - smem_u32(smem)));
+                b = *reinterpret_cast<const float4*>(smem + (addr - smem_u32(smem)) + 16);
+            } else {
+                float4 x[kMaxSplit], y[kMaxSplit];       // (every load in flight before the first is added)
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r)
+                    if (r < p.split) {
+                        x[r] = ld_cluster(addr, uint32_t(r));
+                        y[r] = ld_cluster(addr + 16, uint32_t(r));
+                    }
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r)
+                    if (r < p.split) {
+                        a.x += x[r].x; a.y += x[r].y; a.z += x[r].z; a.w += x[r].w;
+                        b.x += y[r].x; b.y += y[r].y; b.z += y[r].z; b.w += y[r].w;
+                    }
+            }
+            v[half][0] = f32x2::pack(a.x, a.y);
+            v[half][1] = f32x2::pack(a.z, a.w);
+            v[half][2] = f32x2::pack(b.x, b.y);
+            v[half][3] = f32x2::pack(b.z, b.w);
+            if (p.bias) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.bias + half * int64_t(p.F) + f));
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[half][k] = f32x2::add(v[half][k], f32x2::pack(bf16_lo(ww[k]), bf16_hi(ww[k])));
+            }
+            if (p.aux)
+                st_global_v4(p.aux + (2 * int64_t(m) + half) * p.F + f, to_bf16x2(v[half][0]), to_bf16x2(v[half][1]),
+                             to_bf16x2(v[half][2]), to_bf16x2(v[half][3]));
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = to_bf16x2(f32x2::mul(gated::act2(v[0][k], p.act), v[1][k]));
+        st_global_v4(p.D + int64_t(m) * p.F + f, o[0], o[1], o[2], o[3]);
+    }
+    if (p.split > 1) cluster_sync();                     // no block leaves while another may still read its shared memory
+}
+
+}  // namespace
+
+te_mx_status gated_token_launch(const GemmArgs& a, cudaStream_t stream) {
+    TokenParams p{};
+    p.M = int32_t(a.M); p.F = int32_t(a.N); p.K = int32_t(a.K);
+    p.n = (p.M + 15) / 16 * 16;
+    p.k_iters = p.K / kK;
+    p.bias = static_cast<const uint16_t*>(a.has_bias ? a.bias : nullptr);
+    p.D = static_cast<uint16_t*>(a.D);
+    p.aux = static_cast<uint16_t*>(a.aux);
+    p.act = a.act;
+    te_mx_status st = device_status_ptr(&p.status);
+    if (st != TE_MX_OK) return st;
+    int sms = 0;
+    if ((st = device_sm_count(&sms)) != TE_MX_OK) return st;
+    // split K while two blocks per SM are not there, down to one scale group
+    // (512 of K) per block
+    const int32_t tiles = (p.F + kCols - 1) / kCols, groups = (p.k_iters + 3) / 4;
+    p.split = 1;
+    while (p.split < kMaxSplit && 2 * p.split <= groups && int64_t(tiles) * 2 * p.split <= 2 * sms) p.split *= 2;
+    const int stage = kWBytes + p.n * kK;
+    p.stages = (kSmemBytes - 1024 - kSfSlots * kSfSlotBytes) / stage;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+
+    // (rows of scales are at least 16 bytes: their pitch is)
+    const uint64_t K = uint64_t(p.K), sf_cols = uint64_t(p.K / 32) < 16 ? 16 : uint64_t(p.K / 32);
+    CUtensorMap mw, mx, msw, msx;
+    if ((st = encode_tensor_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, K, 2 * uint64_t(p.F), K, kK, kCols,
+                                   CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
+    if ((st = encode_tensor_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, K, uint64_t(p.M), K, kK, uint32_t(p.n),
+                                   CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
+    if ((st = encode_tensor_map_2d(&msw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sB, sf_cols, 2 * uint64_t(p.F), uint64_t(a.ld_sB), 16,
+                                   kCols, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
+    if ((st = encode_tensor_map_2d(&msx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sA, sf_cols, uint64_t(p.M), uint64_t(a.ld_sA), 16,
+                                   uint32_t(p.n), CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
+
+    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(gated_token_kernel), kSmemBytes);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(gated token)");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles * p.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(p.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, gated_token_kernel, mw, mx, msw, msx, p), "gated token kernel launch");
+}
+
+}  // namespace temx

@@ -54,6 +54,7 @@
 // and sets the device status word.
 #include <cuda_runtime.h>
 
+#include "gated_act.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 #include "temx_internal.h"
@@ -635,26 +636,9 @@ __device__ __forceinline__ void store_64_staged(uint32_t* acc, const GemmParams&
 
 // ---------------------------------------------------------------- gated epilogue
 
-// act(x) of two gate values.  SiLU is x / (1 + 2^t) with t = -log2(e) x; GELU
-// the same quotient with its own t (gelu_tanh_f2); ReLU keeps NaN.
-__device__ __forceinline__ void gate_act_f2(float& x0, float& x1, int32_t act) {
-    if (act == TE_MX_ACT_GELU) {
-        gelu_tanh_f2(x0, x1);
-    } else if (act == TE_MX_ACT_SILU) {
-        constexpr float kNegLog2e = -1.4426950408889634f;
-        const uint64_t x = f2_pack(x0, x1);
-        float t0, t1, e0, e1, d0, d1, r0, r1;
-        f2_unpack(f2_mul(x, f2_pack(kNegLog2e, kNegLog2e)), t0, t1);
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
-        f2_unpack(f2_add(f2_pack(e0, e1), f2_pack(1.0f, 1.0f)), d0, d1);
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
-        f2_unpack(f2_mul(x, f2_pack(r0, r1)), x0, x1);
-    } else {
-        asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x0));
-        asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x1));
-    }
+// act(gate) * up of two columns.
+__device__ __forceinline__ void gate_f2(float& g0, float& g1, float u0, float u1, int32_t act) {
+    f2_unpack(f2_mul(gated::act2(f2_pack(g0, g1), act), f2_pack(u0, u1)), g0, g1);
 }
 
 // 16 output columns of one row: gate and up accumulators -> bias, [gate | up]
@@ -690,8 +674,8 @@ __device__ __forceinline__ void store_gated_chunk(const uint32_t* gate, const ui
     }
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-        gate_act_f2(v[0][i], v[0][i + 1], p.act);
-        o[i / 2] = pack_bf16x2(v[0][i] * v[1][i], v[0][i + 1] * v[1][i + 1]);
+        gate_f2(v[0][i], v[0][i + 1], v[1][i], v[1][i + 1], p.act);
+        o[i / 2] = pack_bf16x2(v[0][i], v[0][i + 1]);
     }
     uint16_t* d = p.D + row * p.N + n;
     st_global_v4(d, o[0], o[1], o[2], o[3]);
@@ -768,10 +752,7 @@ __device__ __forceinline__ void store_gated_staged(uint32_t* gate, uint32_t* up,
         store(v[1], 1);
     }
 #pragma unroll
-    for (int i = 0; i < 64; i += 2) {
-        gate_act_f2(v[0][i], v[0][i + 1], p.act);
-        f2_unpack(f2_mul(f2_pack(v[0][i], v[0][i + 1]), f2_pack(v[1][i], v[1][i + 1])), v[0][i], v[0][i + 1]);
-    }
+    for (int i = 0; i < 64; i += 2) gate_f2(v[0][i], v[0][i + 1], v[1][i], v[1][i + 1], p.act);
     store(v[0], 2);
 }
 
@@ -1580,6 +1561,7 @@ te_mx_status gemm_launch(const GemmArgs& a, cudaStream_t stream) {
     // are faster even when fewer tiles than pairs exist (a single-CTA split
     // would keep the same number of SMs busy).  FP32 scales: the same rule.
     const bool pair = a.wgrad ? a.M >= 256 : (a.groups > 0 ? a.M >= 256 * 8 : a.M >= 256);
+    if (a.gated && a.groups == 0 && a.M <= kGatedTokenMaxM) return gated_token_launch(a, stream);
     if (a.gated) return pair ? launch_gemm<2, false, false, false, true>(a, sms, status, stream)
                              : launch_gemm<1, false, false, false, true>(a, sms, status, stream);
     if (a.f32_scales) return pair ? launch_gemm<2, false, false, true>(a, sms, status, stream)
