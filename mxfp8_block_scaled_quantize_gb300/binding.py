@@ -352,14 +352,13 @@ def layernorm_quantize(x, gamma, beta, eps: float = 1e-5, rowwise: bool = True, 
     return o
 
 
-_dtype_codes = None
+_dtype_codes: dict = {}
 
 
 def _dtype_code(t) -> int:
-    global _dtype_codes
-    if _dtype_codes is None:
+    if not _dtype_codes:
         import torch
-        _dtype_codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+        _dtype_codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
     return _dtype_codes[t.dtype]
 
 
@@ -376,25 +375,26 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
     gamma and beta (None: no shift) have its type or fp32.  Returns a dict with
     "y" (the type of x) and, with ``stats``, "mu" and "rsigma" (fp32 [rows])
     for ``layernorm_backward``."""
+    import torch
     rows, hidden = x.shape
     assert x.is_cuda and gamma.is_cuda and gamma.shape == (hidden,) and gamma.is_contiguous()
     b = 0
     if beta is not None:
         assert beta.dtype == gamma.dtype and beta.shape == (hidden,) and beta.is_contiguous()
         b = beta.data_ptr()
-    import torch
     o = {} if out is None else dict(out)
-    y = o.get("y")
-    if y is None:
-        y = o["y"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
-    else:
+    if "y" in o:
+        y, ld_y = o["y"], _pitch(o["y"])
         assert y.shape == x.shape and y.dtype == x.dtype
+    else:
+        y, ld_y = torch.empty(rows, hidden, dtype=x.dtype, device=x.device), hidden
+        o["y"] = y
     if stats and "mu" not in o:
         o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
         o["rsigma"] = torch.empty_like(o["mu"])
     mu, rsigma = (o["mu"].data_ptr(), o["rsigma"].data_ptr()) if "mu" in o else (0, 0)
-    te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), b, _dtype_code(gamma), eps,
-                    y.data_ptr(), _pitch(y), mu, rsigma, _stream_ptr(stream))
+    _check(lib().te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), b,
+                                 _dtype_code(gamma), eps, y.data_ptr(), ld_y, mu, rsigma, _stream_ptr(stream)))
     return o
 
 
@@ -410,11 +410,12 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
     assert mu.is_contiguous() and rsigma.is_contiguous() and _dtype_code(mu) == _dtype_code(rsigma) == FP32
     import torch
     o = {} if out is None else dict(out)
-    dx = o.get("dx")
-    if dx is None:
-        dx = o["dx"] = torch.empty(rows, hidden, dtype=x.dtype, device=x.device)
-    else:
+    if "dx" in o:
+        dx, ld_dx = o["dx"], _pitch(o["dx"])
         assert dx.shape == x.shape and dx.dtype == x.dtype
+    else:
+        dx, ld_dx = torch.empty(rows, hidden, dtype=x.dtype, device=x.device), hidden
+        o["dx"] = dx
     if dparams:
         if "dgamma" not in o:
             o["dgamma"], o["dbeta"] = torch.empty_like(gamma), torch.empty_like(gamma)
@@ -422,10 +423,12 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
             need = te_mx_layernorm_backward_workspace_size(rows, hidden)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, _dtype_code(x),
-                             gamma.data_ptr(), _dtype_code(gamma), mu.data_ptr(), rsigma.data_ptr(), dx.data_ptr(),
-                             _pitch(dx), _ptr(o.get("dgamma")), _ptr(o.get("dbeta")), _ptr(workspace),
-                             workspace.numel() if workspace is not None else 0, _stream_ptr(stream))
+    dga, dbe = o.get("dgamma"), o.get("dbeta")
+    ws, size = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (0, 0)
+    _check(lib().te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, _dtype_code(x),
+                                          gamma.data_ptr(), _dtype_code(gamma), mu.data_ptr(), rsigma.data_ptr(),
+                                          dx.data_ptr(), ld_dx, 0 if dga is None else dga.data_ptr(),
+                                          0 if dbe is None else dbe.data_ptr(), ws, size, _stream_ptr(stream)))
     return o
 
 
