@@ -376,23 +376,28 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
     "y" (the type of x) and, with ``stats``, "mu" and "rsigma" (fp32 [rows])
     for ``layernorm_backward``."""
     import torch
-    rows, hidden = x.shape
-    assert x.is_cuda and gamma.is_cuda and gamma.shape == (hidden,) and gamma.is_contiguous()
+    shape = x.shape
+    rows, hidden = shape
+    assert x.is_cuda and gamma.is_cuda and gamma.shape == shape[1:] and gamma.is_contiguous()
     b = 0
     if beta is not None:
-        assert beta.dtype == gamma.dtype and beta.shape == (hidden,) and beta.is_contiguous()
+        assert beta.dtype == gamma.dtype and beta.shape == gamma.shape and beta.is_contiguous()
         b = beta.data_ptr()
-    o = {} if out is None else dict(out)
-    if "y" in o:
-        y, ld_y = o["y"], _pitch(o["y"])
-        assert y.shape == x.shape and y.dtype == x.dtype
+    if out is None:
+        y, ld_y = torch.empty_like(x, memory_format=torch.contiguous_format), hidden
+        o = {"y": y}
     else:
-        y, ld_y = torch.empty(rows, hidden, dtype=x.dtype, device=x.device), hidden
-        o["y"] = y
+        o = dict(out)
+        if "y" not in o:
+            o["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y, ld_y = o["y"], _pitch(o["y"])
+        assert y.shape == shape and y.dtype == x.dtype
+    mu = rsigma = 0
     if stats and "mu" not in o:
         o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
         o["rsigma"] = torch.empty_like(o["mu"])
-    mu, rsigma = (o["mu"].data_ptr(), o["rsigma"].data_ptr()) if "mu" in o else (0, 0)
+    if "mu" in o:
+        mu, rsigma = o["mu"].data_ptr(), o["rsigma"].data_ptr()
     _check(lib().te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), b,
                                  _dtype_code(gamma), eps, y.data_ptr(), ld_y, mu, rsigma, _stream_ptr(stream)))
     return o
@@ -404,31 +409,33 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
     from the forward pass.  Returns a dict with "dx" and, with ``dparams``,
     "dgamma" and "dbeta" (the type of gamma); their scratch is ``workspace``
     (uint8 CUDA tensor) or allocated here."""
-    rows, hidden = x.shape
-    assert x.is_cuda and dy.is_cuda and dy.shape == x.shape and dy.dtype == x.dtype
-    assert gamma.shape == (hidden,) and gamma.is_contiguous() and mu.shape == rsigma.shape == (rows,)
-    assert mu.is_contiguous() and rsigma.is_contiguous() and _dtype_code(mu) == _dtype_code(rsigma) == FP32
     import torch
-    o = {} if out is None else dict(out)
-    if "dx" in o:
-        dx, ld_dx = o["dx"], _pitch(o["dx"])
-        assert dx.shape == x.shape and dx.dtype == x.dtype
+    shape, dt = x.shape, _dtype_code(x)
+    rows, hidden = shape
+    assert x.is_cuda and dy.is_cuda and dy.shape == shape and dy.dtype == x.dtype
+    assert gamma.shape == shape[1:] and gamma.is_contiguous() and mu.shape == rsigma.shape == shape[:1]
+    assert mu.is_contiguous() and rsigma.is_contiguous() and mu.dtype == rsigma.dtype == torch.float32
+    if out is None:
+        dx, ld_dx = torch.empty_like(x, memory_format=torch.contiguous_format), hidden
+        o = {"dx": dx}
     else:
-        dx, ld_dx = torch.empty(rows, hidden, dtype=x.dtype, device=x.device), hidden
-        o["dx"] = dx
-    if dparams:
-        if "dgamma" not in o:
-            o["dgamma"], o["dbeta"] = torch.empty_like(gamma), torch.empty_like(gamma)
+        o = dict(out)
+        if "dx" not in o:
+            o["dx"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+        dx, ld_dx = o["dx"], _pitch(o["dx"])
+        assert dx.shape == shape and dx.dtype == x.dtype
+    dga = dbe = ws = size = 0
+    if dparams and "dgamma" not in o:
+        o["dgamma"], o["dbeta"] = torch.empty_like(gamma), torch.empty_like(gamma)
+    if "dgamma" in o:
+        dga, dbe = o["dgamma"].data_ptr(), _ptr(o.get("dbeta"))
         if workspace is None:
-            need = te_mx_layernorm_backward_workspace_size(rows, hidden)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    dga, dbe = o.get("dgamma"), o.get("dbeta")
-    ws, size = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (0, 0)
-    _check(lib().te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, _dtype_code(x),
+            workspace = torch.empty(lib().te_mx_layernorm_backward_workspace_size(rows, hidden), dtype=torch.uint8,
+                                    device=x.device)
+        ws, size = workspace.data_ptr(), workspace.numel()
+    _check(lib().te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, dt,
                                           gamma.data_ptr(), _dtype_code(gamma), mu.data_ptr(), rsigma.data_ptr(),
-                                          dx.data_ptr(), ld_dx, 0 if dga is None else dga.data_ptr(),
-                                          0 if dbe is None else dbe.data_ptr(), ws, size, _stream_ptr(stream)))
+                                          dx.data_ptr(), ld_dx, dga, dbe, ws, size, _stream_ptr(stream)))
     return o
 
 
