@@ -1561,7 +1561,7 @@ te_mx_status gemm_launch(const GemmArgs& a, cudaStream_t stream) {
     // are faster even when fewer tiles than pairs exist (a single-CTA split
     // would keep the same number of SMs busy).  FP32 scales: the same rule.
     const bool pair = a.wgrad ? a.M >= 256 : (a.groups > 0 ? a.M >= 256 * 8 : a.M >= 256);
-    if (a.gated && a.groups == 0 && a.M <= kGatedTokenMaxM) return gated_token_launch(a, stream);
+    if (split_gemm_takes(a, sms)) return split_gemm_launch(a, sms, stream);
     if (a.gated) return pair ? launch_gemm<2, false, false, false, true>(a, sms, status, stream)
                              : launch_gemm<1, false, false, false, true>(a, sms, status, stream);
     if (a.f32_scales) return pair ? launch_gemm<2, false, false, true>(a, sms, status, stream)

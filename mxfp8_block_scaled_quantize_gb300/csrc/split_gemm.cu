@@ -1,15 +1,20 @@
-// The gated feed-forward GEMM for few tokens (te_mx_gated_gemm with M <= 128):
-// the bytes of the weights are what it costs, so every SM streams them.
+// MXFP8 GEMM for few tokens or few output tiles, plain or gated: where the 256-
+// column tiles of gemm.cu leave SMs idle, and where the bytes of the weights are
+// what the call costs.
 //
-// The operands change places: the weights' rows are the MMA's M = 128 rows (64
-// gate rows and the 64 up rows of the same output columns), the tokens its N
-// columns (M rounded up to 16), so a block reads 16 KB of weights per 128 of K
-// whatever M is, and tiles of 64 output columns give four times as many blocks
-// as the 256-column tiles of gemm.cu.  Where even those leave SMs idle, K is
+// The operands change places: rows of the weights are the MMA's M = 128 rows,
+// tokens its N columns (a block of up to 128, rounded up to 16), so a block
+// reads 16 KB of weights per 128 of K whatever the tokens are, and tiles are 128
+// weight rows each: 128 output columns, or for the gated GEMM the 64 gate rows
+// and the 64 up rows of 64 output columns.  Where even those leave SMs idle, K is
 // split over a cluster of up to 8 blocks, which add up their accumulators
 // through distributed shared memory in rank order (deterministic).  Two blocks
-// fit on an SM.  Measured: one token, 7168 -> 2 x 18432, 43.3 us (the bytes'
-// floor is 40.1; 56 us in the 256-column tiles); 4096 -> 2 x 1024, 6 us (17 us).
+// fit on an SM.  Measured (us; the bytes' floor, here, the tiles of gemm.cu):
+//   gated, 1 token, 7168 -> 2 x 18432       40.1   43.3   56
+//   gated, 1 token, 4096 -> 2 x 1024         1.3    6     17
+//   gated, 300 tokens, 4096 -> 2 x 1024      1.7   13     20
+//   plain, 1 x 7168 x 18432                 20.1   24.4   94
+//   plain, 1000 x 1024 x 8192                2.8   19.3   29.6
 //
 // One tile per block, 8 warps:
 //   warp 0     TMA producer: weights (128-byte swizzle) and tokens into a ring;
@@ -17,8 +22,8 @@
 //   warp 2     scale factors: a group is 4 K-steps; row-major scale tiles are
 //              turned into the tcgen05 layout in place and copied into TMEM;
 //   warps 4-7  the accumulator's 128 lanes -> shared memory, [token][row] fp32;
-//   all        8 output columns per thread: gate and up summed over the
-//              cluster, bias, activation, product, 16-byte stores.
+//   all        8 output columns per thread: summed over the cluster, bias,
+//              activation and product (gated), 16-byte stores.
 // Every mbarrier wait is bounded; a wait that gives up aborts the block cleanly
 // and sets the device status word.
 #include <cuda_runtime.h>
@@ -35,8 +40,9 @@ namespace temx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsW = 128;                  // accumulator lanes: 64 gate rows, 64 up rows
-constexpr int kCols = 64;                    // output columns per tile
+constexpr int kRowsW = 128;                  // weight rows per tile = accumulator lanes
+template <bool kGated> constexpr int kCols = kGated ? kRowsW / 2 : kRowsW;       // output columns per tile
+constexpr int kTokens = 128;                 // tokens per tile, at most
 constexpr int kK = 128;                      // K per stage (bytes of E4M3)
 constexpr int kWBytes = kRowsW * kK;
 constexpr int kMaxStages = 8;
@@ -49,20 +55,21 @@ constexpr uint32_t kSfCol0 = 128;
 constexpr int kTilePitch = kRowsW + 4;       // floats per token of the accumulator tile in shared memory
 constexpr int kMaxSplit = 8;
 
-struct TokenParams {
-    int32_t M, F, K;
-    int32_t n;               // M rounded up to 16
+struct SplitParams {
+    int32_t M, N, K;         // N: output columns (gated: W has 2N rows)
+    int32_t n;               // tokens of a tile, rounded up to 16
+    int32_t n_tiles;         // tiles along N; the tile index goes through them first
     int32_t k_iters;         // K / 128
     int32_t split;           // blocks of a cluster, each with its part of K
     int32_t stages;
-    const uint16_t* bias;    // bf16 [2F] or null
-    uint16_t* D;             // bf16 [M x F]
-    uint16_t* aux;           // bf16 [M x 2F] or null
+    const uint16_t* bias;    // bf16 [N] (gated: [2N]) or null
+    uint16_t* D;             // bf16 [M x N]
+    uint16_t* aux;           // gated: bf16 [M x 2N] or null
     int32_t act;
     unsigned int* status;
 };
 
-struct __align__(16) TokenShared {
+struct __align__(16) SplitShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t sf_full[kSfSlots];              // a group's scale bytes landed
     uint64_t sf_ready[kSfSlots];             // its scale factors are in TMEM
@@ -73,7 +80,7 @@ struct __align__(16) TokenShared {
 };
 
 // Bounded mbarrier wait that also returns false once another role aborted.
-__device__ __forceinline__ bool wait_or_abort(const uint64_t& b, uint32_t parity, TokenShared& sh, unsigned int* status) {
+__device__ __forceinline__ bool wait_or_abort(const uint64_t& b, uint32_t parity, SplitShared& sh, unsigned int* status) {
     const uint32_t bar = smem_u32(&b);
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
@@ -127,16 +134,19 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
     return r;
 }
 
+template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 2)
-gated_token_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                   const __grid_constant__ CUtensorMap map_sw, const __grid_constant__ CUtensorMap map_sx,
-                   const TokenParams p) {
+split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ CUtensorMap map_sw, const __grid_constant__ CUtensorMap map_sx,
+                  const SplitParams p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ TokenShared sh;
+    __shared__ SplitShared sh;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = p.split > 1 ? cluster_ctarank() : 0u;
-    const int32_t f0 = int32_t(blockIdx.x) / p.split * kCols;
+    constexpr int kTileCols = kCols<kGated>;
+    const int32_t tile = int32_t(blockIdx.x) / p.split;
+    const int32_t f0 = tile % p.n_tiles * kTileCols, m0 = tile / p.n_tiles * kTokens;      // first output column, first token
     const uint32_t stage_bytes = uint32_t(kWBytes + p.n * kK);
     const uint32_t sf_ring = smem_u32(smem) + uint32_t(p.stages) * stage_bytes;
     // this block's scale groups (4 K-steps each) and K-steps
@@ -182,9 +192,10 @@ gated_token_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if (!wait_or_abort(sh.empty[s], phase, sh, p.status)) break;
                 const uint32_t dst = smem_u32(smem) + uint32_t(s) * stage_bytes, bar = smem_u32(&sh.full[s]);
                 mbar_arrive_expect_tx(bar, stage_bytes);
-                tma_load_2d(dst, &map_w, bar, k * kK, f0);                         // 64 gate rows (the box)
-                tma_load_2d(dst + kWBytes / 2, &map_w, bar, k * kK, p.F + f0);     // 64 up rows
-                tma_load_2d(dst + kWBytes, &map_x, bar, k * kK, 0);
+                tma_load_2d(dst, &map_w, bar, k * kK, f0);
+                if constexpr (kGated)                    // (the box is 64 rows: gate, then up)
+                    tma_load_2d(dst + kWBytes / 2, &map_w, bar, k * kK, p.N + f0);
+                tma_load_2d(dst + kWBytes, &map_x, bar, k * kK, m0);
                 if (++s == p.stages) {
                     s = 0;
                     phase ^= 1u;
@@ -234,8 +245,8 @@ gated_token_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             const uint32_t bar = smem_u32(&sh.sf_full[j % kSfSlots]), dst = sf_ring + uint32_t(j % kSfSlots) * kSfSlotBytes;
             mbar_arrive_expect_tx(bar, uint32_t(16 * (kRowsW + p.n)));
             tma_load_2d(dst, &map_sw, bar, (g0 + j) * 16, f0);
-            tma_load_2d(dst + kCols * 16, &map_sw, bar, (g0 + j) * 16, p.F + f0);
-            tma_load_2d(dst + kRowsW * 16, &map_sx, bar, (g0 + j) * 16, 0);
+            if constexpr (kGated) tma_load_2d(dst + kRowsW * 8, &map_sw, bar, (g0 + j) * 16, p.N + f0);
+            tma_load_2d(dst + kRowsW * 16, &map_sx, bar, (g0 + j) * 16, m0);
         };
         const int32_t n_groups = g1 - g0;
         if (lane == 0)
@@ -279,13 +290,13 @@ gated_token_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         if (__all_sync(0xFFFFFFFFu, wait_or_abort(sh.acc_full, 0, sh, p.status))) {
             tc_fence_after();
             const int q = warp & 3;
-            float* tile = reinterpret_cast<float*>(smem) + 32 * q + lane;          // (every stage has been read)
+            float* acc = reinterpret_cast<float*>(smem) + 32 * q + lane;           // (every stage has been read)
             for (int32_t c = 0; c < p.n; c += 16) {
                 uint32_t v[16];
                 tmem_ld_x16(tmem + (uint32_t(32 * q) << 16) + uint32_t(c), v);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) tile[(c + i) * kTilePitch] = __uint_as_float(v[i]);
+                for (int i = 0; i < 16; ++i) acc[(c + i) * kTilePitch] = __uint_as_float(v[i]);
             }
             tc_fence_before();
         }
@@ -299,19 +310,21 @@ gated_token_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     // Items (token, 8 columns), a contiguous part of them per block of the cluster
     // (neighbouring threads read neighbouring bytes: 128 tokens, 4096 -> 2 x 1024,
     // 14.9 us; 19.5 us with a token per thread)
-    const int32_t items = p.M * (kCols / 8), i1 = int32_t(int64_t(items) * (rank + 1) / p.split);
+    constexpr int kChunks = kTileCols / 8;
+    const int32_t items = min(kTokens, p.M - m0) * kChunks, i1 = int32_t(int64_t(items) * (rank + 1) / p.split);
     for (int32_t i = int32_t(int64_t(items) * rank / p.split) + int32_t(threadIdx.x); i < i1; i += kThreads) {
-        const int32_t m = i / (kCols / 8), c = i % (kCols / 8) * 8, f = f0 + c;
-        if (f >= p.F) continue;                          // (F % 16 == 0: 8 columns are in or out together)
-        uint64_t v[2][4];                                // gate, up
+        const int32_t m = i / kChunks, c = i % kChunks * 8, f = f0 + c;
+        if (f >= p.N) continue;                          // (N % 16 == 0: 8 columns are in or out together)
+        uint64_t v[kGated ? 2 : 1][4];                   // (gate, up)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint32_t addr = smem_u32(smem) + uint32_t(m * kTilePitch + half * kCols + c) * 4;
+        for (int half = 0; half < (kGated ? 2 : 1); ++half) {
+            const uint32_t off = uint32_t(m * kTilePitch + half * kTileCols + c) * 4;
             float4 a = make_float4(0, 0, 0, 0), b = a;
             if (p.split == 1) {
-                a = *reinterpret_cast<const float4*>(smem + (addr - smem_u32(smem)));
-                b = *reinterpret_cast<const float4*>(smem + (addr - smem_u32(smem)) + 16);
+                a = *reinterpret_cast<const float4*>(smem + off);
+                b = *reinterpret_cast<const float4*>(smem + off + 16);
             } else {
+                const uint32_t addr = smem_u32(smem) + off;
                 float4 x[kMaxSplit], y[kMaxSplit];       // (every load in flight before the first is added)
 #pragma unroll
                 for (int r = 0; r < kMaxSplit; ++r)
@@ -331,29 +344,32 @@ gated_token_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             v[half][2] = f32x2::pack(b.x, b.y);
             v[half][3] = f32x2::pack(b.z, b.w);
             if (p.bias) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.bias + half * int64_t(p.F) + f));
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.bias + half * int64_t(p.N) + f));
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[half][k] = f32x2::add(v[half][k], f32x2::pack(bf16_lo(ww[k]), bf16_hi(ww[k])));
             }
-            if (p.aux)
-                st_global_v4(p.aux + (2 * int64_t(m) + half) * p.F + f, to_bf16x2(v[half][0]), to_bf16x2(v[half][1]),
+            if (kGated && p.aux)
+                st_global_v4(p.aux + (2 * int64_t(m0 + m) + half) * p.N + f, to_bf16x2(v[half][0]), to_bf16x2(v[half][1]),
                              to_bf16x2(v[half][2]), to_bf16x2(v[half][3]));
         }
         uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = to_bf16x2(f32x2::mul(gated::act2(v[0][k], p.act), v[1][k]));
-        st_global_v4(p.D + int64_t(m) * p.F + f, o[0], o[1], o[2], o[3]);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (kGated) v[0][k] = f32x2::mul(gated::act2(v[0][k], p.act), v[1][k]);
+            o[k] = to_bf16x2(v[0][k]);
+        }
+        st_global_v4(p.D + int64_t(m0 + m) * p.N + f, o[0], o[1], o[2], o[3]);
     }
     if (p.split > 1) cluster_sync();                     // no block leaves while another may still read its shared memory
 }
 
-}  // namespace
-
-te_mx_status gated_token_launch(const GemmArgs& a, cudaStream_t stream) {
-    TokenParams p{};
-    p.M = int32_t(a.M); p.F = int32_t(a.N); p.K = int32_t(a.K);
-    p.n = (p.M + 15) / 16 * 16;
+template <bool kGated>
+te_mx_status launch(const GemmArgs& a, int sms, cudaStream_t stream) {
+    SplitParams p{};
+    p.M = int32_t(a.M); p.N = int32_t(a.N); p.K = int32_t(a.K);
+    p.n = p.M < kTokens ? (p.M + 15) / 16 * 16 : kTokens;
+    p.n_tiles = (p.N + kCols<kGated> - 1) / kCols<kGated>;
     p.k_iters = p.K / kK;
     p.bias = static_cast<const uint16_t*>(a.has_bias ? a.bias : nullptr);
     p.D = static_cast<uint16_t*>(a.D);
@@ -361,31 +377,36 @@ te_mx_status gated_token_launch(const GemmArgs& a, cudaStream_t stream) {
     p.act = a.act;
     te_mx_status st = device_status_ptr(&p.status);
     if (st != TE_MX_OK) return st;
-    int sms = 0;
-    if ((st = device_sm_count(&sms)) != TE_MX_OK) return st;
-    // split K while two blocks per SM are not there, down to one scale group
-    // (512 of K) per block
-    const int32_t tiles = (p.F + kCols - 1) / kCols, groups = (p.k_iters + 3) / 4;
+    // Split K while two blocks per SM are not there, down to one scale group (512
+    // of K) per block; with several blocks of tokens, whose accumulators are
+    // whole tiles to add up, at most four ways and past two only up to a block
+    // per SM (512 x 1024 x 4096: 19 us eight ways, 11.7 four ways)
+    const int64_t tiles = int64_t(p.n_tiles) * ((p.M + kTokens - 1) / kTokens), groups = (p.k_iters + 3) / 4;
+    const bool few = p.M <= kTokens;
     p.split = 1;
-    while (p.split < kMaxSplit && 2 * p.split <= groups && int64_t(tiles) * 2 * p.split <= 2 * sms) p.split *= 2;
+    while (p.split < (few ? kMaxSplit : 4) && 2 * p.split <= groups &&
+           tiles * 2 * p.split <= (few || p.split == 1 ? 2 * sms : sms))
+        p.split *= 2;
     const int stage = kWBytes + p.n * kK;
     p.stages = (kSmemBytes - 1024 - kSfSlots * kSfSlotBytes) / stage;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
 
     // (rows of scales are at least 16 bytes: their pitch is)
     const uint64_t K = uint64_t(p.K), sf_cols = uint64_t(p.K / 32) < 16 ? 16 : uint64_t(p.K / 32);
+    const uint64_t w_rows = uint64_t(p.N) * (kGated ? 2 : 1);
     CUtensorMap mw, mx, msw, msx;
-    if ((st = encode_tensor_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, K, 2 * uint64_t(p.F), K, kK, kCols,
+    if ((st = encode_tensor_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, K, w_rows, K, kK, kCols<kGated>,
                                    CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
     if ((st = encode_tensor_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, K, uint64_t(p.M), K, kK, uint32_t(p.n),
                                    CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
-    if ((st = encode_tensor_map_2d(&msw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sB, sf_cols, 2 * uint64_t(p.F), uint64_t(a.ld_sB), 16,
-                                   kCols, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
+    if ((st = encode_tensor_map_2d(&msw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sB, sf_cols, w_rows, uint64_t(a.ld_sB), 16,
+                                   kCols<kGated>, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
     if ((st = encode_tensor_map_2d(&msx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sA, sf_cols, uint64_t(p.M), uint64_t(a.ld_sA), 16,
                                    uint32_t(p.n), CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
 
-    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(gated_token_kernel), kSmemBytes);
-    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(gated token)");
+    auto kern = split_gemm_kernel<kGated>;
+    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kSmemBytes);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(split GEMM)");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(tiles * p.split));
     cfg.blockDim = dim3(kThreads);
@@ -400,7 +421,24 @@ te_mx_status gated_token_launch(const GemmArgs& a, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cuda_status(cudaLaunchKernelEx(&cfg, gated_token_kernel, mw, mx, msw, msx, p), "gated token kernel launch");
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, mw, mx, msw, msx, p), "split GEMM kernel launch");
+}
+
+}  // namespace
+
+bool split_gemm_takes(const GemmArgs& a, int sms) {
+    if (a.groups != 0 || a.wgrad || a.acc_f32 || a.f32_scales || a.gelu || a.dgelu) return false;
+    // (a plain GEMM below 16 K-steps has its sums in one order in gemm.cu, and keeps it)
+    if (!a.gated && a.K < 16 * kK) return false;
+    if (a.M <= kTokens) return true;
+    // more tokens: while the tiles of gemm.cu (256 rows per pair of SMs, or 128
+    // per SM, by 256 accumulator columns) leave half of the SMs idle
+    const int64_t rows = a.M >= 256 ? 256 : 128, units = a.M >= 256 ? sms / 2 : sms, cols = a.gated ? 128 : 256;
+    return 2 * ((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols) <= units;
+}
+
+te_mx_status split_gemm_launch(const GemmArgs& a, int sms, cudaStream_t stream) {
+    return a.gated ? launch<true>(a, sms, stream) : launch<false>(a, sms, stream);
 }
 
 }  // namespace temx

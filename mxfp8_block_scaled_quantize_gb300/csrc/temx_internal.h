@@ -136,8 +136,10 @@ int64_t ln_quantize_max_hidden();
 // s_row / s_col hold fp32 scales (pitches in elements), else E8M0 bytes.
 te_mx_status block_quantize_launch(const QuantizeArgs& a, bool block_2d, bool fp32_scales, cudaStream_t stream);
 te_mx_status gemm_launch(const GemmArgs& a, cudaStream_t stream);
-constexpr int64_t kGatedTokenMaxM = 128;
-te_mx_status gated_token_launch(const GemmArgs& a, cudaStream_t stream);   // gated, dense, M <= kGatedTokenMaxM
+// Dense GEMMs with few tiles, K split over clusters (split_gemm.cu): whether it
+// takes `a`, and its launch.
+bool split_gemm_takes(const GemmArgs& a, int sms);
+te_mx_status split_gemm_launch(const GemmArgs& a, int sms, cudaStream_t stream);
 
 // Helpers implemented in api.cu.
 // Raise a kernel's dynamic shared memory limit to `bytes` on the current
