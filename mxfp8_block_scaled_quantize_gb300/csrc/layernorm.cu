@@ -639,6 +639,152 @@ ln_backward_vec_kernel(const LnBackwardArgs a, const LnBwdShape sh, unsigned int
     if constexpr (kCluster) all_blocks_sync();             // no block leaves while another may still store to it
 }
 
+// Forward, many long rows on 16-byte boundaries: persistent.  Groups of threads
+// take rows in turn, kFwdVectors vectors per thread; rows come through a ring in
+// shared memory, one bulk copy each, and gamma and beta stay in registers.
+// Measured (us; ring, a block per row, floor): 8192 x 7168 bf16 40.9, 48.4, 34.6
+// (a plain copy of the bytes: 38.9); with fp32 parameters 42.2, 57.8; 16384 x
+// 3584 43.9, 52.6.  Rows of 256 vectors: 8192 x 2048 17.0, 15.4, so shorter rows
+// stay with the block per row.
+constexpr int kFwdVectors = 4;
+constexpr int kFwdRingVectors = 384;             // vectors of a row from which the ring is used
+constexpr int kFwdThreads = 512;
+constexpr int kFwdMaxGroups = 16;
+constexpr int kFwdMaxStages = 16;
+constexpr int kFwdSmem = 200 * 1024;
+
+struct LnFwdShape {
+    int nvec;        // vectors of a row
+    int group;       // threads per group
+    int groups;      // groups per block
+    int stages;      // rows of a group's ring
+};
+
+// Sum over the `warps` warps of a group (the same value in each thread, a fixed
+// order); `part`: 16 slots, zero past the warps.
+__device__ __forceinline__ float group_sum(float v, float* part, int warps, int gwarp, int lane, int id, int threads) {
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    if (lane == 0) part[gwarp] = v;
+    group_barrier(id, threads);
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float4 f = *reinterpret_cast<const float4*>(part + 4 * k);
+        s += (f.x + f.y) + (f.z + f.w);
+    }
+    return s;
+}
+
+template <typename T, bool kP32>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+ln_forward_ring_kernel(const LnArgs a, const LnFwdShape sh, unsigned int* status) {
+    using V = Vec<T>;
+    constexpr int kV = kFwdVectors;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[kFwdMaxGroups][kFwdMaxStages];
+    __shared__ __align__(16) float part[2][kFwdMaxGroups][16];         // of the mean, of the squares
+
+    const int group = threadIdx.x / sh.group, t = threadIdx.x % sh.group, lane = threadIdx.x & 31;
+    const int gwarps = sh.group >> 5, gwarp = t >> 5;
+    const uint32_t bytes = uint32_t(sh.nvec) * 16;
+    const uint32_t ring = smem_u32(smem) + uint32_t(group * sh.stages) * bytes;
+    const int64_t first = int64_t(blockIdx.x) * sh.groups + group, step = int64_t(gridDim.x) * sh.groups;
+    const int n_mine = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
+    if (t == 0) {
+        for (int i = 0; i < sh.stages; ++i) mbar_init(smem_u32(&full[group][i]), 1);
+        fence_mbarrier_init();
+    }
+    if (threadIdx.x < kFwdMaxGroups * 16) (&part[0][0][0])[threadIdx.x] = (&part[1][0][0])[threadIdx.x] = 0.0f;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    __syncthreads();
+    auto load = [&](int i, int s) {                        // row i of this group into stage s, by its thread 0
+        const uint32_t bar = smem_u32(&full[group][s]);
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_load_row(ring + uint32_t(s) * bytes, static_cast<const T*>(a.x) + (first + i * step) * a.ld_x, bytes, bar);
+    };
+    if (t == 0)
+        for (int i = 0; i < sh.stages && i < n_mine; ++i) load(i, i);
+
+    // (threads past the row's end work on its first vector and leave it out of
+    // the sums and the stores)
+    ParamVec<T, kP32> g[kV], b[kV];
+    bool live[kV];
+    uint32_t at[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int j = t + v * sh.group;
+        live[v] = j < sh.nvec;
+        at[v] = ring + 16u * uint32_t(live[v] ? j : 0);
+        g[v].load(a.gamma, live[v] ? j : 0);
+        if (a.beta) b[v].load(a.beta, live[v] ? j : 0);
+        else
+#pragma unroll
+            for (int k = 0; k < ParamVec<T, kP32>::kWords; ++k) b[v].w[k] = make_uint4(0, 0, 0, 0);
+    }
+    const float inv_h = 1.0f / float(a.hidden);
+    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.y) + first * a.ld_y) + t;
+    const int64_t out_step = step * a.ld_y * int64_t(sizeof(T)) / 16;
+    bool ok = true;                                        // false once a wait gave up: no waits or copies from then on
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < n_mine; ++i) {
+        ok = ok && mbar_wait(smem_u32(&full[group][stage]), phase, status);
+        uint4 x[kV];
+        uint64_t s[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            x[v] = lds128(at[v] + uint32_t(stage) * bytes);
+            s[v] = 0;
+#pragma unroll
+            for (int k = 0; k < V::kPairs; ++k) s[v] = f32x2::add(s[v], V::pair(x[v], k));
+            if (!live[v]) s[v] = 0;
+        }
+#pragma unroll
+        for (int v = 1; v < kV; ++v) s[0] = f32x2::add(s[0], s[v]);
+        const float mu = group_sum(f32x2::lo(s[0]) + f32x2::hi(s[0]), part[0][group], gwarps, gwarp, lane, 1 + group, sh.group) * inv_h;
+        if (gwarps == 1) __syncwarp();
+        if (t == 0 && ok && i + sh.stages < n_mine) load(i + sh.stages, stage);      // (every warp has read the stage)
+        const uint64_t mu2 = f32x2::both(mu);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            s[v] = 0;
+#pragma unroll
+            for (int k = 0; k < V::kPairs; ++k) {
+                const uint64_t d = f32x2::sub(V::pair(x[v], k), mu2);
+                s[v] = f32x2::fma(d, d, s[v]);
+            }
+            if (!live[v]) s[v] = 0;
+        }
+#pragma unroll
+        for (int v = 1; v < kV; ++v) s[0] = f32x2::add(s[0], s[v]);
+        const float var = group_sum(f32x2::lo(s[0]) + f32x2::hi(s[0]), part[1][group], gwarps, gwarp, lane, 1 + group, sh.group) * inv_h;
+        const float rs = 1.0f / sqrtf(var + a.eps);
+        const uint64_t rs2 = f32x2::both(rs);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            uint64_t o[V::kPairs];
+#pragma unroll
+            for (int k = 0; k < V::kPairs; ++k)
+                o[k] = f32x2::fma(f32x2::mul(f32x2::sub(V::pair(x[v], k), mu2), rs2), g[v].pair(k), b[v].pair(k));
+            if (live[v]) out[v * sh.group] = V::from_pairs(o);
+        }
+        out += out_step;
+        if (t == 0 && a.mu) {
+            a.mu[first + i * step] = mu;
+            a.rsigma[first + i * step] = rs;
+        }
+        if (++stage == sh.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (!ok && t == 0)                                     // gave up: let the copies in flight land
+        for (int q = 0; q < sh.stages && q < n_mine; ++q)
+            for (uint32_t p = 0; p < 2; ++p) mbar_wait(smem_u32(&full[group][q]), p, status, 1000000ull);
+}
+
 // ---------------------------------------------------------------- launches
 
 // Launch with programmatic stream serialisation: the blocks may start while
@@ -668,8 +814,37 @@ bool rows_on16(const void* p, int64_t ld, int64_t rows, size_t size) {
 }
 
 template <typename T, bool kP32>
-cudaError_t forward_vec(const LnArgs& a, cudaStream_t stream) {
+cudaError_t forward_ring(const LnArgs& a, const LnFwdShape& sh, int sms, unsigned int* status, cudaStream_t stream) {
+    auto kern = ln_forward_ring_kernel<T, kP32>;
+    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kFwdSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t want = (a.rows + sh.groups - 1) / sh.groups;
+    cfg.gridDim = dim3(unsigned(want < sms ? want : sms));
+    cfg.blockDim = dim3(unsigned(sh.group * sh.groups));
+    cfg.dynamicSmemBytes = size_t(sh.groups * sh.stages * sh.nvec * 16);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, sh, status);
+}
+
+template <typename T, bool kP32>
+cudaError_t forward_vec(const LnArgs& a, int sms, unsigned int* status, cudaStream_t stream) {
     const int nvec = int(a.hidden / Vec<T>::kN);
+    LnFwdShape sh{};
+    sh.nvec = nvec;
+    constexpr int kV = kFwdVectors;
+    sh.group = ((nvec + kV - 1) / kV + 31) / 32 * 32;
+    if (sh.group <= kFwdThreads && nvec >= kFwdRingVectors) {
+        sh.groups = kFwdThreads / sh.group;
+        sh.stages = kFwdSmem / (sh.groups * nvec * 16);
+        if (sh.stages > kFwdMaxStages) sh.stages = kFwdMaxStages;
+        if (a.rows >= 2 * int64_t(sms) * sh.groups) return forward_ring<T, kP32>(a, sh, sms, status, stream);
+    }
     // Threads per row: one vector per thread while there are too few rows to
     // fill the GPU with smaller blocks, else up to four (eight for rows past
     // 4096 vectors).
@@ -691,13 +866,13 @@ cudaError_t forward_any(const LnArgs& a, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t forward(const LnArgs& a, cudaStream_t stream) {
+cudaError_t forward(const LnArgs& a, int sms, unsigned int* status, cudaStream_t stream) {
     const int64_t nvec = a.hidden / Vec<T>::kN;
     if (a.hidden % Vec<T>::kN == 0 && nvec <= 8192 && rows_on16(a.x, a.ld_x, a.rows, sizeof(T)) &&
         rows_on16(a.y, a.ld_y, a.rows, sizeof(T)) && on16(a.gamma) && on16(a.beta)) {
         if constexpr (sizeof(T) == 2)
-            if (a.param_dtype != TE_MX_FP32) return forward_vec<T, false>(a, stream);
-        return forward_vec<T, true>(a, stream);
+            if (a.param_dtype != TE_MX_FP32) return forward_vec<T, false>(a, sms, status, stream);
+        return forward_vec<T, true>(a, sms, status, stream);
     }
     if (a.param_dtype == a.dtype) return forward_any<T, T>(a, stream);
     return forward_any<T, float>(a, stream);
@@ -793,9 +968,13 @@ cudaError_t backward(const LnBackwardArgs& a, int sms, unsigned int* status, cud
 int ln_backward_parts(int64_t rows) { return int(rows < kLnMaxParts ? rows : kLnMaxParts); }
 
 te_mx_status ln_forward_launch(const LnArgs& a, cudaStream_t stream) {
-    cudaError_t e = a.dtype == TE_MX_FP32   ? forward<float>(a, stream)
-                    : a.dtype == TE_MX_FP16 ? forward<__half>(a, stream)
-                                            : forward<__nv_bfloat16>(a, stream);
+    int sms = 0;
+    unsigned int* status = nullptr;
+    te_mx_status st = device_sm_count(&sms);
+    if (st != TE_MX_OK || (st = device_status_ptr(&status)) != TE_MX_OK) return st;
+    cudaError_t e = a.dtype == TE_MX_FP32   ? forward<float>(a, sms, status, stream)
+                    : a.dtype == TE_MX_FP16 ? forward<__half>(a, sms, status, stream)
+                                            : forward<__nv_bfloat16>(a, sms, status, stream);
     return cuda_status(e, "layernorm kernel launch");
 }
 
