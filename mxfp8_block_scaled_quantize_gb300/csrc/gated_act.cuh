@@ -42,22 +42,35 @@ __device__ __forceinline__ uint64_t gelu_t2(uint64_t x) {
     return f32x2::mul(x, f32x2::fma(f32x2::mul(x, x), f32x2::both(kNegLog2e * kZ3), f32x2::both(kNegLog2e * kZ1)));
 }
 
-__device__ __forceinline__ uint64_t act2(uint64_t x, int act) {
-    if (act == TE_MX_ACT_RELU) return relu2(x);
-    return f32x2::mul(x, logistic2(act == TE_MX_ACT_GELU ? gelu_t2(x) : f32x2::mul(x, f32x2::both(kNegLog2e))));
+// (The activation is a template argument: a branch between the pairs of an
+// unrolled loop would leave each to the latency of its own MUFU chain.  `with`
+// picks it once, outside the loop.)
+template <int kAct>
+__device__ __forceinline__ uint64_t act2(uint64_t x) {
+    if constexpr (kAct == TE_MX_ACT_RELU) return relu2(x);
+    else return f32x2::mul(x, logistic2(kAct == TE_MX_ACT_GELU ? gelu_t2(x) : f32x2::mul(x, f32x2::both(kNegLog2e))));
+}
+
+template <int kAct> struct Act { static constexpr int value = kAct; };
+template <typename F>
+__device__ __forceinline__ void with(int act, F&& f) {
+    if (act == TE_MX_ACT_SILU) f(Act<TE_MX_ACT_SILU>{});
+    else if (act == TE_MX_ACT_GELU) f(Act<TE_MX_ACT_GELU>{});
+    else f(Act<TE_MX_ACT_RELU>{});
 }
 
 // a = act(x), d = act'(x).  (1 - s cancels where s is near 1; there act' is
 // near 1 and the term's error is a few units of its last place.)
-__device__ __forceinline__ void act_and_grad2(uint64_t x, int act, uint64_t& a, uint64_t& d) {
+template <int kAct>
+__device__ __forceinline__ void act_and_grad2(uint64_t x, uint64_t& a, uint64_t& d) {
     float x0 = f32x2::lo(x), x1 = f32x2::hi(x);
-    if (act == TE_MX_ACT_RELU) {
+    if constexpr (kAct == TE_MX_ACT_RELU) {
         a = relu2(x);
         d = f32x2::pack(x0 > 0.0f ? 1.0f : 0.0f, x1 > 0.0f ? 1.0f : 0.0f);
         return;
     }
     uint64_t y = x, slope_y = x;                           // slope_y = y dz/dx
-    if (act == TE_MX_ACT_GELU) {
+    if constexpr (kAct == TE_MX_ACT_GELU) {
         // (beyond +-30 act' is 0 or 1 to fp32; the clamp keeps x^2 finite and NaN a NaN)
         asm("max.NaN.f32 %0, %0, 0fC1F00000;" : "+f"(x0));
         asm("max.NaN.f32 %0, %0, 0fC1F00000;" : "+f"(x1));
@@ -66,7 +79,7 @@ __device__ __forceinline__ void act_and_grad2(uint64_t x, int act, uint64_t& a, 
         y = f32x2::pack(x0, x1);
         slope_y = f32x2::mul(y, f32x2::fma(f32x2::mul(y, y), f32x2::both(3.0f * kZ3), f32x2::both(kZ1)));
     }
-    const uint64_t s = logistic2(act == TE_MX_ACT_GELU ? gelu_t2(y) : f32x2::mul(x, f32x2::both(kNegLog2e)));
+    const uint64_t s = logistic2(kAct == TE_MX_ACT_GELU ? gelu_t2(y) : f32x2::mul(x, f32x2::both(kNegLog2e)));
     const uint64_t one = f32x2::both(1.0f);
     a = f32x2::mul(x, s);
     d = f32x2::mul(s, f32x2::fma(slope_y, f32x2::sub(one, s), one));

@@ -64,19 +64,21 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
 __device__ __forceinline__ uint64_t bf16_pair(uint32_t w) { return f32x2::pack(bf16_lo(w), bf16_hi(w)); }
 
 // Two elements (a word each of dh, gate and up) -> gate becomes dg, up du.
-__device__ __forceinline__ void dgate2(uint32_t dh, uint32_t& gate, uint32_t& up, int act) {
+template <int kAct>
+__device__ __forceinline__ void dgate2(uint32_t dh, uint32_t& gate, uint32_t& up) {
     uint64_t a, d;
-    gated::act_and_grad2(bf16_pair(gate), act, a, d);
+    gated::act_and_grad2<kAct>(bf16_pair(gate), a, d);
     const uint64_t h = bf16_pair(dh);
     gate = pack_bf16(f32x2::mul(f32x2::mul(h, bf16_pair(up)), d));
     up = pack_bf16(f32x2::mul(h, a));
 }
 
-__device__ __forceinline__ void dgate8(const uint4& dh, uint4& gate, uint4& up, int act) {
-    dgate2(dh.x, gate.x, up.x, act);
-    dgate2(dh.y, gate.y, up.y, act);
-    dgate2(dh.z, gate.z, up.z, act);
-    dgate2(dh.w, gate.w, up.w, act);
+template <int kAct>
+__device__ __forceinline__ void dgate8(const uint4& dh, uint4& gate, uint4& up) {
+    dgate2<kAct>(dh.x, gate.x, up.x);
+    dgate2<kAct>(dh.y, gate.y, up.y);
+    dgate2<kAct>(dh.z, gate.z, up.z);
+    dgate2<kAct>(dh.w, gate.w, up.w);
 }
 
 // ---------------------------------------------------------------- dense
@@ -93,15 +95,17 @@ gated_backward_kernel(const GatedBackwardArgs a) {
     if (i >= total) return;
     int32_t row, c;
     walk.start(i, row, c);
-    for (; i < total; i += int64_t(gridDim.x) * kDenseThreads, walk.step(row, c)) {
-        const uint16_t* gu = static_cast<const uint16_t*>(a.gate_up) + row * a.ld_gate_up + 8 * c;
-        const uint4 dh = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dh) + row * a.ld_dh + 8 * c);
-        uint4 g = *reinterpret_cast<const uint4*>(gu), u = *reinterpret_cast<const uint4*>(gu + a.F);
-        dgate8(dh, g, u, a.act);
-        uint16_t* d = static_cast<uint16_t*>(a.d_gate_up) + row * a.ld_d + 8 * c;
-        st_global_v4(d, g.x, g.y, g.z, g.w);
-        st_global_v4(d + a.F, u.x, u.y, u.z, u.w);
-    }
+    gated::with(a.act, [&](auto act) {
+        for (; i < total; i += int64_t(gridDim.x) * kDenseThreads, walk.step(row, c)) {
+            const uint16_t* gu = static_cast<const uint16_t*>(a.gate_up) + row * a.ld_gate_up + 8 * c;
+            const uint4 dh = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dh) + row * a.ld_dh + 8 * c);
+            uint4 g = *reinterpret_cast<const uint4*>(gu), u = *reinterpret_cast<const uint4*>(gu + a.F);
+            dgate8<decltype(act)::value>(dh, g, u);
+            uint16_t* d = static_cast<uint16_t*>(a.d_gate_up) + row * a.ld_d + 8 * c;
+            st_global_v4(d, g.x, g.y, g.z, g.w);
+            st_global_v4(d + a.F, u.x, u.y, u.z, u.w);
+        }
+    });
 }
 
 // ---------------------------------------------------------------- quantising
@@ -202,14 +206,16 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
         }
         const int64_t r0 = int64_t(band) * kRows, c0 = int64_t(col) * kCols;
         if (ok && mine) {
+            gated::with(p.act, [&](auto act) {
 #pragma unroll 4
-            for (int k = 0; k < 8; ++k) {                      // (every tile has the same swizzle)
-                const uint32_t off = uint32_t(k * 64 + half * 32 + lane) * 16;
-                uint4 g = lds128(unit + kTileBytes + off), u = lds128(unit + 2 * kTileBytes + off);
-                dgate8(lds128(unit + off), g, u, p.act);
-                sts128(unit + kTileBytes + off, g.x, g.y, g.z, g.w);
-                sts128(unit + 2 * kTileBytes + off, u.x, u.y, u.z, u.w);
-            }
+                for (int k = 0; k < 8; ++k) {                  // (every tile has the same swizzle)
+                    const uint32_t off = uint32_t(k * 64 + half * 32 + lane) * 16;
+                    uint4 g = lds128(unit + kTileBytes + off), u = lds128(unit + 2 * kTileBytes + off);
+                    dgate8<decltype(act)::value>(lds128(unit + off), g, u);
+                    sts128(unit + kTileBytes + off, g.x, g.y, g.z, g.w);
+                    sts128(unit + 2 * kTileBytes + off, u.x, u.y, u.z, u.w);
+                }
+            });
             if (kDense) fence_proxy_async_smem();
         }
         named_barrier_sync(1 + pair, 64);         // both tiles of the unit hold the gradient, dh is read

@@ -636,9 +636,15 @@ __device__ __forceinline__ void store_64_staged(uint32_t* acc, const GemmParams&
 
 // ---------------------------------------------------------------- gated epilogue
 
-// act(gate) * up of two columns.
-__device__ __forceinline__ void gate_f2(float& g0, float& g1, float u0, float u1, int32_t act) {
-    f2_unpack(f2_mul(gated::act2(f2_pack(g0, g1), act), f2_pack(u0, u1)), g0, g1);
+// gate = act(gate) * up of kN columns.
+template <int kN>
+__device__ __forceinline__ void apply_gate(float* gate, const float* up, int32_t act) {
+    gated::with(act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < kN; i += 2)
+            f2_unpack(f2_mul(gated::act2<decltype(a)::value>(f2_pack(gate[i], gate[i + 1])), f2_pack(up[i], up[i + 1])), gate[i],
+                      gate[i + 1]);
+    });
 }
 
 // 16 output columns of one row: gate and up accumulators -> bias, [gate | up]
@@ -672,11 +678,9 @@ __device__ __forceinline__ void store_gated_chunk(const uint32_t* gate, const ui
             st_global_v4(aux + 8, o[4], o[5], o[6], o[7]);
         }
     }
+    apply_gate<16>(v[0], v[1], p.act);
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        gate_f2(v[0][i], v[0][i + 1], v[1][i], v[1][i + 1], p.act);
-        o[i / 2] = pack_bf16x2(v[0][i], v[0][i + 1]);
-    }
+    for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(v[0][2 * i], v[0][2 * i + 1]);
     uint16_t* d = p.D + row * p.N + n;
     st_global_v4(d, o[0], o[1], o[2], o[3]);
     st_global_v4(d + 8, o[4], o[5], o[6], o[7]);
@@ -751,8 +755,7 @@ __device__ __forceinline__ void store_gated_staged(uint32_t* gate, uint32_t* up,
         store(v[0], 0);
         store(v[1], 1);
     }
-#pragma unroll
-    for (int i = 0; i < 64; i += 2) gate_f2(v[0][i], v[0][i + 1], v[1][i], v[1][i + 1], p.act);
+    apply_gate<64>(v[0], v[1], p.act);
     store(v[0], 2);
 }
 

@@ -353,12 +353,14 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 st_global_v4(p.aux + (2 * int64_t(m0 + m) + half) * p.N + f, to_bf16x2(v[half][0]), to_bf16x2(v[half][1]),
                              to_bf16x2(v[half][2]), to_bf16x2(v[half][3]));
         }
+        if constexpr (kGated)
+            gated::with(p.act, [&](auto act) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[0][k] = f32x2::mul(gated::act2<decltype(act)::value>(v[0][k]), v[1][k]);
+            });
         uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if constexpr (kGated) v[0][k] = f32x2::mul(gated::act2(v[0][k], p.act), v[1][k]);
-            o[k] = to_bf16x2(v[0][k]);
-        }
+        for (int k = 0; k < 4; ++k) o[k] = to_bf16x2(v[0][k]);
         st_global_v4(p.D + int64_t(m0 + m) * p.N + f, o[0], o[1], o[2], o[3]);
     }
     if (p.split > 1) cluster_sync();                     // no block leaves while another may still read its shared memory
