@@ -233,6 +233,14 @@ def _stream_ptr(stream=None) -> int:
     return _raw_stream()
 
 
+def _on(stream):
+    """Context in which what a helper allocates belongs to ``stream`` as its
+    launches do (else a temporary could be given out again, on the current
+    stream, while the kernel still uses it)."""
+    import torch
+    return torch.cuda.stream(stream)
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -375,6 +383,9 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
     gamma and beta (None: no shift) have its type or fp32.  Returns a dict with
     "y" (the type of x) and, with ``stats``, "mu" and "rsigma" (fp32 [rows])
     for ``layernorm_backward``."""
+    if stream is not None:
+        with _on(stream):
+            return layernorm(x, gamma, beta, eps=eps, stats=stats, out=out)
     import torch
     shape = x.shape
     rows, hidden = shape
@@ -399,7 +410,7 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
     if "mu" in o:
         mu, rsigma = o["mu"].data_ptr(), o["rsigma"].data_ptr()
     _check(lib().te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), b,
-                                 _dtype_code(gamma), eps, y.data_ptr(), ld_y, mu, rsigma, _stream_ptr(stream)))
+                                 _dtype_code(gamma), eps, y.data_ptr(), ld_y, mu, rsigma, _stream_ptr()))
     return o
 
 
@@ -409,6 +420,9 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
     from the forward pass.  Returns a dict with "dx" and, with ``dparams``,
     "dgamma" and "dbeta" (the type of gamma); their scratch is ``workspace``
     (uint8 CUDA tensor) or allocated here."""
+    if stream is not None:
+        with _on(stream):
+            return layernorm_backward(dy, x, gamma, mu, rsigma, dparams=dparams, out=out, workspace=workspace)
     import torch
     shape, dt = x.shape, _dtype_code(x)
     rows, hidden = shape
@@ -435,7 +449,7 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
         ws, size = workspace.data_ptr(), workspace.numel()
     _check(lib().te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, dt,
                                           gamma.data_ptr(), _dtype_code(gamma), mu.data_ptr(), rsigma.data_ptr(),
-                                          dx.data_ptr(), ld_dx, dga, dbe, ws, size, _stream_ptr(stream)))
+                                          dx.data_ptr(), ld_dx, dga, dbe, ws, size, _stream_ptr()))
     return o
 
 
@@ -574,6 +588,9 @@ def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = 
     bf16 [2F] or None, activation "silu", "gelu" (tanh form) or "relu".
     Returns (h, pre): h = act(gate) * up in bf16 [M, F], and with ``aux`` the
     pre-activations [gate | up] in bf16 [M, 2F] for ``gated_backward``, else None."""
+    if stream is not None:
+        with _on(stream):
+            return gated_gemm(qx, sx, qw, sw, activation=activation, bias=bias, aux=aux, out=out)
     import torch
     M, K = qx.shape
     F = qw.shape[0] // 2
@@ -584,7 +601,7 @@ def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = 
     else:
         h, pre = out
     te_mx_gated_gemm(qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(), sw.data_ptr(), _pitch(sw), M, F, K,
-                     _ptr(bias), ACTIVATIONS[activation], h.data_ptr(), _ptr(pre), _stream_ptr(stream))
+                     _ptr(bias), ACTIVATIONS[activation], h.data_ptr(), _ptr(pre), _stream_ptr())
     return h, pre
 
 
@@ -594,6 +611,9 @@ def grouped_gated_gemm(group_m, qx, sx, qw, sw, activation: str = "silu", bias=N
     device, qx [total_m, K] (the experts' rows in order), qw [G, 2F, K], sw
     [G*2F, pitch], bias bf16 [G, 2F] or None.  Returns (h [total_m, F], pre
     [total_m, 2F] or None)."""
+    if stream is not None:
+        with _on(stream):
+            return grouped_gated_gemm(group_m, qx, sx, qw, sw, activation=activation, bias=bias, aux=aux, out=out)
     import torch
     total_m, K = qx.shape
     G, N, _ = qw.shape
@@ -606,7 +626,7 @@ def grouped_gated_gemm(group_m, qx, sx, qw, sw, activation: str = "silu", bias=N
     sw2 = sw.reshape(G * N, -1)
     te_mx_grouped_gated_gemm(G, group_m.data_ptr(), total_m, qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(),
                              sw2.data_ptr(), _pitch(sw2), N // 2, K, _ptr(bias), ACTIVATIONS[activation], h.data_ptr(),
-                             _ptr(pre), _stream_ptr(stream))
+                             _ptr(pre), _stream_ptr())
     return h, pre
 
 
@@ -619,6 +639,10 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
     zero-padded to Kp, M rounded up to 128), so that
     dX = gemm(q_row, s_row, W's column-wise copy) and
     dW = gemm(q_col, s_col, X's column-wise copy, padded likewise)."""
+    if stream is not None:
+        with _on(stream):
+            return gated_backward(dh, gate_up, activation=activation, dense=dense, rowwise=rowwise, colwise=colwise,
+                                  out=out)
     import torch
     assert dh.dtype == gate_up.dtype == torch.bfloat16 and dh.dim() == gate_up.dim() == 2 and dh.is_cuda
     M, F = dh.shape
@@ -637,5 +661,5 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
     te_mx_gated_backward(dh.data_ptr(), _pitch(dh), gate_up.data_ptr(), _pitch(gate_up), M, F, ACTIVATIONS[activation],
                          _ptr(o.get("d_gate_up")), ld("d_gate_up"), _ptr(o.get("q_row")), _ptr(o.get("s_row")),
                          ld("s_row"), _ptr(o.get("q_col")), ld("q_col"), _ptr(o.get("s_col")), ld("s_col"),
-                         _stream_ptr(stream))
+                         _stream_ptr())
     return o
