@@ -21,18 +21,15 @@
 //   warp 0      TMA producer: A/B tiles (128-byte swizzle) into a kStages ring
 //               (completion on the MMA CTA's barrier) and, every 4th K-step,
 //               the row-major scale tiles (completion on the CTA's own barrier);
-//   warps 1, 11 MMA issuers (warp 1 also owns TMEM): in the MMA CTA they take
-//               alternate K-steps, one lane issuing 4 block-scaled MMAs
-//               (K = 32 each) per 128-wide K-step and nothing else (a tcgen05
-//               instruction costs ~80-90 issue cycles and blocks while the
-//               tensor pipe is busy, so one issuer waits while the other
-//               issues, and neither has slack for the scale copies); dense
-//               GEMMs of fewer than 16 K-steps and the grouped wgrad use warp
-//               1 alone;
+//   warp 1      TMEM owner and MMA issuer: in the MMA CTA one lane issues 4
+//               block-scaled MMAs (K = 32 each) per 128-wide K-step, tests
+//               the next K-step's barrier and commits (no slack for the scale
+//               copies).  The sums of a tile are thus always added in one order;
 //   warp 10     scale-factor warp: turns each landed scale tile into the
 //               tcgen05 scale-factor layout in place (a 4x4 word transpose),
 //               copies the group's scale factors into TMEM (tcgen05.cp, from the
 //               MMA CTA for a pair) and commits them to the MMA warp;
+//   warp 11     idle (with FP32 scales the second MMA issuer is warp 3);
 //   warps 2..9  epilogue: each takes one 32-lane quarter x 128 columns of its
 //               CTA's 128 x 256 accumulator into registers, releases TMEM at
 //               once (so the next tile's MMAs overlap this tile's epilogue),
@@ -74,7 +71,6 @@ constexpr int kSFABytes = kBM * 16;      // 128 rows x 16 scale bytes (4 K-steps
 constexpr int kSfRing = 3;               // scale-group slots in shared memory
 constexpr int kSfAhead = 2;              // scale groups loaded ahead of the one being prepared
 constexpr int kSfTmemGroups = 4;         // scale groups resident in TMEM
-constexpr int kSplitMinK = 16;           // MXFP8: dense GEMMs of at least this many K-steps use both MMA issuers
 constexpr int kScrBufs = 2;              // FP32 scales: K-step product buffers in TMEM (256 columns each)
 // FP32 scales: registers per thread after the split (warp group 0 / 1 and 2);
 // 4 x 64 + 8 x 216 = 1984 <= 12 x 168, the launch's 168 per thread
@@ -92,7 +88,7 @@ struct Cfg {
     static constexpr int kBBytes = kBRows * kBK;          // 32 or 16 KB
     static constexpr int kStages = kPair == 2 ? 5 : 4;
     static constexpr int kSfWarp = kF32 ? 2 : 10;         // scale-factor warp
-    static constexpr int kMma2Warp = kF32 ? 3 : 11;       // second MMA issuer
+    static constexpr int kMma2Warp = 3;                   // FP32 scales: second MMA issuer
     static constexpr int kEpiWarp0 = kF32 ? 4 : 2;        // first epilogue warp
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kSFBBytes = kBN * 16;            // every CTA holds all of the tile's B rows' scales
@@ -184,7 +180,6 @@ struct __align__(16) SharedState {
     uint64_t grp_done[kSfTmemGroups];      // (MMA CTA) the MMAs of a scale group completed
     uint64_t tmem_full;
     uint64_t tmem_empty;                   // (MMA CTA) accumulator drained by every epilogue warp of the pair
-    uint64_t first_done;                   // (MMA CTA) the MMAs of a tile's first K-step completed
     // FP32-scale mode: K-step kg's product lands in TMEM buffer kg % kScrBufs
     // (columns 256 * buffer ..; the scaled accumulator lives in registers)
     uint64_t scr_full[kScrBufs];           // a product landed (each CTA)
@@ -813,20 +808,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     extern __shared__ uint8_t smem_raw[];
     __shared__ SH sh;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = kPair == 2 ? cluster_ctarank() : 0u;     // 0 = the MMA CTA
+    // (broadcast: the compiler then knows the roles' branches, and what they
+    // compute from these values, to be the same in all lanes of a warp)
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = kPair == 2 ? __shfl_sync(0xFFFFFFFFu, cluster_ctarank(), 0) : 0u;     // 0 = the MMA CTA
     const int64_t unit = kPair == 2 ? blockIdx.x / 2 : blockIdx.x;  // cluster (pair) index
     const int64_t units = kPair == 2 ? gridDim.x / 2 : gridDim.x;
     // Barriers of the MMA CTA as seen from this CTA (cluster addresses for pairs).
     auto leader = [&](const uint64_t& bar) -> uint32_t {
         return kPair == 2 ? mapa_shared(smem_u32(&bar), 0) : smem_u32(&bar);
     };
-    // MXFP8: two MMA issuers for dense GEMMs of at least kSplitMinK K-steps;
-    // otherwise (short K, or the grouped wgrad's per-expert K ranges) warp 1
-    // alone issues and commits, and the barriers count its arrivals only.  The
-    // gated GEMM keeps one issuer: two reorder the fp32 additions from run to
-    // run, and it would gain 1.6 % (8192 x 36864 x 7168: 1506 against 1530 us).
-    const bool two_issuers = !kWgrad && !kGated && p.k_iters >= kSplitMinK;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -838,9 +829,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             mbar_init(smem_u32(&sh.sf_ready[s]), 1);
             mbar_init(smem_u32(&sh.sf_peer[s]), 1);
         }
-        for (int s = 0; s < kSfTmemGroups; ++s) mbar_init(smem_u32(&sh.grp_done[s]), two_issuers ? 2 : 1);
-        mbar_init(smem_u32(&sh.tmem_full), two_issuers ? 2 : 1);
-        mbar_init(smem_u32(&sh.first_done), 1);
+        for (int s = 0; s < kSfTmemGroups; ++s) mbar_init(smem_u32(&sh.grp_done[s]), 1);
+        mbar_init(smem_u32(&sh.tmem_full), 1);
         mbar_init(smem_u32(&sh.tmem_empty), kPair * kEpiWarps);
         if constexpr (kF32) {
             for (int b = 0; b < kScrBufs; ++b) {
@@ -879,8 +869,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     __syncthreads();
     if constexpr (kPair == 2) cluster_sync();      // peer barriers initialised before any remote use
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
-    const int64_t total = p.groups > 0 ? sh.grouped_tiles : p.total_tiles;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
+    const int64_t total = p.groups > 0 ? __shfl_sync(0xFFFFFFFFu, sh.grouped_tiles, 0) : p.total_tiles;
 
     // FP32 scales: MMA issuer for the K-steps of one parity: 4 MMAs (N = 256,
     // K = 32 each) per K-step into product buffer kg % kScrBufs (= the parity),
@@ -933,93 +923,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
     };
 
-    // MXFP8: MMA issuer for the K-steps of one parity of the global K-step
-    // count: 4 block-scaled MMAs (K = 32 each) per 128-wide K-step.  Two
-    // issuers (warps 1 and kMma2Warp) alternate K-steps, so that one waits for
-    // its operands or blocks in a tcgen05.mma issue while the other issues.
-    // MMAs of different threads may run in either order, which only reorders
-    // the fp32 additions, except for a tile's first K-step, which overwrites
-    // the accumulator: the issuer that does not own it waits until its MMAs
-    // completed (first_done) before issuing any of the tile's MMAs.  That
-    // wait costs about one K-step's latency per tile, so only dense GEMMs of
-    // at least kSplitMinK K-steps use two issuers (two_issuers).  Both
-    // issuers wait for the accumulator, each scale group and the operands of
-    // their own K-steps, and both commit every scale group (grp_done) and
-    // every tile (tmem_full), whose barriers count two arrivals.
-    // (run by a whole warp, values warp-uniform; lane 0's tcgen05 operations
-    // are predicated on: about 4 % fewer cycles per K-step than a loop that
-    // lane 0 runs alone)
-    auto mma_mx = [&](uint32_t par) {
-        const uint32_t issue = lane == 0 ? 1u : 0u;
-        uint32_t g = 0, grp = 0;   // global K-step and scale-group counts (both issuers' K-steps)
-        int32_t local = 0;
-        bool ok = true;
-        auto wait = [&](const uint64_t& bar, uint32_t parity) -> bool {
-            // (the lanes decide together: warp-collective tcgen05 operations follow)
-            return __all_sync(0xFFFFFFFFu, wait_or_abort(smem_u32(&bar), parity, sh, p.status));
-        };
-        for (int64_t t = unit; t < total && ok; t += units, ++local) {
-            const int32_t nk = p.k_iters;
-            if (local > 0) {
-                if (!wait(sh.tmem_empty, uint32_t(local - 1) & 1u)) break;
-                tc_fence_after();
-            }
-            if ((g & 1u) != par) {               // the other issuer owns the tile's first K-step
-                if (!wait(sh.first_done, uint32_t(local) & 1u)) break;
-                tc_fence_after();
-            }
-            for (int32_t k = 0; k < nk; ++k, ++g) {
-                const bool mine = (g & 1u) == par;
-                const uint32_t stage = g % C::kStages, phase = (g / C::kStages) & 1u;
-                // (the operands first, then a new scale group's factors, as in
-                // the single-issuer loop)
-                if (mine && !wait(sh.full[stage], phase)) { ok = false; break; }
-                if ((k & 3) == 0) {
-                    if (!wait(sh.sf_ready[grp % kSfRing], (grp / kSfRing) & 1u)) { ok = false; break; }
-                    tc_fence_after();
-                }
-                if (mine) {
-                    uint8_t* st = smem + stage * C::kStageBytes;
-                    const uint32_t sf_col = tmem + kSfCol0 + ((grp % kSfTmemGroups) * 4 + uint32_t(k & 3)) * kSfSlotCols;
-                    const uint64_t a_desc = smem_desc(smem_u32(st), 16, 1024, 2);
-                    const uint64_t b_desc = smem_desc(smem_u32(st + C::kABytes), 16, 1024, 2);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        // +32 bytes along K inside the 128-byte swizzled row = +2 in the address field
-                        const uint32_t idesc = idesc_sf(C::kIdescBase, uint32_t(kk));
-                        const uint32_t acc = (k | kk) != 0 ? 1u : 0u;
-                        if constexpr (kPair == 2)
-                            mma_mxf8_pair_if(tmem, a_desc + 2 * kk, b_desc + 2 * kk, idesc, sf_col, sf_col + 4, acc,
-                                             issue);
-                        else
-                            mma_mxf8_if(tmem, a_desc + 2 * kk, b_desc + 2 * kk, idesc, sf_col, sf_col + 4, acc, issue);
-                    }
-                    if constexpr (kPair == 2) tc_commit_pair_mc_if(smem_u32(&sh.empty[stage]), 0x3, issue);
-                    else tc_commit_if(smem_u32(&sh.empty[stage]), issue);
-                    if (k == 0) {
-                        if constexpr (kPair == 2) tc_commit_pair_mc_if(smem_u32(&sh.first_done), 0x1, issue);
-                        else tc_commit_if(smem_u32(&sh.first_done), issue);
-                    }
-                }
-                if ((k & 3) == 3 || k == nk - 1) {             // last K-step of the scale group
-                    if constexpr (kPair == 2)
-                        tc_commit_pair_mc_if(smem_u32(&sh.grp_done[grp % kSfTmemGroups]), 0x1, issue);
-                    else tc_commit_if(smem_u32(&sh.grp_done[grp % kSfTmemGroups]), issue);
-                    ++grp;
-                }
-            }
-            if (!ok) break;
-            if constexpr (kPair == 2) tc_commit_pair_mc_if(smem_u32(&sh.tmem_full), 0x3, issue);
-            else tc_commit_if(smem_u32(&sh.tmem_full), issue);
-        }
-    };
-
     // Role warps (for FP32 scales warp group 0) and epilogue warps.  With FP32
     // scales the role warp group gives registers to the epilogue warp groups,
     // whose threads hold 128 accumulator columns and a product slice each
     // (the host checked that the split fits); each side changes its count
     // first, before the warps of a group part ways.
-    const bool role_warp = kF32 ? warp < 4 : (warp < 2 || warp == C::kSfWarp || warp == C::kMma2Warp);
+    const bool role_warp = kF32 ? warp < 4 : (warp < 2 || warp >= C::kSfWarp);
     if (role_warp) {
         if constexpr (kF32) regs_lower<kRegsRoles>();
         if (warp == 0) {
@@ -1057,16 +966,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             // ------------------------------------------------ MMA issuer (the MMA CTA)
             if (rank == 0 && kF32) {
                 mma_f32(0u);
-            } else if (rank == 0 && two_issuers) {
-                mma_mx(0u);
             } else if (rank == 0) {
-                // The whole warp runs the loop (its values stay warp-uniform) and
-                // lane 0's tcgen05.mma / tcgen05.commit are predicated on: about 4 %
-                // fewer cycles per K-step than a loop that lane 0 runs alone.
+                // The whole warp runs the loop and lane 0's tcgen05.mma / tcgen05.commit
+                // are predicated on: about 4 % fewer cycles per K-step than a loop
+                // that lane 0 runs alone.  The loop's issue cycles are what the
+                // mainloop can least afford (at 4 MMAs of 128 cycles per K-step):
+                // every value in it comes from a warp-uniform source, and the next
+                // K-step's barrier is tested between this one's MMAs and commits.
+                // Per K-step of 8192 x 36864 x 7168: 362 ns, 374 ns without either
+                // (and the same with two warps that took K-steps in turn, in an
+                // order of additions that changed from run to run).
                 const uint32_t issue = lane == 0 ? 1u : 0u;
                 uint32_t stage = 0, phase = 0, grp = 0;   // grp: global index of the current scale group
                 int32_t local = 0, hint = 0;
-                bool ok = true;
+                bool ok = true, landed = false;
                 for (int64_t t = unit; t < total && ok; t += units, ++local) {
                     // K-steps of this tile (wgrad: the expert's own; 0 for an expert without tokens)
                     int32_t nk = p.k_iters;
@@ -1078,7 +991,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         tc_fence_after();
                     }
                     for (int32_t k = 0; k < nk; ++k) {
-                        if (!__all_sync(0xFFFFFFFFu, wait_or_abort(smem_u32(&sh.full[stage]), phase, sh, p.status))) {
+                        if (!__all_sync(0xFFFFFFFFu, landed) &&
+                            !__all_sync(0xFFFFFFFFu, wait_or_abort(smem_u32(&sh.full[stage]), phase, sh, p.status))) {
                             ok = false;
                             break;
                         }
@@ -1106,6 +1020,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             else
                                 mma_mxf8_if(tmem, a_desc + 2 * kk, b_desc + 2 * kk, idesc, sf_col, sf_col + 4, acc, issue);
                         }
+                        const uint32_t next = stage + 1 == C::kStages ? 0 : stage + 1;
+                        landed = mbar_test(smem_u32(&sh.full[next]), phase ^ (next == 0 ? 1u : 0u));
                         if constexpr (kPair == 2) tc_commit_pair_mc_if(smem_u32(&sh.empty[stage]), 0x3, issue);
                         else tc_commit_if(smem_u32(&sh.empty[stage]), issue);
                         if ((k & 3) == 3 || k == nk - 1) {             // last K-step of the scale group
@@ -1114,19 +1030,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             else tc_commit_if(smem_u32(&sh.grp_done[grp % kSfTmemGroups]), issue);
                             ++grp;
                         }
-                        if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                        stage = next;
+                        if (next == 0) phase ^= 1u;
                     }
                     if (!ok) break;
                     if constexpr (kPair == 2) tc_commit_pair_mc_if(smem_u32(&sh.tmem_full), 0x3, issue);
                     else tc_commit_if(smem_u32(&sh.tmem_full), issue);
                 }
             }
-        } else if (warp == C::kMma2Warp) {
-            if (rank == 0) {
-                if constexpr (kF32) mma_f32(1u);
-                else if (two_issuers) mma_mx(1u);
-            }
-        } else {                                   // the scale-factor warp
+        } else if (kF32 && warp == C::kMma2Warp) {
+            if (rank == 0) mma_f32(1u);
+        } else if (warp == C::kSfWarp) {
             // ------------------------------------------------ scale-factor layout (every CTA)
             // Scale groups (4 K-steps each, the last of a tile possibly shorter)
             // go through a kSfRing-slot ring: lane 0 loads group j + kSfAhead

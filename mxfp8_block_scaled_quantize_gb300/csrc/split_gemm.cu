@@ -12,9 +12,9 @@
 // fit on an SM.  Measured (us; the bytes' floor, here, the tiles of gemm.cu):
 //   gated, 1 token, 7168 -> 2 x 18432       40.1   43.3   56
 //   gated, 1 token, 4096 -> 2 x 1024         1.3    6     17
-//   gated, 300 tokens, 4096 -> 2 x 1024      1.7   13     20
+//   gated, 300 tokens, 4096 -> 2 x 1024      1.7   11.4   20
 //   plain, 1 x 7168 x 18432                 20.1   24.4   94
-//   plain, 1000 x 1024 x 8192                2.8   19.3   29.6
+//   plain, 1000 x 1024 x 8192                2.8   15.7   29.6
 //
 // One tile per block, 8 warps:
 //   warp 0     TMA producer: weights (128-byte swizzle) and tokens into a ring;
@@ -142,8 +142,9 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     __shared__ SplitShared sh;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = p.split > 1 ? cluster_ctarank() : 0u;
+    // (broadcast: the compiler then knows them to be the same in all lanes)
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = __shfl_sync(0xFFFFFFFFu, p.split > 1 ? cluster_ctarank() : 0u, 0);
     constexpr int kTileCols = kCols<kGated>;
     const int32_t tile = int32_t(blockIdx.x) / p.split;
     const int32_t f0 = tile % p.n_tiles * kTileCols, m0 = tile / p.n_tiles * kTokens;      // first output column, first token
@@ -181,7 +182,7 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     grid_launch_dependents();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -212,31 +213,42 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         // bit 17, UE8M0 scales (bit 23), M >> 4 at bit 24; scale-factor byte ids
         // at bits 4..5 (B) and 29..30 (A)
         const uint32_t idesc = (uint32_t(p.n >> 3) << 17) | (1u << 23) | (uint32_t(kRowsW >> 4) << 24);
-        int32_t s = 0, j = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int32_t k = k0; k < k1; ++k) {
-            ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sh.full[s], phase, sh, p.status));
-            if (ok && ((k - k0) & 3) == 0)
-                ok = __all_sync(0xFFFFFFFFu, wait_or_abort(sh.sf_ready[j % kSfSlots], uint32_t(j / kSfSlots) & 1u, sh, p.status));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t st = smem_u32(smem) + uint32_t(s) * stage_bytes;
-            const uint64_t a_desc = smem_desc(st, 16, 1024, 2), b_desc = smem_desc(st + kWBytes, 16, 1024, 2);
-            const uint32_t sf = tmem + kSfCol0 + uint32_t((j % kSfSlots) * 4 + ((k - k0) & 3)) * 8;
+        // Every value of the loop is warp-uniform, and the next barriers are tested
+        // between a K-step's MMAs and its commits: 4 MMAs cost 255 ns however few
+        // tokens they have, and cost 348 ns without.
+        uint32_t s = 0, phase = 0, slot = 0, sf_phase = 0;
+        bool ok = true, landed = false, sf_landed = false;
+        for (int32_t k = k0; k < k1; k += 4) {           // a scale group
+            const int32_t steps = min(4, k1 - k);
+            const uint32_t next_slot = slot + 1 == kSfSlots ? 0 : slot + 1;
+            const uint32_t next_sf_phase = sf_phase ^ (next_slot == 0 ? 1u : 0u);
+            for (int32_t c = 0; c < steps; ++c) {
+                ok = __all_sync(0xFFFFFFFFu, landed) || __all_sync(0xFFFFFFFFu, wait_or_abort(sh.full[s], phase, sh, p.status));
+                if (ok && c == 0) {
+                    ok = __all_sync(0xFFFFFFFFu, sf_landed) ||
+                         __all_sync(0xFFFFFFFFu, wait_or_abort(sh.sf_ready[slot], sf_phase, sh, p.status));
+                    tc_fence_after();
+                }
+                if (!ok) break;
+                const uint32_t st = smem_u32(smem) + s * stage_bytes;
+                const uint64_t a_desc = smem_desc(st, 16, 1024, 2), b_desc = smem_desc(st + kWBytes, 16, 1024, 2);
+                const uint32_t sf = tmem + kSfCol0 + (slot * 4 + uint32_t(c)) * 8;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)               // (+32 bytes along K = +2 in the address field)
-                mma_mxf8_if(tmem, a_desc + 2 * kk, b_desc + 2 * kk, idesc | (uint32_t(kk) << 4) | (uint32_t(kk) << 29), sf,
-                            sf + 4, (k - k0) | kk ? 1u : 0u, issue);
-            tc_commit_if(smem_u32(&sh.empty[s]), issue);
-            if (((k - k0) & 3) == 3 || k == k1 - 1) {
-                tc_commit_if(smem_u32(&sh.grp_done[j % kSfSlots]), issue);
-                ++j;
+                for (int kk = 0; kk < 4; ++kk)           // (+32 bytes along K = +2 in the address field)
+                    mma_mxf8_if(tmem, a_desc + 2 * kk, b_desc + 2 * kk, idesc | (uint32_t(kk) << 4) | (uint32_t(kk) << 29), sf,
+                                sf + 4, (k - k0) | c | kk ? 1u : 0u, issue);
+                const uint32_t next = s + 1 == uint32_t(p.stages) ? 0 : s + 1;
+                const uint32_t next_phase = phase ^ (next == 0 ? 1u : 0u);
+                landed = mbar_test(smem_u32(&sh.full[next]), next_phase);
+                if (c == steps - 1) sf_landed = mbar_test(smem_u32(&sh.sf_ready[next_slot]), next_sf_phase);
+                tc_commit_if(smem_u32(&sh.empty[s]), issue);
+                if (c == steps - 1) tc_commit_if(smem_u32(&sh.grp_done[slot]), issue);
+                s = next;
+                phase = next_phase;
             }
-            if (++s == p.stages) {
-                s = 0;
-                phase ^= 1u;
-            }
+            if (!ok) break;
+            slot = next_slot;
+            sf_phase = next_sf_phase;
         }
         if (ok) tc_commit_if(smem_u32(&sh.acc_full), issue);
     } else if (warp == 2) {
@@ -382,7 +394,7 @@ te_mx_status launch(const GemmArgs& a, int sms, cudaStream_t stream) {
     // Split K while two blocks per SM are not there, down to one scale group (512
     // of K) per block; with several blocks of tokens, whose accumulators are
     // whole tiles to add up, at most four ways and past two only up to a block
-    // per SM (512 x 1024 x 4096: 19 us eight ways, 11.7 four ways)
+    // per SM (512 x 1024 x 4096: 19 us eight ways, 10.6 four ways)
     const int64_t tiles = int64_t(p.n_tiles) * ((p.M + kTokens - 1) / kTokens), groups = (p.k_iters + 3) / 4;
     const bool few = p.M <= kTokens;
     p.split = 1;
