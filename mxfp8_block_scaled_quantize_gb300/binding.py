@@ -213,24 +213,34 @@ def te_mx_version() -> str:
 
 # ---------------------------------------------------------------- torch helpers
 
-_raw_stream = None
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _raw_stream() -> int:
+    """The current device's current stream's handle, taken without building a
+    Stream object, which costs as much as a small launch (the first call puts the
+    function that does so in this one's place)."""
+    global _raw_stream
+    import torch
+    c = torch._C
+    if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+        torch.cuda.init()
+        current, device = c._cuda_getCurrentRawStream, c._cuda_getDevice
+        _raw_stream = lambda: current(device())  # noqa: E731
+    else:
+        _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
 
 
 def _stream_ptr(stream=None) -> int:
-    """The given stream's handle, or the current device's current stream's (taken
-    without building a Stream object, which costs as much as a small launch)."""
-    global _raw_stream
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is None:
-        import torch
-        c = torch._C
-        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
-            torch.cuda.init()
-            _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
-        else:
-            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-    return _raw_stream()
+    return _raw_stream() if stream is None else stream.cuda_stream
 
 
 def _on(stream):
@@ -360,14 +370,18 @@ def layernorm_quantize(x, gamma, beta, eps: float = 1e-5, rowwise: bool = True, 
     return o
 
 
-_dtype_codes: dict = {}
+class _DtypeCodes(dict):
+    """te_mx_dtype by torch dtype, filled in on first use."""
 
-
-def _dtype_code(t) -> int:
-    if not _dtype_codes:
+    def __missing__(self, dtype):
         import torch
-        _dtype_codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
-    return _dtype_codes[t.dtype]
+        self.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+        if dtype not in self:
+            raise TypeError(f"{dtype} is none of bfloat16, float16 and float32")
+        return self[dtype]
+
+
+_dtype_code = _DtypeCodes()
 
 
 def _pitch(t) -> int:
@@ -378,6 +392,11 @@ def _pitch(t) -> int:
     return ld if rows > 1 else max(ld, cols)
 
 
+def _vectors(a, b, n: int, dtype) -> bool:
+    """Whether a, and b if given, are contiguous CUDA vectors of n elements of that type."""
+    return all(t is None or (t.shape == (n,) and t.dtype == dtype and t.is_contiguous() and t.is_cuda) for t in (a, b))
+
+
 def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream=None, out=None):
     """LayerNorm over the last axis of a 2-D bf16, fp16 or fp32 CUDA tensor;
     gamma and beta (None: no shift) have its type or fp32.  Returns a dict with
@@ -386,7 +405,7 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
     if stream is not None:
         with _on(stream):
             return layernorm(x, gamma, beta, eps=eps, stats=stats, out=out)
-    import torch
+    torch = _torch or _load_torch()
     shape = x.shape
     rows, hidden = shape
     assert x.is_cuda and gamma.is_cuda and gamma.shape == shape[1:] and gamma.is_contiguous()
@@ -403,14 +422,16 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
             o["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
         y, ld_y = o["y"], _pitch(o["y"])
         assert y.shape == shape and y.dtype == x.dtype
+        if "mu" in o:
+            assert _vectors(o["mu"], o["rsigma"], rows, torch.float32)
     mu = rsigma = 0
     if stats and "mu" not in o:
         o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
         o["rsigma"] = torch.empty_like(o["mu"])
     if "mu" in o:
         mu, rsigma = o["mu"].data_ptr(), o["rsigma"].data_ptr()
-    _check(lib().te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code(x), gamma.data_ptr(), b,
-                                 _dtype_code(gamma), eps, y.data_ptr(), ld_y, mu, rsigma, _stream_ptr()))
+    _check(lib().te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code[x.dtype], gamma.data_ptr(), b,
+                                 _dtype_code[gamma.dtype], eps, y.data_ptr(), ld_y, mu, rsigma, _raw_stream()))
     return o
 
 
@@ -423,8 +444,8 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
     if stream is not None:
         with _on(stream):
             return layernorm_backward(dy, x, gamma, mu, rsigma, dparams=dparams, out=out, workspace=workspace)
-    import torch
-    shape, dt = x.shape, _dtype_code(x)
+    torch = _torch or _load_torch()
+    shape, dt = x.shape, _dtype_code[x.dtype]
     rows, hidden = shape
     assert x.is_cuda and dy.is_cuda and dy.shape == shape and dy.dtype == x.dtype
     assert gamma.shape == shape[1:] and gamma.is_contiguous() and mu.shape == rsigma.shape == shape[:1]
@@ -438,6 +459,8 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
             o["dx"] = torch.empty_like(x, memory_format=torch.contiguous_format)
         dx, ld_dx = o["dx"], _pitch(o["dx"])
         assert dx.shape == shape and dx.dtype == x.dtype
+        if "dgamma" in o:
+            assert _vectors(o["dgamma"], o.get("dbeta"), hidden, gamma.dtype)
     dga = dbe = ws = size = 0
     if dparams and "dgamma" not in o:
         o["dgamma"], o["dbeta"] = torch.empty_like(gamma), torch.empty_like(gamma)
@@ -448,8 +471,8 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
                                     device=x.device)
         ws, size = workspace.data_ptr(), workspace.numel()
     _check(lib().te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, dt,
-                                          gamma.data_ptr(), _dtype_code(gamma), mu.data_ptr(), rsigma.data_ptr(),
-                                          dx.data_ptr(), ld_dx, dga, dbe, ws, size, _stream_ptr()))
+                                          gamma.data_ptr(), _dtype_code[gamma.dtype], mu.data_ptr(), rsigma.data_ptr(),
+                                          dx.data_ptr(), ld_dx, dga, dbe, ws, size, _raw_stream()))
     return o
 
 
@@ -582,6 +605,15 @@ def grouped_gemm(group_m, qx, sx, qw, sw, bias=None, gelu: bool = False, stream=
     return d, aux
 
 
+def _mx_operand(q, s, rows: int) -> bool:
+    """Whether q and s are an MXFP8 operand's contiguous codes and scale rows."""
+    return q.is_contiguous() and q.is_cuda and s.is_cuda and s.shape[0] == rows and q.element_size() == s.element_size() == 1
+
+
+def _matrix(t, rows: int, cols: int, dtype) -> bool:
+    return t is None or (t.shape == (rows, cols) and t.dtype == dtype and t.is_contiguous() and t.is_cuda)
+
+
 def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = False, stream=None, out=None):
     """Gated feed-forward of MXFP8 operands: qx [M, K] and qw [2F, K] (the gate
     weight's rows, then the up weight's; ``quantize``'s row-wise copies), bias
@@ -591,17 +623,19 @@ def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = 
     if stream is not None:
         with _on(stream):
             return gated_gemm(qx, sx, qw, sw, activation=activation, bias=bias, aux=aux, out=out)
-    import torch
+    torch = _torch or _load_torch()
     M, K = qx.shape
     F = qw.shape[0] // 2
-    assert qw.shape == (2 * F, K) and (bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == 2 * F))
+    assert qw.shape == (2 * F, K) and _mx_operand(qx, sx, M) and _mx_operand(qw, sw, 2 * F)
+    assert bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == 2 * F and bias.is_contiguous())
     if out is None:
         h = torch.empty(M, F, dtype=torch.bfloat16, device=qx.device)
         pre = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=qx.device) if aux else None
     else:
         h, pre = out
+        assert _matrix(h, M, F, torch.bfloat16) and _matrix(pre, M, 2 * F, torch.bfloat16)
     te_mx_gated_gemm(qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(), sw.data_ptr(), _pitch(sw), M, F, K,
-                     _ptr(bias), ACTIVATIONS[activation], h.data_ptr(), _ptr(pre), _stream_ptr())
+                     _ptr(bias), ACTIVATIONS[activation], h.data_ptr(), _ptr(pre), _raw_stream())
     return h, pre
 
 
@@ -614,19 +648,22 @@ def grouped_gated_gemm(group_m, qx, sx, qw, sw, activation: str = "silu", bias=N
     if stream is not None:
         with _on(stream):
             return grouped_gated_gemm(group_m, qx, sx, qw, sw, activation=activation, bias=bias, aux=aux, out=out)
-    import torch
+    torch = _torch or _load_torch()
     total_m, K = qx.shape
     G, N, _ = qw.shape
+    sw2 = sw.reshape(G * N, -1)
     assert group_m.dtype == torch.int32 and group_m.numel() == G and N % 2 == 0 and qw.shape[2] == K
+    assert group_m.is_cuda and group_m.is_contiguous() and _mx_operand(qx, sx, total_m) and _mx_operand(qw, sw2, G * N)
+    assert bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == G * N and bias.is_contiguous())
     if out is None:
         h = torch.empty(total_m, N // 2, dtype=torch.bfloat16, device=qx.device)
         pre = torch.empty(total_m, N, dtype=torch.bfloat16, device=qx.device) if aux else None
     else:
         h, pre = out
-    sw2 = sw.reshape(G * N, -1)
+        assert _matrix(h, total_m, N // 2, torch.bfloat16) and _matrix(pre, total_m, N, torch.bfloat16)
     te_mx_grouped_gated_gemm(G, group_m.data_ptr(), total_m, qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(),
                              sw2.data_ptr(), _pitch(sw2), N // 2, K, _ptr(bias), ACTIVATIONS[activation], h.data_ptr(),
-                             _ptr(pre), _stream_ptr())
+                             _ptr(pre), _raw_stream())
     return h, pre
 
 
@@ -643,11 +680,19 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
         with _on(stream):
             return gated_backward(dh, gate_up, activation=activation, dense=dense, rowwise=rowwise, colwise=colwise,
                                   out=out)
-    import torch
+    torch = _torch or _load_torch()
     assert dh.dtype == gate_up.dtype == torch.bfloat16 and dh.dim() == gate_up.dim() == 2 and dh.is_cuda
     M, F = dh.shape
     assert gate_up.shape == (M, 2 * F) and dh.stride(1) == gate_up.stride(1) == 1
     o = dict(out or {})
+    if o:
+        shapes = {"d_gate_up": (M, 2 * F), "q_row": (M, 2 * F), "s_row": (M, None), "q_col": (2 * F, None),
+                  "s_col": (2 * F, None)}
+        for k, (rows, cols) in shapes.items():
+            t = o.get(k)
+            assert t is None or (t.is_cuda and t.shape[0] == rows and cols in (None, t.shape[1])
+                                 and t.element_size() == (2 if k == "d_gate_up" else 1)), k
+        assert "q_row" not in o or o["q_row"].is_contiguous()
     if dense and "d_gate_up" not in o:
         o["d_gate_up"] = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=dh.device)
     if rowwise and "q_row" not in o:
@@ -661,5 +706,5 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
     te_mx_gated_backward(dh.data_ptr(), _pitch(dh), gate_up.data_ptr(), _pitch(gate_up), M, F, ACTIVATIONS[activation],
                          _ptr(o.get("d_gate_up")), ld("d_gate_up"), _ptr(o.get("q_row")), _ptr(o.get("s_row")),
                          ld("s_row"), _ptr(o.get("q_col")), ld("q_col"), _ptr(o.get("s_col")), ld("s_col"),
-                         _stream_ptr())
+                         _raw_stream())
     return o
