@@ -304,7 +304,9 @@ TEMX_API te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, co
  * Rules: K % 128 == 0, K >= 128; M, N >= 1 with N % 16 == 0 (M arbitrary);
  * A, B, sA, sB, D, aux 16-byte aligned; ld_s* multiples of 16 >= K/32.
  * Accuracy: |D - exact| <= 2^-7 |exact| + 1e-5 sum_k |a_k b_k| element-wise,
- * exact = the epilogue of the fp64 product of the dequantised operands. */
+ * exact = the epilogue of the fp64 product of the dequantised operands.  The
+ * order of the additions depends on the shapes alone (with few output tiles and
+ * K >= 2048, K is split over a cluster of blocks): results repeat bit for bit. */
 TEMX_API te_mx_status te_mx_gemm(const uint8_t* A, const uint8_t* sA, int64_t ld_sA,
                         const uint8_t* B, const uint8_t* sB, int64_t ld_sB,
                         int64_t M, int64_t N, int64_t K,

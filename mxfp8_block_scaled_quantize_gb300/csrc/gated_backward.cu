@@ -20,6 +20,10 @@
 //               leave as whole words.  Four warps write them a round later, so
 //               that no pair waits for the others and the pairs' loads, arithmetic
 //               and stores overlap.
+// Measured (us; floor, here): dense 4096 x 4096 24.7, 26.7; both copies 8192 x
+// 18432 225, 277 (391 with one warp per unit, 291 with the scale bytes written
+// before the pair goes on); what is left is the arithmetic of two quantisations
+// per element pair at 16 warps per SM.
 #include <cuda_runtime.h>
 
 #include "e4m3.cuh"
