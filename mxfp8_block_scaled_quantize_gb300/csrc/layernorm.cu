@@ -189,10 +189,9 @@ ln_forward_vec_kernel(const LnArgs a, int nvec) {
 
 // ---------------------------------------------------------------- any layout
 
-// One block per row, element by element: the blockDim.x threads hold the row in
-// registers, kE elements each, so it is read once.  Bound by the loads and
-// stores of single elements: 4097 x 1023 fp16 with fp32 parameters 11.9 us (a
-// warp per row: 16.9).
+// Rows of more elements than the persistent kernels for any layout take (below),
+// up to 1024 kE: one block per row, whose threads hold it in registers, kE
+// elements each, so it is read once.
 template <typename T, typename P, int kE>
 __global__ void __launch_bounds__(1024)
 ln_forward_kernel(const LnArgs a) {
@@ -639,6 +638,109 @@ ln_backward_vec_kernel(const LnBackwardArgs a, const LnBwdShape sh, unsigned int
     if constexpr (kCluster) all_blocks_sync();             // no block leaves while another may still store to it
 }
 
+// Rows of up to 512 kE elements in any layout, backward: persistent.
+// blockDim.x threads own the same columns (kE each, element by element) of every
+// row that they take, so dy and x are read once and the columns' sums stay in
+// registers; blockDim.y such groups per block, joined at the end.  The next row
+// is loaded before the sums of this one cross the group.  Measured (us; this, a
+// pass for dx and one for the columns' sums): 4097 x 1023 fp16 with fp32
+// parameters 17.2, 30.5; 5000 x 3001 fp32 49, 141; 1000 x 7001 bf16 30, 56.
+constexpr int kAnyThreads = 512;
+template <int kE> constexpr int kAnyBlocks = kE <= 4 ? 2 : 1;          // per SM
+template <int kE> constexpr bool kAhead = kE <= 8;                     // (more would not fit in the registers)
+template <typename T, typename P, int kE>
+__global__ void __launch_bounds__(kAnyThreads, kAnyBlocks<kE>)
+ln_backward_any_kernel(const LnBackwardArgs a) {
+    __shared__ float part[2][kAnyThreads / 32][2];         // by parity of the row
+    extern __shared__ float sums[];                        // [2][blockDim.x * blockDim.y * kE]
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int hidden = int(a.hidden), t = int(threadIdx.x), tx = int(blockDim.x), group = int(threadIdx.y);
+    const int lane = t & 31, gwarps = tx >> 5, gwarp0 = group * gwarps;
+    const int64_t first = int64_t(blockIdx.x) * blockDim.y + group, step = int64_t(gridDim.x) * blockDim.y;
+    const int n_mine = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
+    float ga[kE], dga[kE], dbe[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        const int i = t + e * tx;
+        ga[e] = i < hidden ? load_param<P>(a.gamma, i) : 0.0f;
+        dga[e] = dbe[e] = 0.0f;
+    }
+    T d[kE], x[kE];
+    float mu = 0.0f, rs = 0.0f;
+    auto load = [&](int64_t row) {                         // (past the row's end: zeros in dy, so zeros in every sum)
+        const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy + t;
+        const T* px = static_cast<const T*>(a.x) + row * a.ld_x + t;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const bool live = t + e * tx < hidden;
+            d[e] = live ? dy[e * tx] : from_f32<T>(0.0f);
+            x[e] = live ? px[e * tx] : from_f32<T>(0.0f);
+        }
+        mu = a.mu[row];
+        rs = a.rsigma[row];
+    };
+    if (n_mine > 0) load(first);
+    const float inv_h = 1.0f / float(hidden);
+    for (int i = 0; i < n_mine; ++i) {
+        const int64_t row = first + i * step;
+        const float m = mu, r = rs;
+        float g[kE], xh[kE], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const float v = to_f32(d[e]);
+            xh[e] = t + e * tx < hidden ? (to_f32(x[e]) - m) * r : 0.0f;
+            g[e] = v * ga[e];
+            s1 += g[e];
+            s2 = fmaf(g[e], xh[e], s2);
+            dga[e] = fmaf(v, xh[e], dga[e]);
+            dbe[e] += v;
+        }
+        if (kAhead<kE> && i + 1 < n_mine) load(row + step);
+        float total = warp_sum2(s1, s2, lane);
+        if (gwarps > 1) {
+            float(*slot)[2] = &part[i & 1][gwarp0];        // (read before the next row's barrier, written again after it)
+            if (lane % 16 == 0) slot[t >> 5][lane / 16] = total;
+            group_barrier(1 + group, tx);
+            const float2 f = lane < gwarps ? make_float2(slot[lane][0], slot[lane][1]) : make_float2(0.0f, 0.0f);
+            total = warp_sum2(f.x, f.y, lane);
+        }
+        const float c1 = __shfl_sync(0xFFFFFFFFu, total, 0) * inv_h, c2 = __shfl_sync(0xFFFFFFFFu, total, 16) * inv_h;
+        if (a.dx) {
+            T* dx = static_cast<T*>(a.dx) + row * a.ld_dx + t;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                if constexpr (!kAhead<kE>) {               // (from the words again, not kept)
+                    g[e] = to_f32(d[e]) * ga[e];
+                    xh[e] = (to_f32(x[e]) - m) * r;
+                }
+                if (t + e * tx < hidden) dx[e * tx] = from_f32<T>(r * (g[e] - c1 - xh[e] * c2));
+            }
+        }
+        if (!kAhead<kE> && i + 1 < n_mine) load(row + step);
+    }
+    if (!a.dgamma) return;
+    // the groups' column sums, added in group order
+    float* sums_b = sums + int(blockDim.y) * tx * kE;
+    float* mine = sums + group * tx * kE;
+    float* mine_b = sums_b + group * tx * kE;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        mine[t + e * tx] = dga[e];
+        mine_b[t + e * tx] = dbe[e];
+    }
+    __syncthreads();
+    for (int c = group * tx + t; c < hidden; c += tx * int(blockDim.y)) {
+        float sg = 0.0f, sb = 0.0f;
+        for (int q = 0; q < int(blockDim.y); ++q) {
+            sg += sums[q * tx * kE + c];
+            sb += sums_b[q * tx * kE + c];
+        }
+        a.partial[2 * int64_t(blockIdx.x) * hidden + c] = sg;
+        a.partial[(2 * int64_t(blockIdx.x) + 1) * hidden + c] = sb;
+    }
+}
+
 // Forward, many long rows on 16-byte boundaries: persistent.  Groups of threads
 // take rows in turn, kFwdVectors vectors per thread; rows come through a ring in
 // shared memory, one bulk copy each, and gamma and beta stay in registers.
@@ -785,6 +887,64 @@ ln_forward_ring_kernel(const LnArgs a, const LnFwdShape sh, unsigned int* status
             for (uint32_t p = 0; p < 2; ++p) mbar_wait(smem_u32(&full[group][q]), p, status, 1000000ull);
 }
 
+// Rows of up to 512 kE elements in any layout, forward: persistent, as the
+// backward pass, with gamma and beta in registers.  Bound by the loads and stores
+// of single elements.  Measured (us; this, a block per row): 4097 x 1023 fp16 with
+// fp32 parameters 11.1, 12.3; 5000 x 3001 fp32 40, 54; 1000 x 7001 bf16 23, 27;
+// 16384 x 65 5.6, 17.4.
+template <int kE> constexpr int kAnyFwdBlocks = kE <= 8 ? 2 : 1;       // per SM
+template <typename T, typename P, int kE>
+__global__ void __launch_bounds__(kAnyThreads, kAnyFwdBlocks<kE>)
+ln_forward_any_kernel(const LnArgs a) {
+    __shared__ __align__(16) float part[2][kAnyThreads / 32][16];      // of the mean, of the squares
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int hidden = int(a.hidden), t = int(threadIdx.x), tx = int(blockDim.x), group = int(threadIdx.y);
+    const int lane = t & 31, gwarps = tx >> 5, gwarp = t >> 5;
+    const int64_t first = int64_t(blockIdx.x) * blockDim.y + group, step = int64_t(gridDim.x) * blockDim.y;
+    if (t < 16) part[0][group][t] = part[1][group][t] = 0.0f;
+    __syncthreads();
+    float ga[kE], be[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        const int i = t + e * tx;
+        ga[e] = i < hidden ? load_param<P>(a.gamma, i) : 0.0f;
+        be[e] = i < hidden && a.beta ? load_param<P>(a.beta, i) : 0.0f;
+    }
+    T x[kE];
+    auto load = [&](int64_t row) {
+        const T* px = static_cast<const T*>(a.x) + row * a.ld_x + t;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) x[e] = t + e * tx < hidden ? px[e * tx] : from_f32<T>(0.0f);
+    };
+    if (first < a.rows) load(first);
+    for (int64_t row = first; row < a.rows; row += step) {
+        float v[kE], s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            v[e] = to_f32(x[e]);
+            s += v[e];
+        }
+        if (row + step < a.rows) load(row + step);
+        const float mu = group_sum(s, part[0][group], gwarps, gwarp, lane, 1 + group, tx) / float(hidden);
+        s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const float d = t + e * tx < hidden ? v[e] - mu : 0.0f;
+            s = fmaf(d, d, s);
+        }
+        const float rs = 1.0f / sqrtf(group_sum(s, part[1][group], gwarps, gwarp, lane, 1 + group, tx) / float(hidden) + a.eps);
+        T* y = static_cast<T*>(a.y) + row * a.ld_y + t;
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+            if (t + e * tx < hidden) y[e * tx] = from_f32<T>(fmaf((v[e] - mu) * rs, ga[e], be[e]));
+        if (t == 0 && a.mu) {
+            a.mu[row] = mu;
+            a.rsigma[row] = rs;
+        }
+    }
+}
+
 // ---------------------------------------------------------------- launches
 
 // Launch with programmatic stream serialisation: the blocks may start while
@@ -846,9 +1006,11 @@ cudaError_t forward_vec(const LnArgs& a, int sms, unsigned int* status, cudaStre
         if (a.rows >= 2 * int64_t(sms) * sh.groups) return forward_ring<T, kP32>(a, sh, sms, status, stream);
     }
     // Threads per row: one vector per thread while there are too few rows to
-    // fill the GPU with smaller blocks, else up to four (eight for rows past
-    // 4096 vectors).
-    int v = a.rows <= 304 && nvec <= 1024 ? 1 : nvec <= 64 ? 2 : nvec <= 4096 ? 4 : 8;
+    // fill the GPU with smaller blocks, else up to four; eight for rows past 2048
+    // vectors, so that two blocks fit on an SM (2000 x 16384 fp32: 45 us, four 67;
+    // 515 x 16384: 17.9, 23.6), unless a block per SM is all there is (150 x
+    // 16384: 9.2, four 7.8).
+    const int v = a.rows <= 304 && nvec <= 1024 ? 1 : nvec <= 64 ? 2 : nvec <= 2048 || (nvec <= 4096 && a.rows <= sms) ? 4 : 8;
     const int tx = ((nvec + v - 1) / v + 31) / 32 * 32, ty = tx == 32 ? 4 : 1;
     const dim3 grid(unsigned((a.rows + ty - 1) / ty)), block{unsigned(tx), unsigned(ty)};
     if (v == 1) return launch_dependent(ln_forward_vec_kernel<T, kP32, 1>, grid, block, stream, a, nvec);
@@ -857,10 +1019,24 @@ cudaError_t forward_vec(const LnArgs& a, int sms, unsigned int* status, cudaStre
     return launch_dependent(ln_forward_vec_kernel<T, kP32, 8>, grid, block, stream, a, nvec);
 }
 
+// (a block takes more rows than one at a time once every SM has a block)
+template <typename T, typename P, int kE>
+cudaError_t forward_any_launch(const LnArgs& a, int sms, cudaStream_t stream) {
+    const unsigned tx = row_block(a.hidden, kE).x;
+    int64_t ty = a.rows / sms;
+    if (ty > kAnyThreads / int(tx)) ty = kAnyThreads / int(tx);
+    if (ty < 1) ty = 1;
+    int64_t blocks = (a.rows + ty - 1) / ty;
+    if (blocks > int64_t(kAnyFwdBlocks<kE>) * sms) blocks = int64_t(kAnyFwdBlocks<kE>) * sms;
+    return launch_dependent(ln_forward_any_kernel<T, P, kE>, dim3(unsigned(blocks)), dim3(tx, unsigned(ty)), stream, a);
+}
+
 template <typename T, typename P>
-cudaError_t forward_any(const LnArgs& a, cudaStream_t stream) {
+cudaError_t forward_any(const LnArgs& a, int sms, cudaStream_t stream) {
+    if (a.hidden <= 4 * kAnyThreads) return forward_any_launch<T, P, 4>(a, sms, stream);
+    if (a.hidden <= 8 * kAnyThreads) return forward_any_launch<T, P, 8>(a, sms, stream);
+    if (a.hidden <= 16 * kAnyThreads) return forward_any_launch<T, P, 16>(a, sms, stream);
     const dim3 grid(unsigned(a.rows));
-    if (a.hidden <= 4096) return launch_dependent(ln_forward_kernel<T, P, 4>, grid, row_block(a.hidden, 4), stream, a);
     if (a.hidden <= 16384) return launch_dependent(ln_forward_kernel<T, P, 16>, grid, row_block(a.hidden, 16), stream, a);
     return launch_dependent(ln_forward_long_kernel<T, P>, grid, dim3(kRowThreads), stream, a);
 }
@@ -874,8 +1050,8 @@ cudaError_t forward(const LnArgs& a, int sms, unsigned int* status, cudaStream_t
             if (a.param_dtype != TE_MX_FP32) return forward_vec<T, false>(a, sms, status, stream);
         return forward_vec<T, true>(a, sms, status, stream);
     }
-    if (a.param_dtype == a.dtype) return forward_any<T, T>(a, stream);
-    return forward_any<T, float>(a, stream);
+    if (a.param_dtype == a.dtype) return forward_any<T, T>(a, sms, stream);
+    return forward_any<T, float>(a, sms, stream);
 }
 
 template <typename T, bool kP32, bool kCluster>
@@ -924,10 +1100,42 @@ cudaError_t backward_vec(const LnBackwardArgs& a, int sms, unsigned int* status,
     return backward_vec_launch<T, kP32, true>(a, sh, smem, sms, status, parts, stream);
 }
 
+template <typename T, typename P, int kE>
+cudaError_t backward_any_launch(const LnBackwardArgs& a, int sms, int* parts, cudaStream_t stream) {
+    const unsigned tx = row_block(a.hidden, kE).x;
+    unsigned ty = kAnyThreads / tx;
+    if (ty > a.rows) ty = unsigned(a.rows);
+    const int64_t want = (a.rows + ty - 1) / ty;
+    int64_t most = int64_t(kAnyBlocks<kE>) * sms;
+    if (most > ln_backward_parts(a.rows)) most = ln_backward_parts(a.rows);
+    *parts = int(want < most ? want : most);
+    const size_t smem = size_t(2) * kE * tx * ty * sizeof(float);
+    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(ln_backward_any_kernel<T, P, kE>), 8 * kE * kAnyThreads);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(*parts));
+    cfg.blockDim = dim3(tx, ty);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ln_backward_any_kernel<T, P, kE>, a);
+}
+
+template <typename T, typename P>
+cudaError_t backward_any(const LnBackwardArgs& a, int sms, int* parts, cudaStream_t stream) {
+    if (a.hidden <= 4 * kAnyThreads) return backward_any_launch<T, P, 4>(a, sms, parts, stream);
+    if (a.hidden <= 8 * kAnyThreads) return backward_any_launch<T, P, 8>(a, sms, parts, stream);
+    return backward_any_launch<T, P, 16>(a, sms, parts, stream);
+}
+
+// (longer rows)
 template <typename T, typename P>
 cudaError_t backward_dx_any(const LnBackwardArgs& a, cudaStream_t stream) {
     const dim3 grid(unsigned(a.rows));
-    if (a.hidden <= 4096) return launch_dependent(ln_backward_dx_kernel<T, P, 4>, grid, row_block(a.hidden, 4), stream, a);
     if (a.hidden <= 16384) return launch_dependent(ln_backward_dx_kernel<T, P, 16>, grid, row_block(a.hidden, 16), stream, a);
     return launch_dependent(ln_backward_dx_long_kernel<T, P>, grid, dim3(kRowThreads), stream, a);
 }
@@ -944,6 +1152,12 @@ cudaError_t backward(const LnBackwardArgs& a, int sms, unsigned int* status, cud
             e = a.param_dtype != TE_MX_FP32 ? backward_vec<T, false>(a, sms, status, &n, stream)
                                             : backward_vec<T, true>(a, sms, status, &n, stream);
         else e = backward_vec<T, true>(a, sms, status, &n, stream);
+        if (e != cudaSuccess || !a.dgamma) return e;
+        return launch_dependent(ln_backward_reduce_kernel, reduce_grid, dim3(kReduceWarps * 32), stream, a, n);
+    }
+    if (a.rows > 0 && a.hidden <= 16 * kAnyThreads) {
+        int n = 0;
+        e = a.param_dtype == a.dtype ? backward_any<T, T>(a, sms, &n, stream) : backward_any<T, float>(a, sms, &n, stream);
         if (e != cudaSuccess || !a.dgamma) return e;
         return launch_dependent(ln_backward_reduce_kernel, reduce_grid, dim3(kReduceWarps * 32), stream, a, n);
     }
