@@ -353,10 +353,13 @@ ln_backward_params_kernel(const LnBackwardArgs a, int parts) {
 }
 
 // dgamma / dbeta from `parts` partial sums per column.  A block owns 32
-// columns (lane = column); warp w adds parts w, w + 32, ... in order, loading
-// four of them at a time (the sums come from L2 and the loads' latency is what
-// this costs), then the warps' sums are added in warp order.
+// columns (lane = column); warp w adds parts w, w + 32, ... in order, then the
+// warps' sums are added in warp order.  The sums come from L2 and the loads'
+// latency is what this costs: 32 warps with five loads in flight each hold the
+// parts of a block per SM (the whole backward pass, 4096 x 4096 fp32: 37.3 us;
+// four loads 37.9, ten 37.0 but 30.4 against 27.4 for 515 x 16384; 8 warps 41.7).
 constexpr int kReduceWarps = 32;
+constexpr int kReduceLoads = 5;
 __global__ void __launch_bounds__(kReduceWarps * 32)
 ln_backward_reduce_kernel(const LnBackwardArgs a, int parts) {
     __shared__ float sums[2][kReduceWarps][33];
@@ -366,16 +369,16 @@ ln_backward_reduce_kernel(const LnBackwardArgs a, int parts) {
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
     float sg = 0.0f, sb = 0.0f;
     if (c < a.hidden)
-        for (int p0 = warp; p0 < parts; p0 += 4 * kReduceWarps) {
-            float g[4], b[4];
+        for (int p0 = warp; p0 < parts; p0 += kReduceLoads * kReduceWarps) {
+            float g[kReduceLoads], b[kReduceLoads];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kReduceLoads; ++k) {
                 const int64_t p = p0 + k * kReduceWarps;
                 g[k] = p < parts ? a.partial[2 * p * a.hidden + c] : 0.0f;
                 b[k] = p < parts ? a.partial[(2 * p + 1) * a.hidden + c] : 0.0f;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kReduceLoads; ++k) {
                 sg += g[k];
                 sb += b[k];
             }
@@ -636,6 +639,139 @@ ln_backward_vec_kernel(const LnBackwardArgs a, const LnBwdShape sh, unsigned int
         }
     }
     if constexpr (kCluster) all_blocks_sync();             // no block leaves while another may still store to it
+}
+
+// Backward, few rows on 16-byte boundaries: one launch.  dgamma and dbeta need no
+// sums over rows' elements (mu and rsigma are given), so the first col_blocks
+// blocks own 8 vectors of columns each and add them over all rows, while a
+// block per row computes dx; dy and x come from L2 the second time.  (dx may not
+// overlap dy or x here.)  Measured (us; this, the persistent kernel and the join
+// of its blocks' sums): 1 x 7168 bf16 2.4, 7.1; 512 x 7168 8.5, 15.2; 2048 x 7168
+// 23.1, 27.8; 4096 x 7168 42.5, 42.3; 1000 x 2048 8.5, 10.8; 2000 x 2048 15.5,
+// 14.1; 100 x 16384 fp32 12.4, 16.7; 515 x 16384 fp32 32, 28: so up to 304 rows,
+// and up to four times the row's vectors where a thread holds at most four of
+// them and L2 the rest (few_rows).
+constexpr int kFewThreads = 512;
+constexpr int kFewRows = 304;
+constexpr int kFewVectors = 8;                   // of columns per column block: 128 bytes of a row
+template <typename T, bool kP32, int kV>
+__global__ void __launch_bounds__(kFewThreads, kV <= 4 ? 2 : 1)
+ln_backward_few_kernel(const LnBackwardArgs a, int nvec, int col_blocks) {
+    using V = Vec<T>;
+    constexpr int kCols = kFewVectors * V::kN;
+    __shared__ float cols[2][kFewThreads / 32][kCols];
+    __shared__ __align__(8) float part[kFewThreads / 32][2];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint4* dy = static_cast<const uint4*>(a.dy);
+    const uint4* x = static_cast<const uint4*>(a.x);
+    const int64_t pitch_dy = a.ld_dy * int64_t(sizeof(T)) / 16, pitch_x = a.ld_x * int64_t(sizeof(T)) / 16;
+    if (int(blockIdx.x) < col_blocks) {
+        const int vec = int(blockIdx.x) * kFewVectors + lane % kFewVectors, groups = blockDim.x / kFewVectors;
+        uint64_t dga[V::kPairs], dbe[V::kPairs];
+#pragma unroll
+        for (int k = 0; k < V::kPairs; ++k) dga[k] = dbe[k] = 0;
+        if (vec < nvec)
+            for (int64_t r0 = threadIdx.x / kFewVectors; r0 < a.rows; r0 += 4 * groups) {       // four rows in flight
+                uint4 wd[4], wx[4];
+                float mu[4], rs[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t row = r0 + q * groups;
+                    const bool live = row < a.rows;
+                    wd[q] = live ? dy[row * pitch_dy + vec] : make_uint4(0, 0, 0, 0);
+                    wx[q] = live ? x[row * pitch_x + vec] : make_uint4(0, 0, 0, 0);
+                    mu[q] = live ? a.mu[row] : 0.0f;
+                    rs[q] = live ? a.rsigma[row] : 0.0f;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t mu2 = f32x2::both(mu[q]), rs2 = f32x2::both(rs[q]);
+#pragma unroll
+                    for (int k = 0; k < V::kPairs; ++k) {
+                        const uint64_t d = V::pair(wd[q], k);
+                        dga[k] = f32x2::fma(d, f32x2::mul(f32x2::sub(V::pair(wx[q], k), mu2), rs2), dga[k]);
+                        dbe[k] = f32x2::add(dbe[k], d);
+                    }
+                }
+            }
+        // the warp's four rows, then the warps in order
+        float v[2][V::kN];
+#pragma unroll
+        for (int k = 0; k < V::kPairs; ++k) {
+            v[0][2 * k] = f32x2::lo(dga[k]);
+            v[0][2 * k + 1] = f32x2::hi(dga[k]);
+            v[1][2 * k] = f32x2::lo(dbe[k]);
+            v[1][2 * k + 1] = f32x2::hi(dbe[k]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < V::kN; ++k) {
+                v[h][k] += __shfl_xor_sync(0xFFFFFFFFu, v[h][k], 8);
+                v[h][k] += __shfl_xor_sync(0xFFFFFFFFu, v[h][k], 16);
+                if (lane < kFewVectors) cols[h][warp][lane * V::kN + k] = v[h][k];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * kCols; i += blockDim.x) {
+            const int h = i / kCols, c = i % kCols;
+            const int64_t col = int64_t(blockIdx.x) * kCols + c;
+            if (col >= a.hidden) continue;
+            float s = cols[h][0][c];
+            for (int w = 1; w < warps; ++w) s += cols[h][w][c];
+            if (h == 0) store_param(a.dgamma, a.param_dtype, col, s);
+            else if (a.dbeta) store_param(a.dbeta, a.param_dtype, col, s);
+        }
+        return;
+    }
+    const int64_t row = int(blockIdx.x) - col_blocks;
+    const float mu = a.mu[row], rs = a.rsigma[row];
+    const uint64_t mu2 = f32x2::both(mu), rs2 = f32x2::both(rs);
+    uint4 wd[kV], wx[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int i = threadIdx.x + v * blockDim.x;
+        wd[v] = i < nvec ? dy[row * pitch_dy + i] : make_uint4(0, 0, 0, 0);
+        wx[v] = i < nvec ? x[row * pitch_x + i] : make_uint4(0, 0, 0, 0);
+    }
+    uint64_t s1 = 0, s2 = 0;
+    ParamVec<T, kP32> g;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int i = threadIdx.x + v * blockDim.x;
+        if (i < nvec) {
+            g.load(a.gamma, i);
+#pragma unroll
+            for (int k = 0; k < V::kPairs; ++k) {
+                const uint64_t d = f32x2::mul(V::pair(wd[v], k), g.pair(k));
+                s1 = f32x2::add(s1, d);
+                s2 = f32x2::fma(d, f32x2::mul(f32x2::sub(V::pair(wx[v], k), mu2), rs2), s2);
+            }
+        }
+    }
+    float total = warp_sum2(f32x2::lo(s1) + f32x2::hi(s1), f32x2::lo(s2) + f32x2::hi(s2), lane);
+    if (lane % 16 == 0) part[warp][lane / 16] = total;
+    __syncthreads();
+    const float2 f = lane < warps ? *reinterpret_cast<const float2*>(part[lane]) : make_float2(0.0f, 0.0f);
+    total = warp_sum2(f.x, f.y, lane);
+    const float inv_h = 1.0f / float(a.hidden);
+    const float c1 = __shfl_sync(0xFFFFFFFFu, total, 0), c2 = __shfl_sync(0xFFFFFFFFu, total, 16);
+    const uint64_t k1 = f32x2::both(-rs * (c1 * inv_h)), k2 = f32x2::both(-rs * rs * (c2 * inv_h));
+    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.ld_dx);
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int i = threadIdx.x + v * blockDim.x;
+        if (i < nvec) {
+            g.load(a.gamma, i);
+            uint64_t o[V::kPairs];
+#pragma unroll
+            for (int k = 0; k < V::kPairs; ++k)
+                o[k] = f32x2::fma(f32x2::mul(V::pair(wd[v], k), g.pair(k)), rs2,
+                                  f32x2::fma(f32x2::sub(V::pair(wx[v], k), mu2), k2, k1));
+            out[i] = V::from_pairs(o);
+        }
+    }
 }
 
 // Rows of up to 512 kE elements in any layout, backward: persistent.
@@ -1100,6 +1236,35 @@ cudaError_t backward_vec(const LnBackwardArgs& a, int sms, unsigned int* status,
     return backward_vec_launch<T, kP32, true>(a, sh, smem, sms, status, parts, stream);
 }
 
+// One launch for dx and the parameters' gradients: see ln_backward_few_kernel.
+bool few_rows(int64_t rows, int64_t nvec) {
+    if (nvec > 8 * kFewThreads) return false;
+    return rows <= kFewRows || (nvec <= 4 * kFewThreads && rows <= 4 * nvec && rows * nvec <= 3 << 20);
+}
+
+template <typename T, bool kP32>
+cudaError_t backward_few(const LnBackwardArgs& a, cudaStream_t stream) {
+    const int nvec = int(a.hidden / Vec<T>::kN);
+    const int v = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8;
+    int threads = ((nvec + v - 1) / v + 31) / 32 * 32;
+    const int least = a.rows <= kFewRows ? 256 : kFewThreads;          // (row groups of the column blocks)
+    if (threads < least) threads = least;
+    const int col_blocks = a.dgamma ? (nvec + kFewVectors - 1) / kFewVectors : 0;
+    const dim3 grid(unsigned(col_blocks + (a.dx ? a.rows : 0))), block{unsigned(threads)};
+    if (v == 1) return launch_dependent(ln_backward_few_kernel<T, kP32, 1>, grid, block, stream, a, nvec, col_blocks);
+    if (v == 2) return launch_dependent(ln_backward_few_kernel<T, kP32, 2>, grid, block, stream, a, nvec, col_blocks);
+    if (v == 4) return launch_dependent(ln_backward_few_kernel<T, kP32, 4>, grid, block, stream, a, nvec, col_blocks);
+    return launch_dependent(ln_backward_few_kernel<T, kP32, 8>, grid, block, stream, a, nvec, col_blocks);
+}
+
+// dx shares memory with dy or x (then the parameters' sums must not read after dx is written).
+template <typename T>
+bool dx_overlaps(const LnBackwardArgs& a) {
+    auto ends = [&](const void* p, int64_t ld) { return static_cast<const T*>(p) + (a.rows - 1) * ld + a.hidden; };
+    auto meet = [&](const void* p, int64_t ld) { return p < ends(a.dx, a.ld_dx) && a.dx < ends(p, ld); };
+    return a.dx && (meet(a.dy, a.ld_dy) || meet(a.x, a.ld_x));
+}
+
 template <typename T, typename P, int kE>
 cudaError_t backward_any_launch(const LnBackwardArgs& a, int sms, int* parts, cudaStream_t stream) {
     const unsigned tx = row_block(a.hidden, kE).x;
@@ -1147,6 +1312,12 @@ cudaError_t backward(const LnBackwardArgs& a, int sms, unsigned int* status, cud
     if (a.rows > 0 && a.hidden % Vec<T>::kN == 0 && a.hidden / Vec<T>::kN <= kBwdVectors<T> * kBwdThreads * kBwdMaxCluster &&
         rows_on16(a.x, a.ld_x, a.rows, sizeof(T)) && rows_on16(a.dy, a.ld_dy, a.rows, sizeof(T)) &&
         rows_on16(a.dx, a.ld_dx, a.rows, sizeof(T)) && on16(a.gamma)) {
+        // (without the parameters' gradients there is nothing to join)
+        if ((a.dgamma || a.rows <= kFewRows) && few_rows(a.rows, a.hidden / Vec<T>::kN) && !dx_overlaps<T>(a)) {
+            if constexpr (sizeof(T) == 2)
+                if (a.param_dtype != TE_MX_FP32) return backward_few<T, false>(a, stream);
+            return backward_few<T, true>(a, stream);
+        }
         int n = 0;
         if constexpr (sizeof(T) == 2)
             e = a.param_dtype != TE_MX_FP32 ? backward_vec<T, false>(a, sms, status, &n, stream)
