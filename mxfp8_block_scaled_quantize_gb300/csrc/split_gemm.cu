@@ -1,4 +1,5 @@
-// MXFP8 GEMM for few tokens or few output tiles, plain or gated: where the 256-
+// MXFP8 GEMM for few tokens or few output tiles, plain, gated or gated over
+// experts (whose blocks of tokens are found on the device): where the 256-
 // column tiles of gemm.cu leave SMs idle, and where the bytes of the weights are
 // what the call costs.
 //
@@ -13,6 +14,8 @@
 //   gated, 1 token, 7168 -> 2 x 18432       40.1   43.3   56
 //   gated, 1 token, 4096 -> 2 x 1024         1.3    6     17
 //   gated, 300 tokens, 4096 -> 2 x 1024      1.7   11.4   20
+//   grouped, 1 token to 8 of 128 experts, 4096 -> 2 x 768
+//                                            7.7   14.0   27.8
 //   plain, 1 x 7168 x 18432                 20.1   24.4   94
 //   plain, 1000 x 1024 x 8192                2.8   15.7   29.6
 //
@@ -56,13 +59,15 @@ constexpr int kTilePitch = kRowsW + 4;       // floats per token of the accumula
 constexpr int kMaxSplit = 8;
 
 struct SplitParams {
-    int32_t M, N, K;         // N: output columns (gated: W has 2N rows)
+    int32_t M, N, K;         // M: tokens in all; N: output columns (gated: W has 2N rows, per group)
+    int32_t groups;          // 0: dense
+    const int32_t* group_m;  // device
     int32_t n;               // tokens of a tile, rounded up to 16
     int32_t n_tiles;         // tiles along N; the tile index goes through them first
     int32_t k_iters;         // K / 128
     int32_t split;           // blocks of a cluster, each with its part of K
     int32_t stages;
-    const uint16_t* bias;    // bf16 [N] (gated: [2N]) or null
+    const uint16_t* bias;    // bf16 [N] (gated: [2N], per group) or null
     uint16_t* D;             // bf16 [M x N]
     uint16_t* aux;           // gated: bf16 [M x 2N] or null
     int32_t act;
@@ -77,7 +82,57 @@ struct __align__(16) SplitShared {
     uint64_t acc_full;                       // every MMA completed
     uint32_t tmem_base;
     int32_t abort;
+    int32_t group, m0, row_end;              // grouped: this block's tokens (group < 0: none)
 };
+
+// Grouped: finds the `want`-th block of up to 128 tokens among the groups' rows
+// (one warp).  Sizes are clamped so that no group reaches past M; a negative size
+// or a sum above M sets the status word, once per launch.
+__device__ __forceinline__ void find_block(const SplitParams& p, SplitShared& sh, int32_t want, int lane) {
+    const int per = (p.groups + 31) / 32, lo = min(p.groups, lane * per), hi = min(p.groups, lo + per);
+    bool bad = false;
+    int64_t rows = 0;
+    for (int g = lo; g < hi; ++g) {
+        bad |= p.group_m[g] < 0;
+        rows += max(p.group_m[g], 0);
+    }
+    int64_t incl = rows;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    bad |= lane == 31 && incl > p.M;
+    const int64_t first = incl - rows, M = p.M;
+    auto blocks_of = [&](int64_t row, int32_t m) { return int32_t((min(row + m, M) - min(row, M) + kTokens - 1) / kTokens); };
+    int32_t blocks = 0;
+    int64_t row = first;
+    for (int g = lo; g < hi; ++g) {
+        const int32_t m = max(p.group_m[g], 0);
+        blocks += blocks_of(row, m);
+        row += m;
+    }
+    int32_t b = blocks;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, b, o);
+        if (lane >= o) b += v;
+    }
+    if (lane == 31 && want >= b) sh.group = -1;
+    b -= blocks;                                          // blocks before this lane's groups
+    if (want >= b && want < b + blocks) {
+        row = first;
+        for (int g = lo; g < hi; ++g) {
+            const int32_t m = max(p.group_m[g], 0), n = blocks_of(row, m);
+            if (want >= b && want < b + n) {
+                sh.group = g;
+                sh.m0 = int32_t(row) + (want - b) * kTokens;
+                sh.row_end = int32_t(min(row + m, M));
+            }
+            b += n;
+            row += m;
+        }
+    }
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && blockIdx.x == 0) set_device_status(p.status, kStatusBadArg);
+}
 
 // Bounded mbarrier wait that also returns false once another role aborted.
 __device__ __forceinline__ bool wait_or_abort(const uint64_t& b, uint32_t parity, SplitShared& sh, unsigned int* status) {
@@ -134,7 +189,7 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
     return r;
 }
 
-template <bool kGated>
+template <bool kGated, bool kGrouped>
 __global__ void __launch_bounds__(kThreads, 2)
 split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_sw, const __grid_constant__ CUtensorMap map_sx,
@@ -147,7 +202,7 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     const uint32_t rank = __shfl_sync(0xFFFFFFFFu, p.split > 1 ? cluster_ctarank() : 0u, 0);
     constexpr int kTileCols = kCols<kGated>;
     const int32_t tile = int32_t(blockIdx.x) / p.split;
-    const int32_t f0 = tile % p.n_tiles * kTileCols, m0 = tile / p.n_tiles * kTokens;      // first output column, first token
+    const int32_t f0 = tile % p.n_tiles * kTileCols;     // first output column
     const uint32_t stage_bytes = uint32_t(kWBytes + p.n * kK);
     const uint32_t sf_ring = smem_u32(smem) + uint32_t(p.stages) * stage_bytes;
     // this block's scale groups (4 K-steps each) and K-steps
@@ -180,9 +235,17 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     }
     grid_dependency_wait();
     grid_launch_dependents();
+    if (kGrouped && warp == 3) find_block(p, sh, tile / p.n_tiles, lane);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
+    if (kGrouped && sh.group < 0) {                      // (every block of a cluster)
+        if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
+    // first token, end of the tile's tokens, group, its first row of W
+    const int32_t m0 = kGrouped ? sh.m0 : tile / p.n_tiles * kTokens, row_end = kGrouped ? sh.row_end : p.M;
+    const int32_t group = kGrouped ? sh.group : 0, w0 = group * (kGated ? 2 : 1) * p.N + f0;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -193,9 +256,9 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (!wait_or_abort(sh.empty[s], phase, sh, p.status)) break;
                 const uint32_t dst = smem_u32(smem) + uint32_t(s) * stage_bytes, bar = smem_u32(&sh.full[s]);
                 mbar_arrive_expect_tx(bar, stage_bytes);
-                tma_load_2d(dst, &map_w, bar, k * kK, f0);
+                tma_load_2d(dst, &map_w, bar, k * kK, w0);
                 if constexpr (kGated)                    // (the box is 64 rows: gate, then up)
-                    tma_load_2d(dst + kWBytes / 2, &map_w, bar, k * kK, p.N + f0);
+                    tma_load_2d(dst + kWBytes / 2, &map_w, bar, k * kK, p.N + w0);
                 tma_load_2d(dst + kWBytes, &map_x, bar, k * kK, m0);
                 if (++s == p.stages) {
                     s = 0;
@@ -256,8 +319,8 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         auto load = [&](int32_t j) {                     // group j (of this block), by lane 0
             const uint32_t bar = smem_u32(&sh.sf_full[j % kSfSlots]), dst = sf_ring + uint32_t(j % kSfSlots) * kSfSlotBytes;
             mbar_arrive_expect_tx(bar, uint32_t(16 * (kRowsW + p.n)));
-            tma_load_2d(dst, &map_sw, bar, (g0 + j) * 16, f0);
-            if constexpr (kGated) tma_load_2d(dst + kRowsW * 8, &map_sw, bar, (g0 + j) * 16, p.N + f0);
+            tma_load_2d(dst, &map_sw, bar, (g0 + j) * 16, w0);
+            if constexpr (kGated) tma_load_2d(dst + kRowsW * 8, &map_sw, bar, (g0 + j) * 16, p.N + w0);
             tma_load_2d(dst + kRowsW * 16, &map_sx, bar, (g0 + j) * 16, m0);
         };
         const int32_t n_groups = g1 - g0;
@@ -323,7 +386,7 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     // (neighbouring threads read neighbouring bytes: 128 tokens, 4096 -> 2 x 1024,
     // 14.9 us; 19.5 us with a token per thread)
     constexpr int kChunks = kTileCols / 8;
-    const int32_t items = min(kTokens, p.M - m0) * kChunks, i1 = int32_t(int64_t(items) * (rank + 1) / p.split);
+    const int32_t items = min(kTokens, row_end - m0) * kChunks, i1 = int32_t(int64_t(items) * (rank + 1) / p.split);
     for (int32_t i = int32_t(int64_t(items) * rank / p.split) + int32_t(threadIdx.x); i < i1; i += kThreads) {
         const int32_t m = i / kChunks, c = i % kChunks * 8, f = f0 + c;
         if (f >= p.N) continue;                          // (N % 16 == 0: 8 columns are in or out together)
@@ -356,7 +419,7 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             v[half][2] = f32x2::pack(b.x, b.y);
             v[half][3] = f32x2::pack(b.z, b.w);
             if (p.bias) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.bias + half * int64_t(p.N) + f));
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.bias + ((kGated ? 2 : 1) * group + half) * int64_t(p.N) + f));
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[half][k] = f32x2::add(v[half][k], f32x2::pack(bf16_lo(ww[k]), bf16_hi(ww[k])));
@@ -378,13 +441,21 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     if (p.split > 1) cluster_sync();                     // no block leaves while another may still read its shared memory
 }
 
-template <bool kGated>
+// Blocks of up to 128 tokens that M tokens can make in `groups` groups (or one).
+int64_t token_blocks(int64_t M, int64_t groups) {
+    if (groups == 0) return (M + kTokens - 1) / kTokens;
+    return (M < groups ? M : groups) + M / kTokens;
+}
+
+template <bool kGated, bool kGrouped>
 te_mx_status launch(const GemmArgs& a, int sms, cudaStream_t stream) {
     SplitParams p{};
     p.M = int32_t(a.M); p.N = int32_t(a.N); p.K = int32_t(a.K);
     p.n = p.M < kTokens ? (p.M + 15) / 16 * 16 : kTokens;
     p.n_tiles = (p.N + kCols<kGated> - 1) / kCols<kGated>;
     p.k_iters = p.K / kK;
+    p.groups = a.groups;
+    p.group_m = a.group_m;
     p.bias = static_cast<const uint16_t*>(a.has_bias ? a.bias : nullptr);
     p.D = static_cast<uint16_t*>(a.D);
     p.aux = static_cast<uint16_t*>(a.aux);
@@ -395,7 +466,7 @@ te_mx_status launch(const GemmArgs& a, int sms, cudaStream_t stream) {
     // of K) per block; with several blocks of tokens, whose accumulators are
     // whole tiles to add up, at most four ways and past two only up to a block
     // per SM (512 x 1024 x 4096: 19 us eight ways, 10.6 four ways)
-    const int64_t tiles = int64_t(p.n_tiles) * ((p.M + kTokens - 1) / kTokens), groups = (p.k_iters + 3) / 4;
+    const int64_t tiles = int64_t(p.n_tiles) * token_blocks(p.M, p.groups), groups = (p.k_iters + 3) / 4;
     const bool few = p.M <= kTokens;
     p.split = 1;
     while (p.split < (few ? kMaxSplit : 4) && 2 * p.split <= groups &&
@@ -407,7 +478,7 @@ te_mx_status launch(const GemmArgs& a, int sms, cudaStream_t stream) {
 
     // (rows of scales are at least 16 bytes: their pitch is)
     const uint64_t K = uint64_t(p.K), sf_cols = uint64_t(p.K / 32) < 16 ? 16 : uint64_t(p.K / 32);
-    const uint64_t w_rows = uint64_t(p.N) * (kGated ? 2 : 1);
+    const uint64_t w_rows = uint64_t(p.N) * (kGated ? 2 : 1) * uint64_t(kGrouped ? p.groups : 1);
     CUtensorMap mw, mx, msw, msx;
     if ((st = encode_tensor_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, K, w_rows, K, kK, kCols<kGated>,
                                    CU_TENSOR_MAP_SWIZZLE_128B)) != TE_MX_OK) return st;
@@ -418,7 +489,7 @@ te_mx_status launch(const GemmArgs& a, int sms, cudaStream_t stream) {
     if ((st = encode_tensor_map_2d(&msx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.sA, sf_cols, uint64_t(p.M), uint64_t(a.ld_sA), 16,
                                    uint32_t(p.n), CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_MX_OK) return st;
 
-    auto kern = split_gemm_kernel<kGated>;
+    auto kern = split_gemm_kernel<kGated, kGrouped>;
     cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kSmemBytes);
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(split GEMM)");
     cudaLaunchConfig_t cfg = {};
@@ -441,7 +512,14 @@ te_mx_status launch(const GemmArgs& a, int sms, cudaStream_t stream) {
 }  // namespace
 
 bool split_gemm_takes(const GemmArgs& a, int sms) {
-    if (a.groups != 0 || a.wgrad || a.acc_f32 || a.f32_scales || a.gelu || a.dgelu) return false;
+    if (a.wgrad || a.acc_f32 || a.f32_scales || a.gelu || a.dgelu) return false;
+    // grouped: few tokens, in few enough blocks for the GPU to hold all at once
+    // (the sizes are on the device: as many as there can be).  Measured (us; here,
+    // the tiles of gemm.cu), 4096 -> 2 x 768: 1 token to 8 of 128 experts 14.0, 27.8;
+    // 32 rows of 8 experts 13.9, 19.4; 512 rows 19.3, 20.3; 1200 rows of 16 experts,
+    // 1024 -> 2 x 256: 11.4, 10.0
+    if (a.groups > 0)
+        return a.gated && a.M <= 4 * kTokens && token_blocks(a.M, a.groups) * ((a.N + kCols<true> - 1) / kCols<true>) <= 2 * int64_t(sms);
     // (a plain GEMM below 16 K-steps has its sums in one order in gemm.cu, and keeps it)
     if (!a.gated && a.K < 16 * kK) return false;
     if (a.M <= kTokens) return true;
@@ -452,7 +530,8 @@ bool split_gemm_takes(const GemmArgs& a, int sms) {
 }
 
 te_mx_status split_gemm_launch(const GemmArgs& a, int sms, cudaStream_t stream) {
-    return a.gated ? launch<true>(a, sms, stream) : launch<false>(a, sms, stream);
+    if (a.groups > 0) return launch<true, true>(a, sms, stream);
+    return a.gated ? launch<true, false>(a, sms, stream) : launch<false, false>(a, sms, stream);
 }
 
 }  // namespace temx
