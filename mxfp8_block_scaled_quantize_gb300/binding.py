@@ -693,18 +693,24 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
             assert t is None or (t.is_cuda and t.shape[0] == rows and cols in (None, t.shape[1])
                                  and t.element_size() == (2 if k == "d_gate_up" else 1)), k
         assert "q_row" not in o or o["q_row"].is_contiguous()
+    dev, u8, kp = dh.device, torch.uint8, (M + 127) // 128 * 128
     if dense and "d_gate_up" not in o:
-        o["d_gate_up"] = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=dh.device)
+        o["d_gate_up"] = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev)
     if rowwise and "q_row" not in o:
-        o["q_row"] = torch.empty(M, 2 * F, dtype=torch.uint8, device=dh.device)
-        o["s_row"] = torch.empty(M, te_mx_scale_pitch(2 * F), dtype=torch.uint8, device=dh.device)
+        o["q_row"] = torch.empty((M, 2 * F), dtype=u8, device=dev)
+        o["s_row"] = torch.empty((M, (F // 16 + 15) // 16 * 16), dtype=u8, device=dev)
     if colwise and "q_col" not in o:
-        kp = (M + 127) // 128 * 128
-        o["q_col"] = torch.empty(2 * F, kp, dtype=torch.uint8, device=dh.device)
-        o["s_col"] = torch.empty(2 * F, te_mx_scale_pitch(kp), dtype=torch.uint8, device=dh.device)
-    ld = lambda k: _pitch(o[k]) if k in o else 0  # noqa: E731
-    te_mx_gated_backward(dh.data_ptr(), _pitch(dh), gate_up.data_ptr(), _pitch(gate_up), M, F, ACTIVATIONS[activation],
-                         _ptr(o.get("d_gate_up")), ld("d_gate_up"), _ptr(o.get("q_row")), _ptr(o.get("s_row")),
-                         ld("s_row"), _ptr(o.get("q_col")), ld("q_col"), _ptr(o.get("s_col")), ld("s_col"),
-                         _raw_stream())
+        o["q_col"] = torch.empty((2 * F, kp), dtype=u8, device=dev)
+        o["s_col"] = torch.empty((2 * F, (kp // 32 + 15) // 16 * 16), dtype=u8, device=dev)
+    d = d_ld = q_row = s_row = s_row_ld = q_col = q_col_ld = s_col = s_col_ld = 0
+    if "d_gate_up" in o:
+        d, d_ld = o["d_gate_up"].data_ptr(), _pitch(o["d_gate_up"])
+    if "q_row" in o:
+        q_row, s_row, s_row_ld = o["q_row"].data_ptr(), o["s_row"].data_ptr(), _pitch(o["s_row"])
+    if "q_col" in o:
+        q_col, q_col_ld = o["q_col"].data_ptr(), _pitch(o["q_col"])
+        s_col, s_col_ld = o["s_col"].data_ptr(), _pitch(o["s_col"])
+    _check(lib().te_mx_gated_backward(dh.data_ptr(), _pitch(dh), gate_up.data_ptr(), _pitch(gate_up), M, F,
+                                      ACTIVATIONS[activation], d, d_ld, q_row, s_row, s_row_ld, q_col, q_col_ld, s_col,
+                                      s_col_ld, _raw_stream()))
     return o
