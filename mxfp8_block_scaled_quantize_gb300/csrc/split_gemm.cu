@@ -524,9 +524,13 @@ bool split_gemm_takes(const GemmArgs& a, int sms) {
     if (!a.gated && a.K < 16 * kK) return false;
     if (a.M <= kTokens) return true;
     // more tokens: while the tiles of gemm.cu (256 rows per pair of SMs, or 128
-    // per SM, by 256 accumulator columns) leave half of the SMs idle
+    // per SM, by 256 accumulator columns) leave half of the SMs idle, three
+    // quarters with fewer than 32 K-steps.  Measured (us; here, those tiles):
+    // plain 1000 x 2048 x 8192 23.4, 29.8; gated 512 tokens, 4096 -> 2 x 2048 17.6,
+    // 19.4, -> 2 x 4096 20.6, 21.6; 300 tokens, 1024 -> 2 x 1024 8.7, 10.4; 1000
+    // tokens 11.7, 10.6; plain 1000 x 2048 x 2048 13.0, 12.2
     const int64_t rows = a.M >= 256 ? 256 : 128, units = a.M >= 256 ? sms / 2 : sms, cols = a.gated ? 128 : 256;
-    return 2 * ((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols) <= units;
+    return (a.K >= 32 * kK ? 2 : 4) * ((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols) <= units;
 }
 
 te_mx_status split_gemm_launch(const GemmArgs& a, int sms, cudaStream_t stream) {
