@@ -224,6 +224,16 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
         }
         named_barrier_sync(1 + pair, 64);         // both tiles of the unit hold the gradient, dh is read
         if (ok && more && lane == 0 && half == 0) load_dh(next_band, next_strip);
+        // The slot's bytes of four rounds ago are written.  Every warp waits for that
+        // before it arrives on scales_full, with a unit or without: an arrival counts
+        // in the phase at hand, so a warp rounds ahead would complete it for the others.
+        // (Warps with a unit wait as late as they can: here 8192 x 18432 took 323 us, not 310.)
+        auto wait_slot = [&]() {
+            if (kRowwise && i >= kScaleSlots)
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&scales_empty[slot]), uint32_t(i / kScaleSlots - 1) & 1u,
+                                                             p.status));
+        };
+        if (!mine) wait_slot();
         if (ok && mine) {
             if (kDense && lane == 0) {
                 if (r0 < p.rows) tma_store_3d(&d_map, tile, int32_t(c0), half, int32_t(r0));
@@ -244,9 +254,7 @@ gated_backward_quantize_kernel(const __grid_constant__ CUtensorMap dh_map, const
                 }
             }
             if (kRowwise) {
-                if (i >= kScaleSlots)             // the slot's bytes of four rounds ago are written
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&scales_empty[slot]), uint32_t(i / kScaleSlots - 1) & 1u,
-                                                           p.status));
+                wait_slot();
 #pragma unroll
                 for (int rr = 0; rr < 2; ++rr) {
                     uint32_t sb[2];
