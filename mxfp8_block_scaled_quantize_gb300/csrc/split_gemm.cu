@@ -522,6 +522,16 @@ bool split_gemm_takes(const GemmArgs& a, int sms) {
         return a.gated && a.M <= 4 * kTokens && token_blocks(a.M, a.groups) * ((a.N + kCols<true> - 1) / kCols<true>) <= 2 * int64_t(sms);
     // (a plain GEMM below 16 K-steps has its sums in one order in gemm.cu, and keeps it)
     if (!a.gated && a.K < 16 * kK) return false;
+    // plain, 65 to 128 tokens at fewer than 28 K-steps, where a tile's start and join
+    // are not small beside its loop: with few tiles, split over K; with up to two
+    // per SM where those fill the SMs, or up to 96 tokens.  Measured (us; here, those
+    // tiles), K = 2048: 128 x 4096 10.5, 13.5; 128 x 8192 16.0, 14.1; 96 x 16384 13.9,
+    // 15.3; 128 x 32768 18.7, 20.1; 128 x 65536 36.2, 32.4; 96 x 131072 59.5, 56.7;
+    // K = 3584: 128 x 8192 17.6, 21.7; 128 x 65536 50.1, 51.3
+    if (!a.gated && a.M > 64 && a.M <= kTokens && a.K < 28 * kK) {
+        const int64_t tiles = (a.N + kCols<false> - 1) / kCols<false>;
+        return 4 * tiles <= sms || (tiles <= 2 * int64_t(sms) && (a.M <= 96 || tiles > sms));
+    }
     if (a.M <= kTokens) return true;
     // more tokens: while the tiles of gemm.cu (256 rows per pair of SMs, or 128
     // per SM, by 256 accumulator columns) leave half of the SMs idle, three
