@@ -392,9 +392,10 @@ def _pitch(t) -> int:
     return ld if rows > 1 else max(ld, cols)
 
 
-def _vectors(a, b, n: int, dtype) -> bool:
-    """Whether a, and b if given, are contiguous CUDA vectors of n elements of that type."""
-    return all(t is None or (t.shape == (n,) and t.dtype == dtype and t.is_contiguous() and t.is_cuda) for t in (a, b))
+def _vectors(a, b, n: int, dtype, device: int) -> bool:
+    """Whether a, and b if given, are contiguous vectors of n elements of that type on that CUDA device."""
+    return all(t is None or (t.shape == (n,) and t.dtype == dtype and t.is_contiguous() and t.get_device() == device)
+               for t in (a, b))
 
 
 def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream=None, out=None):
@@ -408,10 +409,12 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
     torch = _torch or _load_torch()
     shape = x.shape
     rows, hidden = shape
-    assert x.is_cuda and gamma.is_cuda and gamma.shape == shape[1:] and gamma.is_contiguous()
+    device = x.get_device()
+    assert device >= 0 and gamma.get_device() == device and gamma.shape == shape[1:] and gamma.is_contiguous()
     b = 0
     if beta is not None:
-        assert beta.dtype == gamma.dtype and beta.shape == gamma.shape and beta.is_contiguous()
+        assert (beta.dtype == gamma.dtype and beta.shape == gamma.shape and beta.is_contiguous()
+                and beta.get_device() == device)
         b = beta.data_ptr()
     if out is None:
         y, ld_y = torch.empty_like(x, memory_format=torch.contiguous_format), hidden
@@ -421,9 +424,9 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
         if "y" not in o:
             o["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
         y, ld_y = o["y"], _pitch(o["y"])
-        assert y.shape == shape and y.dtype == x.dtype
+        assert y.shape == shape and y.dtype == x.dtype and y.get_device() == device
         if "mu" in o:
-            assert _vectors(o["mu"], o["rsigma"], rows, torch.float32)
+            assert _vectors(o["mu"], o["rsigma"], rows, torch.float32, device)
     mu = rsigma = 0
     if stats and "mu" not in o:
         o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
@@ -447,9 +450,11 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
     torch = _torch or _load_torch()
     shape, dt = x.shape, _dtype_code[x.dtype]
     rows, hidden = shape
-    assert x.is_cuda and dy.is_cuda and dy.shape == shape and dy.dtype == x.dtype
+    device = x.get_device()
+    assert device >= 0 and dy.get_device() == device and dy.shape == shape and dy.dtype == x.dtype
     assert gamma.shape == shape[1:] and gamma.is_contiguous() and mu.shape == rsigma.shape == shape[:1]
     assert mu.is_contiguous() and rsigma.is_contiguous() and mu.dtype == rsigma.dtype == torch.float32
+    assert gamma.get_device() == mu.get_device() == rsigma.get_device() == device
     if out is None:
         dx, ld_dx = torch.empty_like(x, memory_format=torch.contiguous_format), hidden
         o = {"dx": dx}
@@ -458,9 +463,9 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
         if "dx" not in o:
             o["dx"] = torch.empty_like(x, memory_format=torch.contiguous_format)
         dx, ld_dx = o["dx"], _pitch(o["dx"])
-        assert dx.shape == shape and dx.dtype == x.dtype
+        assert dx.shape == shape and dx.dtype == x.dtype and dx.get_device() == device
         if "dgamma" in o:
-            assert _vectors(o["dgamma"], o.get("dbeta"), hidden, gamma.dtype)
+            assert _vectors(o["dgamma"], o.get("dbeta"), hidden, gamma.dtype, device)
     dga = dbe = ws = size = 0
     if dparams and "dgamma" not in o:
         o["dgamma"], o["dbeta"] = torch.empty_like(gamma), torch.empty_like(gamma)
@@ -469,6 +474,8 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
         if workspace is None:
             workspace = torch.empty(lib().te_mx_layernorm_backward_workspace_size(rows, hidden), dtype=torch.uint8,
                                     device=x.device)
+        else:
+            assert workspace.get_device() == device and workspace.is_contiguous()
         ws, size = workspace.data_ptr(), workspace.numel()
     _check(lib().te_mx_layernorm_backward(dy.data_ptr(), _pitch(dy), x.data_ptr(), _pitch(x), rows, hidden, dt,
                                           gamma.data_ptr(), _dtype_code[gamma.dtype], mu.data_ptr(), rsigma.data_ptr(),
@@ -605,13 +612,18 @@ def grouped_gemm(group_m, qx, sx, qw, sw, bias=None, gelu: bool = False, stream=
     return d, aux
 
 
-def _mx_operand(q, s, rows: int) -> bool:
-    """Whether q and s are an MXFP8 operand's contiguous codes and scale rows."""
-    return q.is_contiguous() and q.is_cuda and s.is_cuda and s.shape[0] == rows and q.element_size() == s.element_size() == 1
+def _mx_operand(q, s, rows: int, device: int) -> bool:
+    """Whether q and s are an MXFP8 operand's contiguous codes and scale rows on that CUDA device."""
+    return (q.is_contiguous() and q.get_device() == s.get_device() == device and s.shape[0] == rows
+            and q.element_size() == s.element_size() == 1)
 
 
-def _matrix(t, rows: int, cols: int, dtype) -> bool:
-    return t is None or (t.shape == (rows, cols) and t.dtype == dtype and t.is_contiguous() and t.is_cuda)
+def _matrix(t, rows: int, cols: int, dtype, device: int) -> bool:
+    return t is None or (t.shape == (rows, cols) and t.dtype == dtype and t.is_contiguous() and t.get_device() == device)
+
+
+def _bias(t, n: int, dtype, device: int) -> bool:
+    return t is None or (t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.get_device() == device)
 
 
 def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = False, stream=None, out=None):
@@ -626,14 +638,15 @@ def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = 
     torch = _torch or _load_torch()
     M, K = qx.shape
     F = qw.shape[0] // 2
-    assert qw.shape == (2 * F, K) and _mx_operand(qx, sx, M) and _mx_operand(qw, sw, 2 * F)
-    assert bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == 2 * F and bias.is_contiguous())
+    device = qx.get_device()
+    assert device >= 0 and qw.shape == (2 * F, K) and _mx_operand(qx, sx, M, device) and _mx_operand(qw, sw, 2 * F, device)
+    assert _bias(bias, 2 * F, torch.bfloat16, device)
     if out is None:
         h = torch.empty(M, F, dtype=torch.bfloat16, device=qx.device)
         pre = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=qx.device) if aux else None
     else:
         h, pre = out
-        assert _matrix(h, M, F, torch.bfloat16) and _matrix(pre, M, 2 * F, torch.bfloat16)
+        assert _matrix(h, M, F, torch.bfloat16, device) and _matrix(pre, M, 2 * F, torch.bfloat16, device)
     te_mx_gated_gemm(qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(), sw.data_ptr(), _pitch(sw), M, F, K,
                      _ptr(bias), ACTIVATIONS[activation], h.data_ptr(), _ptr(pre), _raw_stream())
     return h, pre
@@ -653,14 +666,16 @@ def grouped_gated_gemm(group_m, qx, sx, qw, sw, activation: str = "silu", bias=N
     G, N, _ = qw.shape
     sw2 = sw.reshape(G * N, -1)
     assert group_m.dtype == torch.int32 and group_m.numel() == G and N % 2 == 0 and qw.shape[2] == K
-    assert group_m.is_cuda and group_m.is_contiguous() and _mx_operand(qx, sx, total_m) and _mx_operand(qw, sw2, G * N)
-    assert bias is None or (bias.dtype == torch.bfloat16 and bias.numel() == G * N and bias.is_contiguous())
+    device = qx.get_device()
+    assert device >= 0 and group_m.get_device() == device and group_m.is_contiguous()
+    assert _mx_operand(qx, sx, total_m, device) and _mx_operand(qw, sw2, G * N, device)
+    assert _bias(bias, G * N, torch.bfloat16, device)
     if out is None:
         h = torch.empty(total_m, N // 2, dtype=torch.bfloat16, device=qx.device)
         pre = torch.empty(total_m, N, dtype=torch.bfloat16, device=qx.device) if aux else None
     else:
         h, pre = out
-        assert _matrix(h, total_m, N // 2, torch.bfloat16) and _matrix(pre, total_m, N, torch.bfloat16)
+        assert _matrix(h, total_m, N // 2, torch.bfloat16, device) and _matrix(pre, total_m, N, torch.bfloat16, device)
     te_mx_grouped_gated_gemm(G, group_m.data_ptr(), total_m, qx.data_ptr(), sx.data_ptr(), _pitch(sx), qw.data_ptr(),
                              sw2.data_ptr(), _pitch(sw2), N // 2, K, _ptr(bias), ACTIVATIONS[activation], h.data_ptr(),
                              _ptr(pre), _raw_stream())
@@ -681,7 +696,9 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
             return gated_backward(dh, gate_up, activation=activation, dense=dense, rowwise=rowwise, colwise=colwise,
                                   out=out)
     torch = _torch or _load_torch()
-    assert dh.dtype == gate_up.dtype == torch.bfloat16 and dh.dim() == gate_up.dim() == 2 and dh.is_cuda
+    device = dh.get_device()
+    assert dh.dtype == gate_up.dtype == torch.bfloat16 and dh.dim() == gate_up.dim() == 2
+    assert device >= 0 and gate_up.get_device() == device
     M, F = dh.shape
     assert gate_up.shape == (M, 2 * F) and dh.stride(1) == gate_up.stride(1) == 1
     o = dict(out or {})
@@ -690,7 +707,7 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
                   "s_col": (2 * F, None)}
         for k, (rows, cols) in shapes.items():
             t = o.get(k)
-            assert t is None or (t.is_cuda and t.shape[0] == rows and cols in (None, t.shape[1])
+            assert t is None or (t.get_device() == device and t.shape[0] == rows and cols in (None, t.shape[1])
                                  and t.element_size() == (2 if k == "d_gate_up" else 1)), k
         assert "q_row" not in o or o["q_row"].is_contiguous()
     dev, u8, kp = dh.device, torch.uint8, (M + 127) // 128 * 128
