@@ -613,13 +613,21 @@ def grouped_gemm(group_m, qx, sx, qw, sw, bias=None, gelu: bool = False, stream=
 
 
 def _mx_operand(q, s, rows: int, device: int) -> bool:
-    """Whether q and s are an MXFP8 operand's contiguous codes and scale rows on that CUDA device."""
+    """Whether q and s are an MXFP8 operand's contiguous codes and scale rows (a scale
+    per 32 codes, at least) on that CUDA device."""
     return (q.is_contiguous() and q.get_device() == s.get_device() == device and s.shape[0] == rows
-            and q.element_size() == s.element_size() == 1)
+            and 32 * s.shape[1] >= q.shape[-1] and q.element_size() == s.element_size() == 1)
 
 
 def _matrix(t, rows: int, cols: int, dtype, device: int) -> bool:
     return t is None or (t.shape == (rows, cols) and t.dtype == dtype and t.is_contiguous() and t.get_device() == device)
+
+
+def _bytes(t, rows: int, cols: int, device: int) -> bool:
+    """Whether t, if given, is a matrix of bytes on that CUDA device with that many
+    rows and at least so many columns (what it has more is left alone)."""
+    return t is None or (t.dim() == 2 and t.shape[0] == rows and t.shape[1] >= cols and t.element_size() == 1
+                         and t.get_device() == device)
 
 
 def _bias(t, n: int, dtype, device: int) -> bool:
@@ -702,15 +710,13 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
     M, F = dh.shape
     assert gate_up.shape == (M, 2 * F) and dh.stride(1) == gate_up.stride(1) == 1
     o = dict(out or {})
-    if o:
-        shapes = {"d_gate_up": (M, 2 * F), "q_row": (M, 2 * F), "s_row": (M, None), "q_col": (2 * F, None),
-                  "s_col": (2 * F, None)}
-        for k, (rows, cols) in shapes.items():
-            t = o.get(k)
-            assert t is None or (t.get_device() == device and t.shape[0] == rows and cols in (None, t.shape[1])
-                                 and t.element_size() == (2 if k == "d_gate_up" else 1)), k
-        assert "q_row" not in o or o["q_row"].is_contiguous()
     dev, u8, kp = dh.device, torch.uint8, (M + 127) // 128 * 128
+    if o:
+        d, q = o.get("d_gate_up"), o.get("q_row")
+        assert d is None or (d.shape == (M, 2 * F) and d.dtype == torch.bfloat16 and d.get_device() == device)
+        assert q is None or (q.shape == (M, 2 * F) and q.is_contiguous())
+        assert _bytes(q, M, 2 * F, device) and _bytes(o.get("s_row"), M, F // 16, device)
+        assert _bytes(o.get("q_col"), 2 * F, kp, device) and _bytes(o.get("s_col"), 2 * F, kp // 32, device)
     if dense and "d_gate_up" not in o:
         o["d_gate_up"] = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev)
     if rowwise and "q_row" not in o:

@@ -119,3 +119,37 @@ def test_operands_on_another_device_are_refused(op, i, lib):
         with pytest.raises(AssertionError):
             CALLS[op](**kw)
         assert not lib.launched
+
+
+# tensors that are too narrow for the call inside wider buffers, whose pitches
+# alone would do, and outputs of another type with the right size of element
+NARROW = {
+    "gated": [dict(s=u8(M, 16)[:, :3]), dict(sw=u8(2 * F, 16)[:, :3])],
+    "moe": [dict(s=u8(M, 16)[:, :3]), dict(sw=u8(4 * F, 16)[:, :3])],
+    "gated_bwd": [dict(out={"q_row": u8(M, 2 * F), "s_row": u8(M, 16)[:, :1]}),
+                  dict(out={"q_col": u8(2 * F, 128)[:, :112], "s_col": u8(2 * F, 16)}),
+                  dict(out={"q_col": u8(2 * F, 128), "s_col": u8(2 * F, 16)[:, :3]}),
+                  dict(dense=True, out={"d_gate_up": zeros(M, 2 * F, dtype=torch.float16)}),
+                  dict(dense=True, out={"d_gate_up": zeros(M, 4 * F)[:, :F]}),
+                  dict(out={"q_row": u8(M, 4 * F)[:, :2 * F], "s_row": u8(M, 16)})],
+}
+WIDE = {
+    "gated": [dict(s=u8(M, 32)[:, :4]), dict(sw=u8(2 * F, 48)[:, :16])],
+    "moe": [dict(s=u8(M, 32)[:, :5])],
+    "gated_bwd": [dict(out={"q_row": u8(M, 2 * F), "s_row": u8(M, 32)[:, :2]}),
+                  dict(out={"q_col": u8(2 * F, 160), "s_col": u8(2 * F, 16)[:, :4]}),
+                  dict(dense=True, out={"d_gate_up": zeros(M, 4 * F)[:, :2 * F]})],
+}
+
+
+@pytest.mark.parametrize("op,i", [(op, i) for op in sorted(NARROW) for i in range(len(NARROW[op]))])
+def test_views_narrower_than_the_call_are_refused(op, i, lib):
+    with pytest.raises(AssertionError):
+        CALLS[op](**NARROW[op][i])
+    assert not lib.launched
+
+
+@pytest.mark.parametrize("op,i", [(op, i) for op in sorted(WIDE) for i in range(len(WIDE[op]))])
+def test_views_of_the_call_s_width_are_taken(op, i, lib):
+    CALLS[op](**WIDE[op][i])
+    assert len(lib.launched) == 1
