@@ -425,12 +425,14 @@ def layernorm(x, gamma, beta=None, eps: float = 1e-5, stats: bool = True, stream
             o["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
         y, ld_y = o["y"], _pitch(o["y"])
         assert y.shape == shape and y.dtype == x.dtype and y.get_device() == device
-        if "mu" in o:
-            assert _vectors(o["mu"], o["rsigma"], rows, torch.float32, device)
+        assert stats or ("mu" in o) == ("rsigma" in o)     # (a lone one would be left unwritten)
+        assert _vectors(o.get("mu"), o.get("rsigma"), rows, torch.float32, device)
     mu = rsigma = 0
-    if stats and "mu" not in o:
-        o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
-        o["rsigma"] = torch.empty_like(o["mu"])
+    if stats:
+        if "mu" not in o:
+            o["mu"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if "rsigma" not in o:
+            o["rsigma"] = torch.empty_like(o["mu"])
     if "mu" in o:
         mu, rsigma = o["mu"].data_ptr(), o["rsigma"].data_ptr()
     _check(lib().te_mx_layernorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code[x.dtype], gamma.data_ptr(), b,
@@ -464,11 +466,14 @@ def layernorm_backward(dy, x, gamma, mu, rsigma, dparams: bool = True, stream=No
             o["dx"] = torch.empty_like(x, memory_format=torch.contiguous_format)
         dx, ld_dx = o["dx"], _pitch(o["dx"])
         assert dx.shape == shape and dx.dtype == x.dtype and dx.get_device() == device
-        if "dgamma" in o:
-            assert _vectors(o["dgamma"], o.get("dbeta"), hidden, gamma.dtype, device)
+        assert dparams or "dgamma" in o or "dbeta" not in o       # (a lone dbeta would be left unwritten)
+        assert _vectors(o.get("dgamma"), o.get("dbeta"), hidden, gamma.dtype, device)
     dga = dbe = ws = size = 0
-    if dparams and "dgamma" not in o:
-        o["dgamma"], o["dbeta"] = torch.empty_like(gamma), torch.empty_like(gamma)
+    if dparams:
+        if "dgamma" not in o:
+            o["dgamma"] = torch.empty_like(gamma)
+        if "dbeta" not in o:
+            o["dbeta"] = torch.empty_like(gamma)
     if "dgamma" in o:
         dga, dbe = o["dgamma"].data_ptr(), _ptr(o.get("dbeta"))
         if workspace is None:
@@ -717,14 +722,20 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
         assert q is None or (q.shape == (M, 2 * F) and q.is_contiguous())
         assert _bytes(q, M, 2 * F, device) and _bytes(o.get("s_row"), M, F // 16, device)
         assert _bytes(o.get("q_col"), 2 * F, kp, device) and _bytes(o.get("s_col"), 2 * F, kp // 32, device)
+        # (lone codes or scales would be left unwritten)
+        assert (rowwise or ("q_row" in o) == ("s_row" in o)) and (colwise or ("q_col" in o) == ("s_col" in o))
     if dense and "d_gate_up" not in o:
         o["d_gate_up"] = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev)
-    if rowwise and "q_row" not in o:
-        o["q_row"] = torch.empty((M, 2 * F), dtype=u8, device=dev)
-        o["s_row"] = torch.empty((M, (F // 16 + 15) // 16 * 16), dtype=u8, device=dev)
-    if colwise and "q_col" not in o:
-        o["q_col"] = torch.empty((2 * F, kp), dtype=u8, device=dev)
-        o["s_col"] = torch.empty((2 * F, (kp // 32 + 15) // 16 * 16), dtype=u8, device=dev)
+    if rowwise:
+        if "q_row" not in o:
+            o["q_row"] = torch.empty((M, 2 * F), dtype=u8, device=dev)
+        if "s_row" not in o:
+            o["s_row"] = torch.empty((M, (F // 16 + 15) // 16 * 16), dtype=u8, device=dev)
+    if colwise:
+        if "q_col" not in o:
+            o["q_col"] = torch.empty((2 * F, kp), dtype=u8, device=dev)
+        if "s_col" not in o:
+            o["s_col"] = torch.empty((2 * F, (kp // 32 + 15) // 16 * 16), dtype=u8, device=dev)
     d = d_ld = q_row = s_row = s_row_ld = q_col = q_col_ld = s_col = s_col_ld = 0
     if "d_gate_up" in o:
         d, d_ld = o["d_gate_up"].data_ptr(), _pitch(o["d_gate_up"])

@@ -153,3 +153,32 @@ def test_views_narrower_than_the_call_are_refused(op, i, lib):
 def test_views_of_the_call_s_width_are_taken(op, i, lib):
     CALLS[op](**WIDE[op][i])
     assert len(lib.launched) == 1
+
+
+# outputs that the library writes in pairs, one of them given
+LONE = {
+    "ln": [({"mu": f32(M)}, "stats"), ({"rsigma": f32(M)}, "stats")],
+    "ln_bwd": [({"dbeta": zeros(H)}, "dparams")],
+    "gated_bwd": [({"q_row": u8(M, 2 * F)}, "rowwise"), ({"s_row": u8(M, 16)}, "rowwise"),
+                  ({"q_col": u8(2 * F, 128)}, "colwise"), ({"s_col": u8(2 * F, 16)}, "colwise")],
+}
+PAIRS = {"stats": ("mu", "rsigma"), "dparams": ("dgamma", "dbeta"), "rowwise": ("q_row", "s_row"), "colwise": ("q_col", "s_col")}
+
+
+@pytest.mark.parametrize("op,i", [(op, i) for op in sorted(LONE) for i in range(len(LONE[op]))])
+def test_a_lone_output_is_kept_beside_a_new_one_or_refused(op, i, lib):
+    out, switch = LONE[op][i]
+    o = CALLS[op](out=out)
+    (name, t), = out.items()
+    assert o[name] is t and all(k in o for k in PAIRS[switch]) and len(lib.launched) == 1
+    with pytest.raises(AssertionError):
+        CALLS[op](out=out, **{switch: False})
+    assert len(lib.launched) == 1
+
+
+def test_a_given_dgamma_does_not_take_the_place_of_dbeta(lib):
+    g = zeros(H)
+    o = CALLS["ln_bwd"](out={"dgamma": g})
+    assert o["dgamma"] is g and o["dbeta"].shape == g.shape
+    o = CALLS["ln_bwd"](out={"dgamma": g}, dparams=False)      # (asked for by giving it; dbeta was not)
+    assert o["dgamma"] is g and "dbeta" not in o
