@@ -1175,7 +1175,7 @@ cudaError_t forward_vec(const LnArgs& a, int sms, unsigned int* status, cudaStre
     // vectors, so that two blocks fit on an SM (2000 x 16384 fp32: 45 us, four 67;
     // 515 x 16384: 17.9, 23.6), unless a block per SM is all there is (150 x
     // 16384: 9.2, four 7.8).
-    const int v = a.rows <= 304 && nvec <= 1024 ? 1 : nvec <= 64 ? 2 : nvec <= 2048 || (nvec <= 4096 && a.rows <= sms) ? 4 : 8;
+    const int v = a.rows <= 2 * sms && nvec <= 1024 ? 1 : nvec <= 64 ? 2 : nvec <= 2048 || (nvec <= 4096 && a.rows <= sms) ? 4 : 8;
     const int tx = ((nvec + v - 1) / v + 31) / 32 * 32, ty = tx == 32 ? 4 : 1;
     const dim3 grid(unsigned((a.rows + ty - 1) / ty)), block{unsigned(tx), unsigned(ty)};
     if (v == 1) return launch_dependent(ln_forward_vec_kernel<T, kP32, 1>, grid, block, stream, a, nvec);
@@ -1225,7 +1225,9 @@ cudaError_t backward_vec_launch(const LnBackwardArgs& a, const LnBwdShape& sh, i
     auto kern = ln_backward_vec_kernel<T, kP32, kCluster>;
     cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kBwdSmem);
     if (e != cudaSuccess) return e;
-    const int64_t want = (a.rows + sh.groups - 1) / sh.groups, most = sms / sh.cluster;
+    const int64_t want = (a.rows + sh.groups - 1) / sh.groups;
+    int64_t most = sms / sh.cluster;
+    if (most > ln_backward_parts(a.rows)) most = ln_backward_parts(a.rows);        // (the workspace's rows)
     *parts = int(want < most ? want : most);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(*parts * sh.cluster));
