@@ -617,11 +617,12 @@ def grouped_gemm(group_m, qx, sx, qw, sw, bias=None, gelu: bool = False, stream=
     return d, aux
 
 
-def _mx_operand(q, s, rows: int, device: int) -> bool:
+def _mx_operand(q, s, rows: int, cols: int, device: int) -> bool:
     """Whether q and s are an MXFP8 operand's contiguous codes and scale rows (a scale
     per 32 codes, at least) on that CUDA device."""
-    return (q.is_contiguous() and q.get_device() == s.get_device() == device and s.shape[0] == rows
-            and 32 * s.shape[1] >= q.shape[-1] and q.element_size() == s.element_size() == 1)
+    n, width = s.shape
+    return (n == rows and 32 * width >= cols and q.get_device() == s.get_device() == device
+            and q.is_contiguous() and q.element_size() == s.element_size() == 1)
 
 
 def _matrix(t, rows: int, cols: int, dtype, device: int) -> bool:
@@ -636,7 +637,7 @@ def _bytes(t, rows: int, cols: int, device: int) -> bool:
 
 
 def _bias(t, n: int, dtype, device: int) -> bool:
-    return t is None or (t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.get_device() == device)
+    return t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.get_device() == device
 
 
 def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = False, stream=None, out=None):
@@ -652,8 +653,8 @@ def gated_gemm(qx, sx, qw, sw, activation: str = "silu", bias=None, aux: bool = 
     M, K = qx.shape
     F = qw.shape[0] // 2
     device = qx.get_device()
-    assert device >= 0 and qw.shape == (2 * F, K) and _mx_operand(qx, sx, M, device) and _mx_operand(qw, sw, 2 * F, device)
-    assert _bias(bias, 2 * F, torch.bfloat16, device)
+    assert device >= 0 and qw.shape == (2 * F, K) and _mx_operand(qx, sx, M, K, device) and _mx_operand(qw, sw, 2 * F, K, device)
+    assert bias is None or _bias(bias, 2 * F, torch.bfloat16, device)
     if out is None:
         h = torch.empty(M, F, dtype=torch.bfloat16, device=qx.device)
         pre = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=qx.device) if aux else None
@@ -681,8 +682,8 @@ def grouped_gated_gemm(group_m, qx, sx, qw, sw, activation: str = "silu", bias=N
     assert group_m.dtype == torch.int32 and group_m.numel() == G and N % 2 == 0 and qw.shape[2] == K
     device = qx.get_device()
     assert device >= 0 and group_m.get_device() == device and group_m.is_contiguous()
-    assert _mx_operand(qx, sx, total_m, device) and _mx_operand(qw, sw2, G * N, device)
-    assert _bias(bias, G * N, torch.bfloat16, device)
+    assert _mx_operand(qx, sx, total_m, K, device) and _mx_operand(qw, sw2, G * N, K, device)
+    assert bias is None or _bias(bias, G * N, torch.bfloat16, device)
     if out is None:
         h = torch.empty(total_m, N // 2, dtype=torch.bfloat16, device=qx.device)
         pre = torch.empty(total_m, N, dtype=torch.bfloat16, device=qx.device) if aux else None
