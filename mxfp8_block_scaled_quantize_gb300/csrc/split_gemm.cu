@@ -313,7 +313,9 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             slot = next_slot;
             sf_phase = next_sf_phase;
         }
-        if (ok) tc_commit_if(smem_u32(&sh.acc_full), issue);
+        tc_commit_if(smem_u32(&sh.acc_full), issue);
+        if (!ok && lane == 0)                            // gave up: let the MMAs in flight end before TMEM is freed
+            mbar_wait(smem_u32(&sh.acc_full), 0, p.status, 1000000ull);
     } else if (warp == 2) {
         // ------------------------------------------------ scale factors
         auto load = [&](int32_t j) {                     // group j (of this block), by lane 0
@@ -360,6 +362,9 @@ split_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             }
             if (!ok) break;
         }
+        if (sh.abort && lane == 0)                       // gave up: let the scale loads in flight land
+            for (int i = 0; i < kSfSlots; ++i)
+                for (uint32_t q = 0; q < 2; ++q) mbar_wait(smem_u32(&sh.sf_full[i]), q, p.status, 1000000ull);
     } else if (warp >= 4) {
         // ------------------------------------------------ accumulator -> [token][row] fp32
         if (__all_sync(0xFFFFFFFFu, wait_or_abort(sh.acc_full, 0, sh, p.status))) {
