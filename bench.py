@@ -47,7 +47,9 @@ def load_peaks():
         return {"hbm_gbs": 6800.0, "bf16": 1900.0, "bf16_sustained": 1700.0, "source": "fallback"}
 
 
-KERNEL_SOURCES = {"gemm": ["gemm.cu", "ptx.cuh", "tcgen05.cuh"], "quant": ["quantize.cu", "e4m3.cuh", "ptx.cuh", "units.cuh"],
+# Sources behind the bench kernels' names, with what they include (te_mx_gemm may run either GEMM kernel).
+KERNEL_SOURCES = {"gemm": ["gemm.cu", "split_gemm.cu", "ptx.cuh", "tcgen05.cuh", "e4m3.cuh", "f32x2.cuh", "gated_act.cuh"],
+                  "quant": ["quantize.cu", "e4m3.cuh", "mx_unit.cuh", "ptx.cuh", "units.cuh"],
                   "grouped": ["grouped_quantize.cu", "e4m3.cuh", "ptx.cuh", "units.cuh"],
                   "block": ["block_quantize.cu", "e4m3.cuh", "ptx.cuh"],
                   "ln": ["layernorm_quantize.cu", "e4m3.cuh", "ptx.cuh", "units.cuh"]}
