@@ -260,7 +260,9 @@ typedef enum te_mx_dtype { TE_MX_BF16 = 0, TE_MX_FP16 = 1, TE_MX_FP32 = 2 } te_m
  *   mu, rsigma  fp32 [rows], for the backward pass; both NULL: not written.
  * Pointers aligned to their elements; any hidden <= 2^24 and any pitches >=
  * hidden (rows that start on 16-byte boundaries are read and written 16 bytes
- * at a time); rows == 0 or hidden == 0 is a no-op.  Deterministic. */
+ * at a time); rows == 0 or hidden == 0 is a no-op.  Deterministic: a call
+ * repeats its bits.  The order of the sums follows from the sizes, the types and
+ * the rows' alignment, so other pitches can give other last bits. */
 TEMX_API te_mx_status te_mx_layernorm(const void* x, int64_t rows, int64_t hidden, int64_t ld_x, int32_t dtype,
                                       const void* gamma, const void* beta, int32_t param_dtype, float eps,
                                       void* y, int64_t ld_y, float* mu, float* rsigma, void* stream);
@@ -278,9 +280,10 @@ TEMX_API te_mx_status te_mx_layernorm(const void* x, int64_t rows, int64_t hidde
  *   workspace  device scratch of te_mx_layernorm_backward_workspace_size(rows,
  *              hidden) bytes, 16-byte aligned, for dgamma / dbeta (else NULL);
  *              its contents on entry do not matter and it is clobbered.
- * Types, alignment and sizes as te_mx_layernorm.  The column sums are taken in
- * a fixed order (deterministic).  TE_MX_ERR_WORKSPACE_TOO_SMALL if
- * workspace_bytes is short. */
+ * Types, alignment and sizes as te_mx_layernorm.  Deterministic, as there; the
+ * order of the sums also follows from whether dgamma is asked for and whether dx
+ * shares memory with dy or x.  TE_MX_ERR_WORKSPACE_TOO_SMALL if workspace_bytes
+ * is short. */
 TEMX_API size_t te_mx_layernorm_backward_workspace_size(int64_t rows, int64_t hidden);
 TEMX_API te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t rows,
                                                int64_t hidden, int32_t dtype, const void* gamma, int32_t param_dtype,

@@ -11,7 +11,7 @@
 //   dgamma = sum over the rows of dy xh,  dbeta = sum over the rows of dy.
 // x, y, dy and dx are bf16, fp16 or fp32; gamma, beta, dgamma and dbeta have
 // that type or fp32.  Everything between a load and a store is fp32; each
-// result is rounded once, when it is stored.  Sums are taken in a fixed order.
+// result is rounded once, when it is stored.  Each kernel adds in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
