@@ -1,0 +1,133 @@
+// What the row-wise kernels share: elements of bf16, fp16 and fp32 as fp32,
+// 16-byte vectors of them as packed fp32 pairs, parameters, warp sums, and
+// launches that overlap the end of the kernel before.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "f32x2.cuh"
+#include "temx_internal.h"
+
+namespace temx {
+
+// ---------------------------------------------------------------- elements
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Element i of a parameter array of type P.
+template <typename P> __device__ __forceinline__ float load_param(const void* p, int64_t i) {
+    return to_f32(static_cast<const P*>(p)[i]);
+}
+__device__ __forceinline__ void store_param(void* p, int dt, int64_t i, float v) {
+    if (dt == TE_MX_FP32) static_cast<float*>(p)[i] = v;
+    else if (dt == TE_MX_FP16) static_cast<__half*>(p)[i] = from_f32<__half>(v);
+    else static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v);
+}
+
+// Warp sum in a fixed butterfly order (every lane gets the same value).
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- 16-byte vectors
+
+// A 16-byte vector of T as kPairs packed fp32 pairs, and back (one rounding).
+template <typename T> struct Vec {
+    static constexpr int kN = 16 / sizeof(T), kPairs = kN / 2;
+    static __device__ __forceinline__ uint64_t pair(const uint4& v, int i) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (sizeof(T) == 4) {
+            return f32x2::pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            return f32x2::pack(f.x, f.y);
+        } else {
+            return f32x2::pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        }
+    }
+    static __device__ __forceinline__ uint4 from_pairs(const uint64_t (&p)[kPairs]) {
+        uint32_t w[4];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                w[2 * i] = uint32_t(p[i]);
+                w[2 * i + 1] = uint32_t(p[i] >> 32);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (std::is_same<T, __half>::value)
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f32x2::hi(p[i])), "f"(f32x2::lo(p[i])));
+                else
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f32x2::hi(p[i])), "f"(f32x2::lo(p[i])));
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// The parameters of the vector's elements: kWords 16-byte loads (two when the
+// parameters are fp32 and the activations are not).
+template <typename T, bool kP32> struct ParamVec {
+    static constexpr int kWords = (kP32 && sizeof(T) == 2) ? 2 : 1;
+    uint4 w[kWords];
+    __device__ __forceinline__ void load(const void* p, int vec) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = __ldg(static_cast<const uint4*>(p) + vec * kWords + i);
+    }
+    __device__ __forceinline__ uint64_t pair(int i) const {
+        if constexpr (kWords == 2) return Vec<float>::pair(w[i >> 1], i & 1);
+        else return Vec<T>::pair(w[0], i);
+    }
+};
+
+// ---------------------------------------------------------------- blocks
+
+// Sizes and both addresses are multiples of 16 bytes; counted on the mbarrier `bar`.
+__device__ __forceinline__ void bulk_load_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+// Barrier `id` over `threads` threads (whole warps) of the block.
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+// ---------------------------------------------------------------- launches
+
+// Launch with programmatic stream serialisation: the blocks may start while
+// the previous kernel in the stream finishes (every kernel here waits for it
+// before its first access to global memory).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+inline bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// Rows of a matrix of elements of `size` bytes start on 16-byte boundaries.
+inline bool rows_on16(const void* p, int64_t ld, int64_t rows, size_t size) {
+    return on16(p) && (rows == 1 || ld * int64_t(size) % 16 == 0);
+}
+
+}  // namespace temx
