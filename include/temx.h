@@ -291,6 +291,169 @@ TEMX_API te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, co
                                                void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
                                                void* stream);
 
+/* te_mx_rmsnorm — root-mean-square norm with the residual's addition (the pre-norm
+ * blocks that scale by the root mean square alone; te.RMSNorm beside te.LayerNorm,
+ * leeroopedia "FP8 Training Quickstart").  Per row r:
+ *   z[r] = x[r] + residual[r], rounded to `dtype` (z = x if residual is NULL),
+ *   rsigma[r] = 1/sqrt(mean(z[r]^2) + eps),  y = (z rsigma) gamma,
+ * in fp32, y rounded once.  z is what the next layer and the backward pass read.
+ *   x, residual  [rows x hidden] of `dtype`, row pitches ld_x, ld_residual (device);
+ *   gamma   [hidden] of `param_dtype`, which is `dtype` or TE_MX_FP32;
+ *   z       [rows x hidden] of `dtype`, pitch ld_z: given with residual, else NULL;
+ *   y       [rows x hidden] of `dtype`, pitch ld_y;
+ *   rsigma  fp32 [rows] or NULL: for the backward pass.
+ * z may be x or residual, and y x or residual (the same pointer and pitch); other
+ * overlaps of an output are refused (TE_MX_ERR_INVALID_ARG).  Pointers aligned to
+ * their elements; any hidden <= 2^24 and any pitches >= hidden (rows that start on
+ * 16-byte boundaries are read and written 16 bytes at a time); rows == 0 or hidden
+ * == 0 is a no-op.  Deterministic, as te_mx_layernorm. */
+TEMX_API te_mx_status te_mx_rmsnorm(const void* x, int64_t rows, int64_t hidden, int64_t ld_x, int32_t dtype,
+                                    const void* residual, int64_t ld_residual, const void* gamma, int32_t param_dtype,
+                                    float eps, void* z, int64_t ld_z, void* y, int64_t ld_y, float* rsigma,
+                                    void* stream);
+
+/* te_mx_rmsnorm_quantize — te_mx_rmsnorm of bf16 with an MXFP8 output: y, unrounded,
+ * is quantised exactly as te_mx_quantize quantises its input, so codes and scales are
+ * the exact MXFP8 quantisation of fl(fl(z rsigma) gamma) in fp32.
+ *   x, residual, z  bf16, as there, on 16-byte boundaries with pitches % 8 == 0;
+ *   gamma   [hidden] of `param_dtype`, TE_MX_BF16 or TE_MX_FP32, 16-byte aligned;
+ *   y       bf16 [rows x hidden], pitch ld_y, or NULL (not written); where no residual
+ *           is given and q_col is, y may not be x;
+ *   q_row/s_row, q_col/s_col  as te_mx_quantize (either pair may be NULL);
+ *   rsigma  fp32 [rows] (required).
+ * Rules: hidden % 32 == 0 and hidden <= 32768; rows % 32 == 0 when q_col is given;
+ * rows == 0 or hidden == 0 is a no-op. */
+TEMX_API te_mx_status te_mx_rmsnorm_quantize(const void* x, int64_t rows, int64_t hidden, int64_t ld_x,
+                                             const void* residual, int64_t ld_residual, const void* gamma,
+                                             int32_t param_dtype, float eps, void* z, int64_t ld_z, void* y, int64_t ld_y,
+                                             uint8_t* q_row, uint8_t* s_row, int64_t ld_s_row,
+                                             uint8_t* q_col, uint8_t* s_col, int64_t ld_s_col,
+                                             float* rsigma, void* stream);
+
+/* te_mx_rmsnorm_backward — gradients of te_mx_rmsnorm and te_mx_rmsnorm_quantize.
+ * With xh = z rsigma and g = dy gamma:
+ *   dx = rsigma (g - xh mean(g xh)) + dz    per row: of x and of the residual alike,
+ *   dgamma[c] = sum_r dy[r][c] xh[r][c],
+ * in fp32, each result rounded once.
+ *   dy, z   [rows x hidden] of `dtype`, pitches ld_dy, ld_z;
+ *   dz      [rows x hidden], pitch ld_dz: the gradient that reaches z by the residual
+ *           path, or NULL (zero);
+ *   dx      [rows x hidden], pitch ld_dx, or NULL (not computed); may be dy, z or dz
+ *           (the same pointer and pitch); other overlaps are refused;
+ *   dgamma  [hidden] of `param_dtype`, or NULL.  With rows == 0 it is set to zero;
+ *   workspace  device scratch of te_mx_rmsnorm_backward_workspace_size(rows, hidden)
+ *           bytes, 16-byte aligned, for dgamma (else NULL); its contents on entry do
+ *           not matter and it is clobbered.
+ * Types, alignment and sizes as te_mx_rmsnorm.  Deterministic, as te_mx_layernorm_backward.
+ * TE_MX_ERR_WORKSPACE_TOO_SMALL if workspace_bytes is short. */
+TEMX_API size_t te_mx_rmsnorm_backward_workspace_size(int64_t rows, int64_t hidden);
+TEMX_API te_mx_status te_mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* z, int64_t ld_z, int64_t rows,
+                                             int64_t hidden, int32_t dtype, const void* gamma, int32_t param_dtype,
+                                             const float* rsigma, const void* dz, int64_t ld_dz, void* dx, int64_t ld_dx,
+                                             void* dgamma, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scores of the router: the softmax of a token's logits over the experts, or the
+ * logistic function 1 / (1 + e^-x) of each. */
+typedef enum te_mx_scoring { TE_MX_SCORE_SOFTMAX = 0, TE_MX_SCORE_SIGMOID = 1 } te_mx_scoring;
+
+/* te_mx_route — the k experts of each token and their weights (what routing hands to
+ * the grouped GEMMs, "Single-Launch Grouped GEMM Backends on ROCm",
+ * ROCm/TransformerEngine README).  Per token, with key[e] = fl32(logit[e] + bias[e])
+ * (the logit itself without a bias):
+ *   index   the k largest keys in falling order, ties to the lowest expert;
+ *   weight  scale * p[index], p the scores of the logits (the bias only chooses);
+ *           renormalise = 1: scale * p[index] / sum over the chosen of p.
+ *   logits  [tokens x experts] of `dtype`, pitch ld_logits >= experts (device);
+ *   bias    fp32 [experts] or NULL;
+ *   index   int32 [tokens x k];  weight  fp32 [tokens x k].
+ * An expert masked with -inf has the score 0, and is chosen only after all others;
+ * where the scores to divide by sum to 0 the weights are 0.  A NaN logit is chosen
+ * last, and NaN or +inf logits give weights as the formula does.  The k indices of a
+ * token always differ.  Rules: 1 <= k <= 32, k <= experts <= 1024, tokens * k < 2^31;
+ * pointers aligned to their elements; scale finite; tokens == 0 is a no-op. */
+TEMX_API te_mx_status te_mx_route(const void* logits, int64_t tokens, int32_t experts, int64_t ld_logits, int32_t dtype,
+                                  const float* bias, int32_t k, int32_t scoring, int32_t renormalise, float scale,
+                                  int32_t* index, float* weight, void* stream);
+
+/* te_mx_route_backward — the gradient of te_mx_route's logits from that of its
+ * weights (the choice itself has none).
+ *   dweight  fp32 [tokens x k];  logits, index and the options as in the forward call;
+ *            an index outside the experts (a choice dropped since) takes no part; the
+ *            others of a token differ;
+ *   dlogits  [tokens x experts] of `dtype`, pitch ld_dlogits: every element is written;
+ *            may not overlap logits. */
+TEMX_API te_mx_status te_mx_route_backward(const float* dweight, const void* logits, int64_t ld_logits,
+                                           const int32_t* index, int64_t tokens, int32_t experts, int32_t dtype, int32_t k,
+                                           int32_t scoring, int32_t renormalise, float scale, void* dlogits,
+                                           int64_t ld_dlogits, void* stream);
+
+/* te_mx_moe_sort — slots sorted by expert: where the grouped GEMMs' rows come from.
+ * Slot s = token * k + j is a token's j-th choice; its row is its place in a stable
+ * sort of the slots by expert.
+ *   index    int32 [slots]: the expert of each slot; a negative one has no row (the
+ *            padding of a batch, a dropped choice);
+ *   group_m  int32 [experts]: rows of each expert (te_mx_grouped_gemm's group_m);
+ *   row      int32 [slots]: the row of each slot, -1 without one;
+ *   slot     int32 [slots]: the slot of each row; -1 behind the last row.
+ * An index >= experts has no row, and makes te_mx_device_status() report
+ * TE_MX_ERR_INVALID_ARG.  One launch, no workspace.  Rules: 1 <= experts <= 1024,
+ * 0 <= slots < 2^31; the arrays do not overlap. */
+TEMX_API te_mx_status te_mx_moe_sort(const int32_t* index, int64_t slots, int32_t experts, int32_t* group_m,
+                                     int32_t* row, int32_t* slot, void* stream);
+
+/* te_mx_moe_dispatch — every token's row copied to the rows of its slots:
+ *   out[row[t][j]] = x[t]  (and out_scales[row[t][j]] = scales[t]).
+ * Rows are bytes: of any type, or MXFP8 codes with their scale bytes, so that a token
+ * is quantised once for all its experts.
+ *   x    [tokens] rows of row_bytes bytes, pitch ld_x bytes;
+ *   scales  [tokens] rows of scale_bytes bytes, pitch ld_scales, or NULL (then
+ *        scale_bytes and ld_scales are ignored, and out_scales is NULL);
+ *   row  int32 [tokens x k], no row twice; a negative one is skipped;
+ *   out  [total_rows] rows of row_bytes, pitch ld_out;  out_scales likewise.
+ * Rows of out that no slot has, and bytes past row_bytes and scale_bytes, are not
+ * written.  A row >= total_rows is skipped and makes te_mx_device_status() report
+ * TE_MX_ERR_INVALID_ARG.  Any alignment (rows on 16-byte boundaries are copied 16
+ * bytes at a time).  Its gradient is te_mx_moe_combine without weights.  Rules:
+ * 1 <= k <= 32; tokens * k < 2^31; tokens * row_bytes <= 2^39; out does not overlap x. */
+TEMX_API te_mx_status te_mx_moe_dispatch(const void* x, int64_t ld_x, int64_t row_bytes, const uint8_t* scales,
+                                         int64_t ld_scales, int64_t scale_bytes, const int32_t* row, int64_t tokens,
+                                         int32_t k, int64_t total_rows, void* out, int64_t ld_out, uint8_t* out_scales,
+                                         int64_t ld_out_scales, void* stream);
+
+/* te_mx_moe_combine — the experts' outputs added up for the tokens:
+ *   out[t] = sum_j weight[t][j] y[row[t][j]] + residual[t],
+ * in fp32 (the choices in order, then the residual), rounded once.
+ *   y    [total_rows x hidden] of `dtype`, pitch ld_y;
+ *   row  int32 [tokens x k]; a negative one is skipped, whatever its weight is;
+ *   weight    fp32 [tokens x k], or NULL (all 1: the gradient of te_mx_moe_dispatch);
+ *   residual  [tokens x hidden], pitch ld_residual, or NULL;
+ *   out       [tokens x hidden], pitch ld_out; may be residual (the same pointer and
+ *             pitch), other overlaps are refused.
+ * A row >= total_rows is skipped and makes te_mx_device_status() report
+ * TE_MX_ERR_INVALID_ARG.  Rules: dtype a te_mx_dtype; 1 <= k <= 32; tokens * k < 2^31;
+ * hidden <= 2^24; tokens * hidden <= 2^38; pointers aligned to their elements; tokens
+ * == 0 or hidden == 0 is a no-op. */
+TEMX_API te_mx_status te_mx_moe_combine(const void* y, int64_t ld_y, int64_t total_rows, int64_t hidden, int32_t dtype,
+                                        const int32_t* row, int64_t tokens, int32_t k, const float* weight,
+                                        const void* residual, int64_t ld_residual, void* out, int64_t ld_out,
+                                        void* stream);
+
+/* te_mx_moe_combine_backward — gradients of te_mx_moe_combine (the residual's is
+ * dout itself):
+ *   dy[row[t][j]] = weight[t][j] dout[t],  dweight[t][j] = sum_c dout[t][c] y[row[t][j]][c].
+ *   dout  [tokens x hidden] of `dtype`, pitch ld_dout;  y, row, weight as there, no
+ *         row twice; weight is required;
+ *   dy    [total_rows x hidden], pitch ld_dy, or NULL (not computed); may be y (the
+ *         same pointer and pitch), other overlaps are refused.  Rows that no slot has
+ *         are not written;
+ *   dweight  fp32 [tokens x k], or NULL (not computed; y may then be NULL); 0 for a slot
+ *         without a row.
+ * Rules and device-side errors as te_mx_moe_combine. */
+TEMX_API te_mx_status te_mx_moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y,
+                                                 int64_t total_rows, int64_t hidden, int32_t dtype, const int32_t* row,
+                                                 const float* weight, int64_t tokens, int32_t k, void* dy, int64_t ld_dy,
+                                                 float* dweight, void* stream);
+
 /* te_mx_gemm — MXFP8 TN GEMM with fused epilogue (HipKittens MXFP8 GEMM
  * Support, PR description: MXFP8 GEMM with BIAS and GELU AUX epilogues; the
  * review thread's TN layout and its K % 128 rule for MXFP8 scaling):

@@ -22,6 +22,8 @@ STATUS_NAMES = {0: "TE_MX_OK", 1: "TE_MX_ERR_INVALID_ARG", 2: "TE_MX_ERR_UNSUPPO
 BF16, FP16, FP32 = 0, 1, 2                       # te_mx_dtype
 ACT_SILU, ACT_GELU, ACT_RELU = 0, 1, 2           # te_mx_activation
 ACTIVATIONS = {"silu": ACT_SILU, "gelu": ACT_GELU, "relu": ACT_RELU}
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1              # te_mx_scoring
+SCORINGS = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 EPI_NONE, EPI_BIAS, EPI_GELU_AUX, EPI_BIAS_GELU_AUX, EPI_DGELU, EPI_ACCUMULATE_F32 = 0, 1, 2, 3, 4, 5
 
 # (name, restype, argtypes) for every function declared in include/temx.h
@@ -38,6 +40,21 @@ SIGNATURES = {
     "te_mx_layernorm_backward_workspace_size": (_SZ, [_I64, _I64]),
     "te_mx_layernorm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _P, _P, _P, _I64, _P,
                                                 _P, _P, _SZ, _P]),
+    "te_mx_rmsnorm": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _I64, _P, _I32, ctypes.c_float, _P, _I64, _P, _I64, _P,
+                                     _P]),
+    "te_mx_rmsnorm_quantize": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _I32, ctypes.c_float, _P, _I64, _P, _I64,
+                                              _P, _P, _I64, _P, _P, _I64, _P, _P]),
+    "te_mx_rmsnorm_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "te_mx_rmsnorm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _P, _P, _I64, _P, _I64, _P,
+                                              _P, _SZ, _P]),
+    "te_mx_route": (ctypes.c_int, [_P, _I64, _I32, _I64, _I32, _P, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
+    "te_mx_route_backward": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _I64,
+                                            _P]),
+    "te_mx_moe_sort": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _P, _P]),
+    "te_mx_moe_dispatch": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _I64, _P, _I64, _P, _I64, _P]),
+    "te_mx_moe_combine": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _I64, _I32, _P, _P, _I64, _P, _I64, _P]),
+    "te_mx_moe_combine_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _I64, _I32, _P, _I64, _P,
+                                                  _P]),
     "te_mx_grouped_code_width": (_I64, [_I64, _I32]),
     "te_mx_grouped_scale_width": (_I64, [_I64, _I32]),
     "te_mx_quantize_colwise_grouped": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _I64, _P]),
@@ -128,6 +145,62 @@ def te_mx_layernorm_backward(dy, ld_dy, x, ld_x, rows, hidden, dtype, gamma, par
                              dgamma, dbeta, workspace, workspace_bytes, stream) -> None:
     _check(lib().te_mx_layernorm_backward(dy, ld_dy, x, ld_x, rows, hidden, dtype, gamma, param_dtype, mu, rsigma, dx,
                                           ld_dx, dgamma, dbeta, workspace, workspace_bytes, stream))
+
+
+def te_mx_rmsnorm(x, rows, hidden, ld_x, dtype, residual, ld_residual, gamma, param_dtype, eps, z, ld_z, y, ld_y, rsigma,
+                  stream) -> None:
+    _check(lib().te_mx_rmsnorm(x, rows, hidden, ld_x, dtype, residual, ld_residual, gamma, param_dtype, eps, z, ld_z, y,
+                               ld_y, rsigma, stream))
+
+
+def te_mx_rmsnorm_quantize(x, rows, hidden, ld_x, residual, ld_residual, gamma, param_dtype, eps, z, ld_z, y, ld_y, q_row,
+                           s_row, ld_s_row, q_col, s_col, ld_s_col, rsigma, stream) -> None:
+    _check(lib().te_mx_rmsnorm_quantize(x, rows, hidden, ld_x, residual, ld_residual, gamma, param_dtype, eps, z, ld_z, y,
+                                        ld_y, q_row, s_row, ld_s_row, q_col, s_col, ld_s_col, rsigma, stream))
+
+
+def te_mx_rmsnorm_backward_workspace_size(rows, hidden) -> int:
+    return lib().te_mx_rmsnorm_backward_workspace_size(rows, hidden)
+
+
+def te_mx_rmsnorm_backward(dy, ld_dy, z, ld_z, rows, hidden, dtype, gamma, param_dtype, rsigma, dz, ld_dz, dx, ld_dx,
+                           dgamma, workspace, workspace_bytes, stream) -> None:
+    _check(lib().te_mx_rmsnorm_backward(dy, ld_dy, z, ld_z, rows, hidden, dtype, gamma, param_dtype, rsigma, dz, ld_dz, dx,
+                                        ld_dx, dgamma, workspace, workspace_bytes, stream))
+
+
+def te_mx_route(logits, tokens, experts, ld_logits, dtype, bias, k, scoring, renormalise, scale, index, weight,
+                stream) -> None:
+    _check(lib().te_mx_route(logits, tokens, experts, ld_logits, dtype, bias, k, scoring, renormalise, scale, index, weight,
+                             stream))
+
+
+def te_mx_route_backward(dweight, logits, ld_logits, index, tokens, experts, dtype, k, scoring, renormalise, scale, dlogits,
+                         ld_dlogits, stream) -> None:
+    _check(lib().te_mx_route_backward(dweight, logits, ld_logits, index, tokens, experts, dtype, k, scoring, renormalise,
+                                      scale, dlogits, ld_dlogits, stream))
+
+
+def te_mx_moe_sort(index, slots, experts, group_m, row, slot, stream) -> None:
+    _check(lib().te_mx_moe_sort(index, slots, experts, group_m, row, slot, stream))
+
+
+def te_mx_moe_dispatch(x, ld_x, row_bytes, scales, ld_scales, scale_bytes, row, tokens, k, total_rows, out, ld_out,
+                       out_scales, ld_out_scales, stream) -> None:
+    _check(lib().te_mx_moe_dispatch(x, ld_x, row_bytes, scales, ld_scales, scale_bytes, row, tokens, k, total_rows, out,
+                                    ld_out, out_scales, ld_out_scales, stream))
+
+
+def te_mx_moe_combine(y, ld_y, total_rows, hidden, dtype, row, tokens, k, weight, residual, ld_residual, out, ld_out,
+                      stream) -> None:
+    _check(lib().te_mx_moe_combine(y, ld_y, total_rows, hidden, dtype, row, tokens, k, weight, residual, ld_residual, out,
+                                   ld_out, stream))
+
+
+def te_mx_moe_combine_backward(dout, ld_dout, y, ld_y, total_rows, hidden, dtype, row, weight, tokens, k, dy, ld_dy,
+                               dweight, stream) -> None:
+    _check(lib().te_mx_moe_combine_backward(dout, ld_dout, y, ld_y, total_rows, hidden, dtype, row, weight, tokens, k, dy,
+                                            ld_dy, dweight, stream))
 
 
 def te_mx_grouped_code_width(total_m, num_groups) -> int:
@@ -237,6 +310,16 @@ def _raw_stream() -> int:
     else:
         _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
     return _raw_stream()
+
+
+def _current_device() -> int:
+    """The current CUDA device's index (the first call puts the function that
+    looks it up in this one's place)."""
+    global _current_device
+    import torch
+    torch.cuda.init()
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
 
 
 def _stream_ptr(stream=None) -> int:
@@ -748,4 +831,312 @@ def gated_backward(dh, gate_up, activation: str = "silu", dense: bool = False, r
     _check(lib().te_mx_gated_backward(dh.data_ptr(), _pitch(dh), gate_up.data_ptr(), _pitch(gate_up), M, F,
                                       ACTIVATIONS[activation], d, d_ld, q_row, s_row, s_row_ld, q_col, q_col_ld, s_col,
                                       s_col_ld, _raw_stream()))
+    return o
+
+
+def _like(t, shape, dtype, device: int) -> bool:
+    """Whether t, if given, is a 2-D tensor of that shape and type, its rows contiguous, on that CUDA device."""
+    return t is None or (t.shape == shape and t.dtype == dtype and t.get_device() == device)
+
+
+def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, stats: bool = True, stream=None, out=None):
+    """RMSNorm over the last axis of a 2-D bf16, fp16 or fp32 CUDA tensor, of
+    z = x + residual if one is given; gamma has its type or fp32.  Returns a dict
+    with "y" (the type of x), "z" (with a residual; the sum, rounded) and, with
+    ``stats``, "rsigma" (fp32 [rows]) for ``rmsnorm_backward``."""
+    if stream is not None:
+        with _on(stream):
+            return rmsnorm(x, gamma, eps=eps, residual=residual, stats=stats, out=out)
+    torch = _torch or _load_torch()
+    shape, dtype = x.shape, x.dtype
+    rows, hidden = shape
+    device = x.get_device()
+    assert device >= 0 and device == _current_device() and gamma.get_device() == device and gamma.shape == shape[1:] and gamma.is_contiguous()
+    o = {} if out is None else dict(out)
+    if o:
+        assert _like(o.get("y"), shape, dtype, device) and _like(o.get("z"), shape, dtype, device)
+        assert _vectors(o.get("rsigma"), None, rows, torch.float32, device)
+    if "y" not in o:
+        o["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+    res = ld_res = z = ld_z = rs = 0
+    if residual is not None:
+        assert _like(residual, shape, dtype, device)
+        if "z" not in o:
+            o["z"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+        res, ld_res, z, ld_z = residual.data_ptr(), _pitch(residual), o["z"].data_ptr(), _pitch(o["z"])
+    else:
+        assert "z" not in o                                    # (it would be left unwritten)
+    if stats and "rsigma" not in o:
+        o["rsigma"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if "rsigma" in o:
+        rs = o["rsigma"].data_ptr()
+    y = o["y"]
+    _check(lib().te_mx_rmsnorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code[dtype], res, ld_res, gamma.data_ptr(),
+                               _dtype_code[gamma.dtype], eps, z, ld_z, y.data_ptr(), _pitch(y), rs, _raw_stream()))
+    return o
+
+
+def rmsnorm_quantize(x, gamma, eps: float = 1e-5, residual=None, rowwise: bool = True, colwise: bool = False,
+                     dense: bool = False, stream=None, out=None):
+    """``rmsnorm`` of a 2-D bf16 CUDA tensor with its MXFP8 quantisation; gamma
+    has bf16 or fp32.  Returns a dict with q_row/s_row and/or q_col/s_col (as
+    ``quantize``), "rsigma" (fp32 [rows]), "z" (with a residual) and, with
+    ``dense``, "y" in bf16."""
+    if stream is not None:
+        with _on(stream):
+            return rmsnorm_quantize(x, gamma, eps=eps, residual=residual, rowwise=rowwise, colwise=colwise, dense=dense,
+                                    out=out)
+    torch = _torch or _load_torch()
+    shape, bf16, u8, dev = x.shape, torch.bfloat16, torch.uint8, x.device
+    rows, hidden = shape
+    device = x.get_device()
+    assert device >= 0 and device == _current_device() and x.dtype == bf16
+    assert gamma.get_device() == device and gamma.shape == shape[1:] and gamma.is_contiguous()
+    o = {} if out is None else dict(out)
+    if o:
+        q = o.get("q_row")
+        assert (rowwise or ("q_row" in o) == ("s_row" in o)) and (colwise or ("q_col" in o) == ("s_col" in o))
+        assert q is None or (q.shape == shape and q.is_contiguous())
+        assert _bytes(q, rows, hidden, device) and _bytes(o.get("s_row"), rows, hidden // 32, device)
+        q = o.get("q_col")
+        assert q is None or (q.shape == (hidden, rows) and q.is_contiguous())
+        assert _bytes(q, hidden, rows, device) and _bytes(o.get("s_col"), hidden, rows // 32, device)
+        assert _like(o.get("y"), shape, bf16, device) and _like(o.get("z"), shape, bf16, device)
+        assert _vectors(o.get("rsigma"), None, rows, torch.float32, device)
+    if rowwise:
+        if "q_row" not in o:
+            o["q_row"] = torch.empty(shape, dtype=u8, device=dev)
+        if "s_row" not in o:
+            o["s_row"] = torch.empty((rows, (hidden // 32 + 15) // 16 * 16), dtype=u8, device=dev)
+    if colwise:
+        if "q_col" not in o:
+            o["q_col"] = torch.empty((hidden, rows), dtype=u8, device=dev)
+        if "s_col" not in o:
+            o["s_col"] = torch.empty((hidden, (rows // 32 + 15) // 16 * 16), dtype=u8, device=dev)
+    if dense and "y" not in o:
+        o["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if "rsigma" not in o:
+        o["rsigma"] = torch.empty(rows, dtype=torch.float32, device=dev)
+    res = ld_res = z = ld_z = y = ld_y = q_row = s_row = ld_row = q_col = s_col = ld_col = 0
+    if residual is not None:
+        assert _like(residual, shape, bf16, device)
+        if "z" not in o:
+            o["z"] = torch.empty_like(x, memory_format=torch.contiguous_format)
+        res, ld_res, z, ld_z = residual.data_ptr(), _pitch(residual), o["z"].data_ptr(), _pitch(o["z"])
+    else:
+        assert "z" not in o                                    # (it would be left unwritten)
+    if "y" in o:
+        y, ld_y = o["y"].data_ptr(), _pitch(o["y"])
+    if "q_row" in o:
+        q_row, s_row, ld_row = o["q_row"].data_ptr(), o["s_row"].data_ptr(), _pitch(o["s_row"])
+    if "q_col" in o:
+        q_col, s_col, ld_col = o["q_col"].data_ptr(), o["s_col"].data_ptr(), _pitch(o["s_col"])
+    _check(lib().te_mx_rmsnorm_quantize(x.data_ptr(), rows, hidden, _pitch(x), res, ld_res, gamma.data_ptr(),
+                                        _dtype_code[gamma.dtype], eps, z, ld_z, y, ld_y, q_row, s_row, ld_row, q_col,
+                                        s_col, ld_col, o["rsigma"].data_ptr(), _raw_stream()))
+    return o
+
+
+def rmsnorm_backward(dy, z, gamma, rsigma, dz=None, dparams: bool = True, stream=None, out=None, workspace=None):
+    """Gradients of ``rmsnorm`` and ``rmsnorm_quantize``: dy and z [rows, hidden]
+    of one type (z is x where there was no residual), rsigma from the forward
+    pass, dz the gradient that reaches z by the residual path (None: zero).
+    Returns a dict with "dx" (of x and of the residual alike) and, with
+    ``dparams``, "dgamma" (the type of gamma); its scratch is ``workspace`` (uint8
+    CUDA tensor) or allocated here."""
+    if stream is not None:
+        with _on(stream):
+            return rmsnorm_backward(dy, z, gamma, rsigma, dz=dz, dparams=dparams, out=out, workspace=workspace)
+    torch = _torch or _load_torch()
+    shape, dtype = z.shape, z.dtype
+    rows, hidden = shape
+    device = z.get_device()
+    assert device >= 0 and device == _current_device() and _like(dy, shape, dtype, device) and _like(dz, shape, dtype, device)
+    assert gamma.shape == shape[1:] and gamma.is_contiguous() and gamma.get_device() == device
+    assert _vectors(rsigma, None, rows, torch.float32, device)
+    o = {} if out is None else dict(out)
+    if o:
+        assert _like(o.get("dx"), shape, dtype, device) and _vectors(o.get("dgamma"), None, hidden, gamma.dtype, device)
+    if "dx" not in o:
+        o["dx"] = torch.empty_like(z, memory_format=torch.contiguous_format)
+    if dparams and "dgamma" not in o:
+        o["dgamma"] = torch.empty_like(gamma)
+    dga = ws = size = 0
+    if "dgamma" in o:
+        dga = o["dgamma"].data_ptr()
+        if workspace is None:
+            workspace = torch.empty(lib().te_mx_rmsnorm_backward_workspace_size(rows, hidden), dtype=torch.uint8,
+                                    device=z.device)
+        else:
+            assert workspace.dtype == torch.uint8 and workspace.get_device() == device and workspace.is_contiguous()
+        ws, size = workspace.data_ptr(), workspace.numel()
+    dx, res, ld_res = o["dx"], 0, 0
+    if dz is not None:
+        res, ld_res = dz.data_ptr(), _pitch(dz)
+    _check(lib().te_mx_rmsnorm_backward(dy.data_ptr(), _pitch(dy), z.data_ptr(), _pitch(z), rows, hidden, _dtype_code[dtype],
+                                        gamma.data_ptr(), _dtype_code[gamma.dtype], rsigma.data_ptr(), res, ld_res,
+                                        dx.data_ptr(), _pitch(dx), dga, ws, size, _raw_stream()))
+    return o
+
+
+def route(logits, k: int, scoring: str = "softmax", renormalise: bool = True, scale: float = 1.0, bias=None, stream=None,
+          out=None):
+    """The k experts of each token (logits [tokens, experts], bf16, fp16 or fp32)
+    with the largest logit + bias (bias fp32 [experts] or None; it chooses only),
+    ties to the lowest index, and their weights: ``scale`` times the softmax (or
+    "sigmoid") of the logits, with ``renormalise`` over the chosen ones.  Returns
+    {"index": int32 [tokens, k], "weight": fp32 [tokens, k]}."""
+    if stream is not None:
+        with _on(stream):
+            return route(logits, k, scoring=scoring, renormalise=renormalise, scale=scale, bias=bias, out=out)
+    torch = _torch or _load_torch()
+    tokens, experts = logits.shape
+    device = logits.get_device()
+    assert device >= 0 and device == _current_device() and _vectors(bias, None, experts, torch.float32, device)
+    o = {} if out is None else dict(out)
+    if o:
+        assert _matrix(o.get("index"), tokens, k, torch.int32, device)
+        assert _matrix(o.get("weight"), tokens, k, torch.float32, device)
+    if "index" not in o:
+        o["index"] = torch.empty((tokens, k), dtype=torch.int32, device=logits.device)
+    if "weight" not in o:
+        o["weight"] = torch.empty((tokens, k), dtype=torch.float32, device=logits.device)
+    _check(lib().te_mx_route(logits.data_ptr(), tokens, experts, _pitch(logits), _dtype_code[logits.dtype],
+                             0 if bias is None else bias.data_ptr(), k, SCORINGS[scoring], int(bool(renormalise)), scale,
+                             o["index"].data_ptr(), o["weight"].data_ptr(), _raw_stream()))
+    return o
+
+
+def route_backward(dweight, logits, index, scoring: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                   stream=None, out=None):
+    """The gradient of ``route``'s logits (their type, [tokens, experts]) from that
+    of its weights (fp32 [tokens, k]); index and the options as in the forward
+    call (a negative index: a choice dropped since)."""
+    if stream is not None:
+        with _on(stream):
+            return route_backward(dweight, logits, index, scoring=scoring, renormalise=renormalise, scale=scale, out=out)
+    torch = _torch or _load_torch()
+    tokens, experts = logits.shape
+    k = index.shape[1]
+    device = logits.get_device()
+    assert device >= 0 and device == _current_device()
+    assert _matrix(index, tokens, k, torch.int32, device) and _matrix(dweight, tokens, k, torch.float32, device)
+    assert _like(out, logits.shape, logits.dtype, device)
+    d = torch.empty_like(logits, memory_format=torch.contiguous_format) if out is None else out
+    _check(lib().te_mx_route_backward(dweight.data_ptr(), logits.data_ptr(), _pitch(logits), index.data_ptr(), tokens,
+                                      experts, _dtype_code[logits.dtype], k, SCORINGS[scoring], int(bool(renormalise)),
+                                      scale, d.data_ptr(), _pitch(d), _raw_stream()))
+    return d
+
+
+def moe_sort(index, experts: int, stream=None, out=None):
+    """Slots sorted by expert: index int32 [tokens, k] (or any shape; a negative
+    one has no row).  Returns {"group_m": int32 [experts], the experts' row counts
+    (``grouped_gemm``'s group_m), "row": the row of each slot (the shape of index,
+    -1 without one), "slot": int32 [slots], the slot of each row (-1 behind the
+    last)}."""
+    if stream is not None:
+        with _on(stream):
+            return moe_sort(index, experts, out=out)
+    torch = _torch or _load_torch()
+    device, n, i32 = index.get_device(), index.numel(), torch.int32
+    assert device >= 0 and device == _current_device() and index.dtype == i32 and index.is_contiguous()
+    o = {} if out is None else dict(out)
+    if o:
+        r = o.get("row")
+        assert r is None or (r.shape == index.shape and r.dtype == i32 and r.is_contiguous() and r.get_device() == device)
+        assert _vectors(o.get("group_m"), None, experts, i32, device) and _vectors(o.get("slot"), None, n, i32, device)
+    if "group_m" not in o:
+        o["group_m"] = torch.empty(experts, dtype=i32, device=index.device)
+    if "row" not in o:
+        o["row"] = torch.empty_like(index)
+    if "slot" not in o:
+        o["slot"] = torch.empty(n, dtype=i32, device=index.device)
+    _check(lib().te_mx_moe_sort(index.data_ptr(), n, experts, o["group_m"].data_ptr(), o["row"].data_ptr(),
+                                o["slot"].data_ptr(), _raw_stream()))
+    return o
+
+
+def moe_dispatch(x, row, scales=None, total_rows=None, stream=None, out=None):
+    """Every token's row copied to the rows of its slots: x [tokens, hidden] of any
+    type (or MXFP8 codes, with their ``scales`` [tokens, pitch]), row int32
+    [tokens, k] (``moe_sort``).  Returns out [total_rows, hidden] (tokens * k rows
+    if not said), or (out, out_scales); rows without a slot are not written.  Its
+    gradient is ``moe_combine`` without weights."""
+    if stream is not None:
+        with _on(stream):
+            return moe_dispatch(x, row, scales=scales, total_rows=total_rows, out=out)
+    torch = _torch or _load_torch()
+    tokens, hidden = x.shape
+    k = row.shape[1]
+    device, size = x.get_device(), x.element_size()
+    assert device >= 0 and device == _current_device() and _matrix(row, tokens, k, torch.int32, device)
+    s = ld_s = width = d_s = ld_ds = 0
+    if scales is not None:
+        width = hidden // 32
+        assert size == 1 and _bytes(scales, tokens, width, device)
+    if out is None:
+        m = tokens * k if total_rows is None else total_rows
+        d = torch.empty((m, hidden), dtype=x.dtype, device=x.device)
+        ds = None if scales is None else torch.empty((m, (width + 15) // 16 * 16), dtype=scales.dtype, device=x.device)
+    else:
+        d, ds = out if scales is not None else (out, None)
+        m = d.shape[0]
+        assert (total_rows is None or total_rows == m) and _like(d, (m, hidden), x.dtype, device)
+        assert _bytes(ds, m, width, device)
+    if scales is not None:
+        s, ld_s, d_s, ld_ds = scales.data_ptr(), _pitch(scales), ds.data_ptr(), _pitch(ds)
+    _check(lib().te_mx_moe_dispatch(x.data_ptr(), _pitch(x) * size, hidden * size, s, ld_s, width, row.data_ptr(), tokens, k,
+                                    m, d.data_ptr(), _pitch(d) * size, d_s, ld_ds, _raw_stream()))
+    return d if scales is None else (d, ds)
+
+
+def moe_combine(y, row, weight=None, residual=None, stream=None, out=None):
+    """out[t] = sum_j weight[t, j] y[row[t, j]] + residual[t]: y [rows, hidden] of
+    bf16, fp16 or fp32, row int32 [tokens, k] (a negative one is skipped), weight
+    fp32 [tokens, k] or None (all 1: the gradient of ``moe_dispatch``), residual
+    [tokens, hidden] or None.  Returns out [tokens, hidden] in the type of y."""
+    if stream is not None:
+        with _on(stream):
+            return moe_combine(y, row, weight=weight, residual=residual, out=out)
+    torch = _torch or _load_torch()
+    rows, hidden = y.shape
+    tokens, k = row.shape
+    device = y.get_device()
+    assert device >= 0 and device == _current_device()
+    assert _matrix(row, tokens, k, torch.int32, device) and _matrix(weight, tokens, k, torch.float32, device)
+    assert _like(residual, (tokens, hidden), y.dtype, device) and _like(out, (tokens, hidden), y.dtype, device)
+    d = torch.empty((tokens, hidden), dtype=y.dtype, device=y.device) if out is None else out
+    _check(lib().te_mx_moe_combine(y.data_ptr(), _pitch(y), rows, hidden, _dtype_code[y.dtype], row.data_ptr(), tokens, k,
+                                   0 if weight is None else weight.data_ptr(), 0 if residual is None else residual.data_ptr(),
+                                   0 if residual is None else _pitch(residual), d.data_ptr(), _pitch(d), _raw_stream()))
+    return d
+
+
+def moe_combine_backward(dout, y, row, weight, dweight: bool = True, stream=None, out=None):
+    """Gradients of ``moe_combine``: dout [tokens, hidden], y, row and weight of the
+    forward call.  Returns a dict with "dy" [rows, hidden] (rows without a slot are
+    not written) and, with ``dweight``, "dweight" (fp32 [tokens, k], 0 for a slot
+    without a row)."""
+    if stream is not None:
+        with _on(stream):
+            return moe_combine_backward(dout, y, row, weight, dweight=dweight, out=out)
+    torch = _torch or _load_torch()
+    rows, hidden = y.shape
+    tokens, k = row.shape
+    device = y.get_device()
+    assert device >= 0 and device == _current_device()
+    assert _matrix(row, tokens, k, torch.int32, device) and _matrix(weight, tokens, k, torch.float32, device)
+    assert weight is not None and _like(dout, (tokens, hidden), y.dtype, device)
+    o = {} if out is None else dict(out)
+    if o:
+        assert _like(o.get("dy"), y.shape, y.dtype, device) and _matrix(o.get("dweight"), tokens, k, torch.float32, device)
+    if "dy" not in o:
+        o["dy"] = torch.empty_like(y, memory_format=torch.contiguous_format)
+    if dweight and "dweight" not in o:
+        o["dweight"] = torch.empty_like(weight)
+    dy = o["dy"]
+    _check(lib().te_mx_moe_combine_backward(dout.data_ptr(), _pitch(dout), y.data_ptr(), _pitch(y), rows, hidden,
+                                            _dtype_code[y.dtype], row.data_ptr(), weight.data_ptr(), tokens, k,
+                                            dy.data_ptr(), _pitch(dy), _ptr(o.get("dweight")), _raw_stream()))
     return o

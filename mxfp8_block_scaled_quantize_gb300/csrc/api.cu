@@ -453,6 +453,300 @@ te_mx_status te_mx_grouped_gemm_wgrad(int32_t num_groups, const int32_t* group_m
     return gemm_launch(a, static_cast<cudaStream_t>(stream));
 }
 
+// An output may be an input (the same pointer and pitch) or lie apart from it; rows
+// side by side in one buffer (equal pitches) are apart.
+static bool apart_or_same(const void* out, int64_t out_rows, int64_t ld_out, const void* in, int64_t in_rows, int64_t ld_in,
+                          int64_t width, bool may_be_same) {
+    if (!out || !in || out_rows <= 0 || in_rows <= 0 || width <= 0) return true;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+    if (may_be_same && o == i && (ld_out == ld_in || (out_rows == 1 && in_rows == 1))) return true;
+    const uintptr_t o_end = o + uintptr_t((out_rows - 1) * ld_out + width), i_end = i + uintptr_t((in_rows - 1) * ld_in + width);
+    if (o >= i_end || i >= o_end) return true;
+    if (ld_out != ld_in) return false;
+    const uintptr_t d = (o > i ? o - i : i - o) % uintptr_t(ld_out);
+    return d >= uintptr_t(width) && d + uintptr_t(width) <= uintptr_t(ld_out);
+}
+
+static int64_t element_bytes(int32_t dtype) { return dtype == TE_MX_FP32 ? 4 : 2; }
+
+static te_mx_status overlap_error(const char* out, const char* in) {
+    return set_error(TE_MX_ERR_INVALID_ARG, "%s overlaps %s without being it (the same pointer and pitch), or may not be it", out, in);
+}
+
+// Checks of the RMSNorm forward entry points past sizes and types.
+static te_mx_status validate_rms(const RmsArgs& a) {
+    te_mx_status st;
+    const int64_t b = element_bytes(a.dtype), w = a.hidden * b;
+    if (!a.gamma) return set_error(TE_MX_ERR_INVALID_ARG, "gamma is NULL");
+    if (!aligned(a.gamma, uintptr_t(element_bytes(a.param_dtype))) || !aligned(a.rsigma, 4))
+        return set_error(TE_MX_ERR_MISALIGNED, "gamma or rsigma is not aligned to its elements");
+    if ((st = validate_ln_matrix(a.x, a.ld_x, a.hidden, a.dtype, "x")) != TE_MX_OK) return st;
+    if ((a.residual == nullptr) != (a.z == nullptr))
+        return set_error(TE_MX_ERR_INVALID_ARG, "residual and z must both be given or both be NULL");
+    if (a.residual) {
+        if ((st = validate_ln_matrix(a.residual, a.ld_residual, a.hidden, a.dtype, "residual")) != TE_MX_OK) return st;
+        if ((st = validate_ln_matrix(a.z, a.ld_z, a.hidden, a.dtype, "z")) != TE_MX_OK) return st;
+        if (!apart_or_same(a.z, a.rows, a.ld_z * b, a.x, a.rows, a.ld_x * b, w, true)) return overlap_error("z", "x");
+        if (!apart_or_same(a.z, a.rows, a.ld_z * b, a.residual, a.rows, a.ld_residual * b, w, true)) return overlap_error("z", "residual");
+    }
+    if (a.y) {
+        if ((st = validate_ln_matrix(a.y, a.ld_y, a.hidden, a.dtype, "y")) != TE_MX_OK) return st;
+        // (the column-wise copy is made of x after y is written, if there is no z)
+        if (!apart_or_same(a.y, a.rows, a.ld_y * b, a.x, a.rows, a.ld_x * b, w, a.residual || !a.q_col)) return overlap_error("y", "x");
+        if (!apart_or_same(a.y, a.rows, a.ld_y * b, a.residual, a.rows, a.ld_residual * b, w, true)) return overlap_error("y", "residual");
+        if (!apart_or_same(a.y, a.rows, a.ld_y * b, a.z, a.rows, a.ld_z * b, w, false)) return overlap_error("y", "z");
+    }
+    return TE_MX_OK;
+}
+
+te_mx_status te_mx_rmsnorm(const void* x, int64_t rows, int64_t hidden, int64_t ld_x, int32_t dtype,
+                           const void* residual, int64_t ld_residual, const void* gamma, int32_t param_dtype,
+                           float eps, void* z, int64_t ld_z, void* y, int64_t ld_y, float* rsigma, void* stream) {
+    t_last_error[0] = '\0';
+    te_mx_status st = validate_layernorm(rows, hidden, dtype, param_dtype);
+    if (st != TE_MX_OK) return st;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return set_error(TE_MX_ERR_INVALID_ARG, "eps must be positive and finite");
+    if (rows == 0 || hidden == 0) return TE_MX_OK;
+    if (!y) return set_error(TE_MX_ERR_INVALID_ARG, "y is NULL");
+    RmsArgs a{x, rows, hidden, ld_x, dtype, param_dtype, residual, ld_residual, gamma, eps, z, ld_z, y, ld_y, rsigma,
+              nullptr, nullptr, 0, nullptr, nullptr, 0};
+    if ((st = validate_rms(a)) != TE_MX_OK || (st = check_device(nullptr)) != TE_MX_OK) return st;
+    return rms_forward_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+te_mx_status te_mx_rmsnorm_quantize(const void* x, int64_t rows, int64_t hidden, int64_t ld_x,
+                                    const void* residual, int64_t ld_residual, const void* gamma,
+                                    int32_t param_dtype, float eps, void* z, int64_t ld_z, void* y, int64_t ld_y,
+                                    uint8_t* q_row, uint8_t* s_row, int64_t ld_s_row,
+                                    uint8_t* q_col, uint8_t* s_col, int64_t ld_s_col,
+                                    float* rsigma, void* stream) {
+    t_last_error[0] = '\0';
+    te_mx_status st = validate_layernorm(rows, hidden, TE_MX_BF16, param_dtype);
+    if (st != TE_MX_OK) return st;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return set_error(TE_MX_ERR_INVALID_ARG, "eps must be positive and finite");
+    RmsArgs a{x, rows, hidden, ld_x, TE_MX_BF16, param_dtype, residual, ld_residual, gamma, eps, z, ld_z, y, ld_y, rsigma,
+              q_row, s_row, ld_s_row, q_col, s_col, ld_s_col};
+    const bool work = rows > 0 && hidden > 0;
+    if (work) {
+        if (!rsigma) return set_error(TE_MX_ERR_INVALID_ARG, "rsigma is NULL");
+        if (hidden > rms_quantize_max_hidden())
+            return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "hidden=%lld exceeds %lld", (long long)hidden,
+                             (long long)rms_quantize_max_hidden());
+        if ((st = validate_rms(a)) != TE_MX_OK) return st;
+        if (!aligned(gamma, 16)) return set_error(TE_MX_ERR_MISALIGNED, "gamma is not 16-byte aligned");
+        if (!aligned(residual, 16) || !aligned(z, 16) || !aligned(y, 16))
+            return set_error(TE_MX_ERR_MISALIGNED, "residual, z or y is not 16-byte aligned");
+        if ((residual && (ld_residual % 8 || ld_z % 8)) || (y && ld_y % 8))
+            return set_error(TE_MX_ERR_MISALIGNED, "ld_residual, ld_z and ld_y must be multiples of 8");
+    }
+    st = validate_quantize(x, rows, hidden, ld_x, q_row, s_row, ld_s_row, q_col, s_col, ld_s_col, true);
+    if (st != TE_MX_OK || !work) return st;
+    return rms_quantize_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t te_mx_rmsnorm_backward_workspace_size(int64_t rows, int64_t hidden) {
+    if (rows <= 0 || hidden <= 0) return 0;
+    return size_t(rms_backward_parts(rows)) * size_t(hidden) * sizeof(float);
+}
+
+te_mx_status te_mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* z, int64_t ld_z, int64_t rows,
+                                    int64_t hidden, int32_t dtype, const void* gamma, int32_t param_dtype,
+                                    const float* rsigma, const void* dz, int64_t ld_dz, void* dx, int64_t ld_dx,
+                                    void* dgamma, void* workspace, size_t workspace_bytes, void* stream) {
+    t_last_error[0] = '\0';
+    te_mx_status st = validate_layernorm(rows, hidden, dtype, param_dtype);
+    if (st != TE_MX_OK) return st;
+    if (hidden == 0) return TE_MX_OK;
+    const int64_t b = element_bytes(dtype), w = hidden * b;
+    if (!dx && !dgamma) return rows == 0 ? TE_MX_OK : set_error(TE_MX_ERR_INVALID_ARG, "dx and dgamma are both NULL");
+    if (!aligned(dgamma, uintptr_t(element_bytes(param_dtype))))
+        return set_error(TE_MX_ERR_MISALIGNED, "dgamma is not aligned to its elements");
+    if (rows > 0) {
+        if (!gamma || !rsigma) return set_error(TE_MX_ERR_INVALID_ARG, "gamma and rsigma are required");
+        if (!aligned(gamma, uintptr_t(element_bytes(param_dtype))) || !aligned(rsigma, 4))
+            return set_error(TE_MX_ERR_MISALIGNED, "gamma or rsigma is not aligned to its elements");
+        if ((st = validate_ln_matrix(dy, ld_dy, hidden, dtype, "dy")) != TE_MX_OK) return st;
+        if ((st = validate_ln_matrix(z, ld_z, hidden, dtype, "z")) != TE_MX_OK) return st;
+        if (dz && (st = validate_ln_matrix(dz, ld_dz, hidden, dtype, "dz")) != TE_MX_OK) return st;
+        if (dx) {
+            if ((st = validate_ln_matrix(dx, ld_dx, hidden, dtype, "dx")) != TE_MX_OK) return st;
+            if (!apart_or_same(dx, rows, ld_dx * b, dy, rows, ld_dy * b, w, true)) return overlap_error("dx", "dy");
+            if (!apart_or_same(dx, rows, ld_dx * b, z, rows, ld_z * b, w, true)) return overlap_error("dx", "z");
+            if (!apart_or_same(dx, rows, ld_dx * b, dz, rows, ld_dz * b, w, true)) return overlap_error("dx", "dz");
+        }
+        if (dgamma) {
+            if (!workspace || workspace_bytes < te_mx_rmsnorm_backward_workspace_size(rows, hidden))
+                return set_error(TE_MX_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0),
+                                 te_mx_rmsnorm_backward_workspace_size(rows, hidden));
+            if (!aligned(workspace, 16)) return set_error(TE_MX_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+        }
+    } else if (!dgamma) {
+        return TE_MX_OK;
+    }
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    RmsBackwardArgs a{dy, ld_dy, z, rows, hidden, ld_z, dtype, param_dtype, gamma, rsigma, dz, ld_dz, dx, ld_dx, dgamma,
+                      static_cast<float*>(workspace)};
+    return rms_backward_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+// Checks shared by the router's two entry points.
+static te_mx_status validate_route(const RouteArgs& a, int32_t renormalise) {
+    if (a.tokens < 0) return set_error(TE_MX_ERR_INVALID_ARG, "negative size %lld", (long long)a.tokens);
+    if (a.dtype < TE_MX_BF16 || a.dtype > TE_MX_FP32) return set_error(TE_MX_ERR_INVALID_ARG, "unknown dtype %d", int(a.dtype));
+    if (a.scoring != TE_MX_SCORE_SOFTMAX && a.scoring != TE_MX_SCORE_SIGMOID)
+        return set_error(TE_MX_ERR_INVALID_ARG, "unknown scoring %d", int(a.scoring));
+    if (renormalise != 0 && renormalise != 1) return set_error(TE_MX_ERR_INVALID_ARG, "renormalise=%d must be 0 or 1", int(renormalise));
+    if (!std::isfinite(a.scale)) return set_error(TE_MX_ERR_INVALID_ARG, "scale must be finite");
+    if (a.k < 1 || a.k > 32 || a.experts < a.k || a.experts > 1024)
+        return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "k=%d must be 1 .. 32 and experts=%d k .. 1024", int(a.k), int(a.experts));
+    if (a.tokens >= (int64_t(1) << 31) / a.k) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "tokens * k reaches 2^31");
+    if (a.tokens == 0) return TE_MX_OK;
+    if (!a.logits || !a.index || !a.weight) return set_error(TE_MX_ERR_INVALID_ARG, "logits, index and the weights are required");
+    if (a.ld_logits < a.experts)
+        return set_error(TE_MX_ERR_MISALIGNED, "ld_logits=%lld is less than experts=%d", (long long)a.ld_logits, int(a.experts));
+    if (!aligned(a.logits, uintptr_t(element_bytes(a.dtype))) || !aligned(a.bias, 4) || !aligned(a.index, 4) || !aligned(a.weight, 4))
+        return set_error(TE_MX_ERR_MISALIGNED, "logits, bias, index or weights are not aligned to their elements");
+    return TE_MX_OK;
+}
+
+te_mx_status te_mx_route(const void* logits, int64_t tokens, int32_t experts, int64_t ld_logits, int32_t dtype,
+                         const float* bias, int32_t k, int32_t scoring, int32_t renormalise, float scale,
+                         int32_t* index, float* weight, void* stream) {
+    t_last_error[0] = '\0';
+    RouteArgs a{logits, tokens, ld_logits, experts, k, dtype, bias, scoring, renormalise == 1, scale, index, weight, nullptr, 0};
+    te_mx_status st = validate_route(a, renormalise);
+    if (st != TE_MX_OK || tokens == 0 || (st = check_device(nullptr)) != TE_MX_OK) return st;
+    return route_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+te_mx_status te_mx_route_backward(const float* dweight, const void* logits, int64_t ld_logits,
+                                  const int32_t* index, int64_t tokens, int32_t experts, int32_t dtype, int32_t k,
+                                  int32_t scoring, int32_t renormalise, float scale, void* dlogits,
+                                  int64_t ld_dlogits, void* stream) {
+    t_last_error[0] = '\0';
+    RouteArgs a{logits, tokens, ld_logits, experts, k, dtype, nullptr, scoring, renormalise == 1, scale,
+                const_cast<int32_t*>(index), const_cast<float*>(dweight), dlogits, ld_dlogits};
+    te_mx_status st = validate_route(a, renormalise);
+    if (st != TE_MX_OK || tokens == 0) return st;
+    const int64_t b = element_bytes(dtype);
+    if ((st = validate_ln_matrix(dlogits, ld_dlogits, experts, dtype, "dlogits")) != TE_MX_OK) return st;
+    if (!apart_or_same(dlogits, tokens, ld_dlogits * b, logits, tokens, ld_logits * b, experts * b, false))
+        return overlap_error("dlogits", "logits");
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    return route_backward_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+te_mx_status te_mx_moe_sort(const int32_t* index, int64_t slots, int32_t experts, int32_t* group_m, int32_t* row,
+                            int32_t* slot, void* stream) {
+    t_last_error[0] = '\0';
+    if (slots < 0) return set_error(TE_MX_ERR_INVALID_ARG, "negative size %lld", (long long)slots);
+    if (experts < 1 || experts > 1024) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "experts=%d must be 1 .. 1024", int(experts));
+    if (slots >= int64_t(1) << 31) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "slots=%lld reaches 2^31", (long long)slots);
+    if (!group_m || (slots > 0 && (!index || !row || !slot)))
+        return set_error(TE_MX_ERR_INVALID_ARG, "index, group_m, row and slot are required");
+    if (!aligned(index, 4) || !aligned(group_m, 4) || !aligned(row, 4) || !aligned(slot, 4))
+        return set_error(TE_MX_ERR_MISALIGNED, "index, group_m, row or slot is not aligned to its elements");
+    const int64_t b = 4 * slots;
+    if (!apart_or_same(row, 1, b, index, 1, b, b, false) || !apart_or_same(slot, 1, b, index, 1, b, b, false) ||
+        !apart_or_same(row, 1, b, slot, 1, b, b, false))
+        return set_error(TE_MX_ERR_INVALID_ARG, "index, row and slot overlap");
+    te_mx_status st = check_device(nullptr);
+    if (st != TE_MX_OK) return st;
+    return moe_sort_launch(index, slots, experts, group_m, row, slot, static_cast<cudaStream_t>(stream));
+}
+
+// Checks shared by dispatch and combine: tokens, choices and rows.
+static te_mx_status validate_slots(int64_t tokens, int32_t k, int64_t total_rows) {
+    if (tokens < 0 || total_rows < 0)
+        return set_error(TE_MX_ERR_INVALID_ARG, "negative size %lld or %lld", (long long)tokens, (long long)total_rows);
+    if (k < 1 || k > 32) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "k=%d must be 1 .. 32", int(k));
+    if (tokens >= (int64_t(1) << 31) / k || total_rows >= int64_t(1) << 31)
+        return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "tokens * k or total_rows reaches 2^31");
+    return TE_MX_OK;
+}
+
+te_mx_status te_mx_moe_dispatch(const void* x, int64_t ld_x, int64_t row_bytes, const uint8_t* scales,
+                                int64_t ld_scales, int64_t scale_bytes, const int32_t* row, int64_t tokens,
+                                int32_t k, int64_t total_rows, void* out, int64_t ld_out, uint8_t* out_scales,
+                                int64_t ld_out_scales, void* stream) {
+    t_last_error[0] = '\0';
+    te_mx_status st = validate_slots(tokens, k, total_rows);
+    if (st != TE_MX_OK) return st;
+    if (row_bytes < 0 || (scales && scale_bytes < 0)) return set_error(TE_MX_ERR_INVALID_ARG, "negative row size");
+    if (tokens > 0 && row_bytes > (int64_t(1) << 39) / tokens)
+        return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "tokens * row_bytes exceeds 2^39");
+    if ((scales == nullptr) != (out_scales == nullptr))
+        return set_error(TE_MX_ERR_INVALID_ARG, "scales and out_scales must both be given or both be NULL");
+    if (tokens == 0 || row_bytes == 0) return TE_MX_OK;
+    if (!x || (!out && total_rows > 0) || !row) return set_error(TE_MX_ERR_INVALID_ARG, "x, row and out are required");
+    if (!aligned(row, 4)) return set_error(TE_MX_ERR_MISALIGNED, "row is not aligned to its elements");
+    if (ld_x < row_bytes || ld_out < row_bytes) return set_error(TE_MX_ERR_MISALIGNED, "a row pitch is less than row_bytes");
+    if (scales && (ld_scales < scale_bytes || ld_out_scales < scale_bytes))
+        return set_error(TE_MX_ERR_MISALIGNED, "a scale pitch is less than scale_bytes");
+    if (!apart_or_same(out, total_rows, ld_out, x, tokens, ld_x, row_bytes, false)) return overlap_error("out", "x");
+    if (scales && !apart_or_same(out_scales, total_rows, ld_out_scales, scales, tokens, ld_scales, scale_bytes, false))
+        return overlap_error("out_scales", "scales");
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    DispatchArgs a{static_cast<const uint8_t*>(x), ld_x, row_bytes, scales, ld_scales, scale_bytes, row, tokens, total_rows, k,
+                   static_cast<uint8_t*>(out), ld_out, out_scales, ld_out_scales};
+    return moe_dispatch_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+static te_mx_status validate_combine(const CombineArgs& a) {
+    te_mx_status st = validate_slots(a.tokens, a.k, a.total_rows);
+    if (st != TE_MX_OK) return st;
+    if (a.hidden < 0) return set_error(TE_MX_ERR_INVALID_ARG, "negative size %lld", (long long)a.hidden);
+    if (a.dtype < TE_MX_BF16 || a.dtype > TE_MX_FP32) return set_error(TE_MX_ERR_INVALID_ARG, "unknown dtype %d", int(a.dtype));
+    if (a.hidden > int64_t(1) << 24 || (a.tokens > 0 && a.hidden > (int64_t(1) << 38) / a.tokens))
+        return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "hidden=%lld exceeds 2^24, or tokens * hidden 2^38", (long long)a.hidden);
+    if (a.tokens == 0 || a.hidden == 0) return TE_MX_OK;
+    if (!a.row) return set_error(TE_MX_ERR_INVALID_ARG, "row is NULL");
+    if (!aligned(a.row, 4) || !aligned(a.weight, 4) || !aligned(a.dweight, 4))
+        return set_error(TE_MX_ERR_MISALIGNED, "row or weights are not aligned to their elements");
+    return TE_MX_OK;
+}
+
+te_mx_status te_mx_moe_combine(const void* y, int64_t ld_y, int64_t total_rows, int64_t hidden, int32_t dtype,
+                               const int32_t* row, int64_t tokens, int32_t k, const float* weight,
+                               const void* residual, int64_t ld_residual, void* out, int64_t ld_out, void* stream) {
+    t_last_error[0] = '\0';
+    CombineArgs a{y, ld_y, total_rows, hidden, dtype, k, row, tokens, weight, residual, ld_residual, out, ld_out,
+                  nullptr, 0, nullptr, 0, nullptr};
+    te_mx_status st = validate_combine(a);
+    if (st != TE_MX_OK || tokens == 0 || hidden == 0) return st;
+    const int64_t b = element_bytes(dtype), w = hidden * b;
+    if (total_rows > 0 && (st = validate_ln_matrix(y, ld_y, hidden, dtype, "y")) != TE_MX_OK) return st;
+    if (residual && (st = validate_ln_matrix(residual, ld_residual, hidden, dtype, "residual")) != TE_MX_OK) return st;
+    if ((st = validate_ln_matrix(out, ld_out, hidden, dtype, "out")) != TE_MX_OK) return st;
+    if (!apart_or_same(out, tokens, ld_out * b, y, total_rows, ld_y * b, w, false)) return overlap_error("out", "y");
+    if (!apart_or_same(out, tokens, ld_out * b, residual, tokens, ld_residual * b, w, true)) return overlap_error("out", "residual");
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    return moe_combine_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+te_mx_status te_mx_moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y,
+                                        int64_t total_rows, int64_t hidden, int32_t dtype, const int32_t* row,
+                                        const float* weight, int64_t tokens, int32_t k, void* dy, int64_t ld_dy,
+                                        float* dweight, void* stream) {
+    t_last_error[0] = '\0';
+    CombineArgs a{dweight ? y : nullptr, ld_y, total_rows, hidden, dtype, k, row, tokens, weight, nullptr, 0, nullptr, 0,
+                  dout, ld_dout, dy, ld_dy, dweight};
+    te_mx_status st = validate_combine(a);
+    if (st != TE_MX_OK || tokens == 0 || hidden == 0) return st;
+    if (!dy && !dweight) return set_error(TE_MX_ERR_INVALID_ARG, "dy and dweight are both NULL");
+    if (!weight) return set_error(TE_MX_ERR_INVALID_ARG, "weight is NULL");
+    const int64_t b = element_bytes(dtype), w = hidden * b;
+    if ((st = validate_ln_matrix(dout, ld_dout, hidden, dtype, "dout")) != TE_MX_OK) return st;
+    if (total_rows > 0) {
+        if (dweight && (st = validate_ln_matrix(y, ld_y, hidden, dtype, "y")) != TE_MX_OK) return st;
+        if (dy && (st = validate_ln_matrix(dy, ld_dy, hidden, dtype, "dy")) != TE_MX_OK) return st;
+        if (!apart_or_same(dy, total_rows, ld_dy * b, a.y, total_rows, ld_y * b, w, true)) return overlap_error("dy", "y");
+        if (!apart_or_same(dy, total_rows, ld_dy * b, dout, tokens, ld_dout * b, w, false)) return overlap_error("dy", "dout");
+    }
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
+    return moe_combine_backward_launch(a, static_cast<cudaStream_t>(stream));
+}
+
 size_t te_mx_quantize_dbias_workspace_size(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0) return 0;
     return size_t((rows + kDbiasBandRows - 1) / kDbiasBandRows) * size_t(cols) * sizeof(float);

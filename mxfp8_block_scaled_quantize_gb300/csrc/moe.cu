@@ -1,0 +1,601 @@
+// Around the experts of a mixture: the choice of experts with its gradient, the
+// slots sorted by expert, tokens copied to their experts' rows, and the experts'
+// outputs added up for the tokens, with the gradients.  (Dispatch's gradient is a
+// combine without weights.)  Slot s = token * k + j is a token's j-th choice.
+#include <cuda_runtime.h>
+
+#include <cfloat>
+
+#include "f32x2.cuh"
+#include "ptx.cuh"
+#include "row_ops.cuh"
+#include "temx_internal.h"
+
+namespace temx {
+
+namespace {
+
+// ---------------------------------------------------------------- router
+
+// A warp per token; lane l holds experts l, l + 32, ... (kN of them).
+//   key[e] = fl32(logit[e] + bias[e]);  the k largest keys, ties to the lowest index.
+//   p = softmax of the logits over all experts, or the logistic function of each;
+//   weight = scale p, or scale p / (the chosen experts' sum of p).
+// Keys are compared as integers in the order of the numbers; NaN comes last, after
+// -inf, so the indices are always k different experts.
+constexpr int kRouteWarps = 8;
+
+__device__ __forceinline__ uint32_t ordered_key(float v) {
+    if (v != v) return 1u;                                 // (0: taken already)
+    const uint32_t b = __float_as_uint(v + 0.0f);          // (-0 and 0 are equal)
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;       // -inf: 0x007FFFFF
+}
+
+__device__ __forceinline__ float logistic(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+template <typename T, int kN>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t token, int lane, float (&l)[kN]) {
+    const T* p = static_cast<const T*>(a.logits) + token * a.ld_logits;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) l[i] = lane + 32 * i < a.experts ? to_f32(p[lane + 32 * i]) : -INFINITY;
+}
+
+// Largest logit of the row and the sum of exp(logit - largest).
+template <int kN>
+__device__ __forceinline__ void softmax_sum(const float (&l)[kN], float& most, float& sum) {
+    float m = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) s += l[i] == -INFINITY ? 0.0f : expf(l[i] - m);
+    most = m;
+    sum = warp_sum(s);
+}
+
+template <typename T, int kN>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+route_kernel(const RouteArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t token = int64_t(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    if (token >= a.tokens) return;
+    float l[kN];
+    load_logits<T, kN>(a, token, lane, l);
+    uint32_t key[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = e < a.experts ? ordered_key(a.bias ? l[i] + a.bias[e] : l[i]) : 0u;
+    }
+    int mine = 0;                                          // lane j: the j-th choice and its logit
+    float logit = -INFINITY;
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) best = max(best, key[i]);
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+        uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = kN - 1; i >= 0; --i)
+            if (key[i] == top) at = uint32_t(lane + 32 * i);
+        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, at);
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (e == uint32_t(lane + 32 * i)) {
+                v = l[i];
+                key[i] = 0u;
+            }
+        v = __shfl_sync(0xFFFFFFFFu, v, int(e & 31u));
+        if (lane == j) {
+            mine = int(e);
+            logit = v;
+        }
+    }
+    const bool chosen = lane < a.k;
+    float w;
+    if (a.scoring == TE_MX_SCORE_SOFTMAX) {
+        float most, sum;
+        if (a.renormalise) {                               // of the chosen ones alone: the others' sum cancels
+            most = warp_max(logit);
+            const float p = chosen && logit != -INFINITY ? expf(logit - most) : 0.0f;
+            sum = warp_sum(p);
+            w = p;
+        } else {
+            softmax_sum(l, most, sum);
+            w = logit != -INFINITY ? expf(logit - most) : 0.0f;
+        }
+        w = sum == 0.0f ? 0.0f : w / sum;
+    } else {
+        w = chosen ? logistic(logit) : 0.0f;
+        if (a.renormalise) {
+            const float sum = warp_sum(w);
+            w = sum == 0.0f ? 0.0f : w / sum;
+        }
+    }
+    if (chosen) {
+        a.index[token * a.k + lane] = mine;
+        a.weight[token * a.k + lane] = w * a.scale;
+    }
+}
+
+// Gradient of the logits from that of the weights (g = scale dweight, w before the
+// scale, p and s the scores):
+//   softmax, renormalised   dl_i = w_i (g_i - sum_j w_j g_j)          chosen i, else 0
+//   softmax                 dl_e = p_e ([e chosen] g_e - sum_j p_j g_j)
+//   logistic, renormalised  dl_i = w_i (1 - s_i) (g_i - sum_j w_j g_j)
+//   logistic                dl_i = s_i (1 - s_i) g_i
+// An index outside the experts (a dropped choice) takes no part.
+template <typename T, int kN>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+route_backward_kernel(const RouteArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t token = int64_t(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    if (token >= a.tokens) return;
+    const T* row = static_cast<const T*>(a.logits) + token * a.ld_logits;
+    int e = -1;
+    float g = 0.0f, logit = -INFINITY;
+    if (lane < a.k) {
+        e = a.index[token * a.k + lane];
+        if (e < 0 || e >= a.experts) e = -1;
+        else {
+            g = a.weight[token * a.k + lane] * a.scale;
+            logit = to_f32(row[e]);
+        }
+    }
+    float d[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) d[i] = 0.0f;
+    float mine;                                            // a chosen expert's gradient (added to d)
+    if (a.scoring == TE_MX_SCORE_SOFTMAX) {
+        if (a.renormalise) {
+            const float most = warp_max(logit);
+            const float p = logit != -INFINITY ? expf(logit - most) : 0.0f;
+            const float sum = warp_sum(p), w = sum == 0.0f ? 0.0f : p / sum;
+            mine = w * (g - warp_sum(w * g));
+        } else {
+            float l[kN], most, sum;
+            load_logits<T, kN>(a, token, lane, l);
+            softmax_sum(l, most, sum);
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float p = logit != -INFINITY ? expf(logit - most) * inv : 0.0f;
+            const float total = warp_sum(p * g);
+            mine = p * (g - total);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) d[i] = l[i] == -INFINITY ? 0.0f : -total * (expf(l[i] - most) * inv);
+        }
+    } else {
+        const float s = e < 0 ? 0.0f : logistic(logit), rest = logistic(-logit);
+        if (a.renormalise) {
+            const float sum = warp_sum(s), w = sum == 0.0f ? 0.0f : s / sum;
+            const float total = warp_sum(w * g);
+            mine = e < 0 ? 0.0f : w * rest * (g - total);
+        } else {
+            mine = e < 0 ? 0.0f : s * rest * g;
+        }
+    }
+    for (int j = 0; j < a.k; ++j) {
+        const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
+        const float vj = __shfl_sync(0xFFFFFFFFu, mine, j);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (ej == lane + 32 * i) d[i] = vj;
+    }
+    T* out = static_cast<T*>(a.dlogits) + token * a.ld_dlogits;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (lane + 32 * i < a.experts) out[lane + 32 * i] = from_f32<T>(d[i]);
+}
+
+// ---------------------------------------------------------------- slots sorted by expert
+
+// A stable counting sort in one launch: a cluster of blocks, each with a contiguous
+// part of the slots, each warp with a contiguous part of its block's.  Every warp
+// counts its slots by expert (in shared memory of its own, so no atomic's order
+// matters); the counts are summed over the warps and, through distributed shared
+// memory, over the blocks; then every warp goes through its slots again, 32 at a time,
+// and gives each slot its expert's next row: the slots of one expert in a group of 32
+// find each other with a match, and their order among themselves is the lanes'.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+constexpr int kMaxExperts = 1024;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int32_t remote_load(const int32_t* p, uint32_t rank) {
+    uint32_t addr;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1)
+moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t experts, int blocks, int32_t* __restrict__ group_m,
+                int32_t* __restrict__ row, int32_t* __restrict__ slot, unsigned int* status) {
+    extern __shared__ int32_t counts[];                    // [kSortWarps][experts]: counts, then next rows
+    __shared__ int32_t total[kMaxExperts];                 // of this block's slots (read by the other blocks)
+    __shared__ int32_t warp_total[kSortWarps];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int t = int(threadIdx.x), lane = t & 31, warp = t >> 5;
+    const uint32_t rank = blocks > 1 ? cluster_rank() : 0u;
+    // this warp's slots: whole groups of 32
+    const int64_t groups = (slots + 31) / 32, parts = int64_t(blocks) * kSortWarps;
+    const int64_t part = int64_t(rank) * kSortWarps + warp;
+    const int64_t s0 = 32 * (groups * part / parts), s1 = 32 * (groups * (part + 1) / parts);
+    for (int i = t; i < kSortWarps * experts; i += kSortThreads) counts[i] = 0;
+    __syncthreads();
+    int32_t* mine = counts + warp * experts;
+    for (int64_t s = s0 + lane; s < s1; s += 32) {
+        const int32_t e = s < slots ? index[s] : -1;
+        if (e >= experts) set_device_status(status, kStatusBadArg);
+        else if (e >= 0) atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+    // over the warps: counts become the sums of the warps before
+    int32_t here = 0;
+    if (t < experts) {
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int32_t c = counts[w * experts + t];
+            counts[w * experts + t] = here;
+            here += c;
+        }
+        total[t] = here;
+    }
+    if (blocks > 1) cluster_sync_all();
+    else __syncthreads();
+    // over the blocks: this expert's slots in the blocks before, and in all
+    int32_t before = 0, all = here;
+    if (blocks > 1 && t < experts) {
+        all = 0;
+        for (int b = 0; b < blocks; ++b) {
+            const int32_t c = remote_load(&total[t], uint32_t(b));
+            if (b < int(rank)) before += c;
+            all += c;
+        }
+    }
+    // over the experts: an inclusive scan of `all`
+    int32_t upto = t < experts ? all : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) warp_total[warp] = upto;
+    __syncthreads();
+    int32_t of_warps = lane < kSortWarps ? warp_total[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, of_warps, o);
+        if (lane >= o) of_warps += v;
+    }
+    const int32_t kept = __shfl_sync(0xFFFFFFFFu, of_warps, 31);
+    upto += warp > 0 ? __shfl_sync(0xFFFFFFFFu, of_warps, warp - 1) : 0;
+    if (t < experts) {
+        const int32_t base = upto - all + before;
+        for (int w = 0; w < kSortWarps; ++w) counts[w * experts + t] += base;
+        if (rank == 0) group_m[t] = all;
+    }
+    __syncthreads();
+    for (int64_t s = s0 + lane; s < s1; s += 32) {         // (s1 - s0 is a multiple of 32: whole warps)
+        const int32_t e = s < slots ? index[s] : -1;
+        const bool live = e >= 0 && e < experts;
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, live ? e : -1);
+        int32_t r = -1;
+        if (live) r = mine[e] + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (live && lane == 31 - __clz(peers)) mine[e] = r + 1;
+        __syncwarp();
+        if (s < slots) {
+            row[s] = r;
+            if (live) slot[r] = int32_t(s);
+        }
+    }
+    // rows without a slot
+    for (int64_t r = kept + int64_t(rank) * kSortThreads + t; r < slots; r += int64_t(blocks) * kSortThreads) slot[r] = -1;
+    if (blocks > 1) cluster_sync_all();                    // no block leaves while another may still read its counts
+}
+
+// ---------------------------------------------------------------- dispatch
+
+// Every token's row is read once and written to the rows of its slots.  A block takes
+// a token's part of kCopyThreads pieces of kBytes bytes; the scales of MXFP8 rows go
+// byte by byte with the first part.
+constexpr int kCopyThreads = 128;
+constexpr int kCopyPieces = 4;                   // per thread
+template <int kBytes> struct PieceOf;
+template <> struct PieceOf<16> { using Type = uint4; };
+template <> struct PieceOf<4> { using Type = uint32_t; };
+template <> struct PieceOf<2> { using Type = uint16_t; };
+template <> struct PieceOf<1> { using Type = uint8_t; };
+
+template <int kBytes>
+__global__ void __launch_bounds__(kCopyThreads)
+moe_dispatch_kernel(const DispatchArgs a, int parts, unsigned int* status) {
+    using Piece = typename PieceOf<kBytes>::Type;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t token = int64_t(blockIdx.x) / parts;
+    const int part = int(int64_t(blockIdx.x) % parts);
+    const int64_t pieces = a.row_bytes / kBytes, p0 = int64_t(part) * kCopyThreads * kCopyPieces + threadIdx.x;
+    const Piece* x = reinterpret_cast<const Piece*>(a.x + token * a.ld_x);
+    Piece v[kCopyPieces];
+#pragma unroll
+    for (int i = 0; i < kCopyPieces; ++i)
+        if (p0 + i * kCopyThreads < pieces) v[i] = x[p0 + i * kCopyThreads];
+    for (int j = 0; j < a.k; ++j) {
+        const int64_t r = a.row[token * a.k + j];
+        if (r < 0) continue;
+        if (r >= a.total_rows) {
+            if (threadIdx.x == 0) set_device_status(status, kStatusBadArg);
+            continue;
+        }
+        Piece* out = reinterpret_cast<Piece*>(a.out + r * a.ld_out);
+#pragma unroll
+        for (int i = 0; i < kCopyPieces; ++i)
+            if (p0 + i * kCopyThreads < pieces) out[p0 + i * kCopyThreads] = v[i];
+        if (a.scales && part == 0)
+            for (int64_t b = threadIdx.x; b < a.scale_bytes; b += kCopyThreads)
+                a.out_scales[r * a.ld_out_scales + b] = a.scales[token * a.ld_scales + b];
+    }
+}
+
+// ---------------------------------------------------------------- combine
+
+// out[t] = sum_j weight[t][j] y[row[t][j]] + residual[t], in fp32, the choices in
+// order, rounded once.  kVec: rows on 16-byte boundaries, a 16-byte vector per thread
+// and step; else an element.
+constexpr int kCombineThreads = 256;
+constexpr int kMaxChoices = 32;
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kCombineThreads)
+moe_combine_kernel(const CombineArgs a, int parts, unsigned int* status) {
+    using V = Vec<T>;
+    __shared__ int32_t row[kMaxChoices];
+    __shared__ float weight[kMaxChoices];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t token = int64_t(blockIdx.x) / parts;
+    const int64_t i = int64_t(int64_t(blockIdx.x) % parts) * kCombineThreads + threadIdx.x;
+    if (threadIdx.x < a.k) {
+        int32_t r = a.row[token * a.k + threadIdx.x];
+        if (r >= a.total_rows) {
+            set_device_status(status, kStatusBadArg);
+            r = -1;
+        }
+        row[threadIdx.x] = r;
+        weight[threadIdx.x] = a.weight ? a.weight[token * a.k + threadIdx.x] : 1.0f;
+    }
+    __syncthreads();
+    const T* y = static_cast<const T*>(a.y);
+    const T* res = a.residual ? static_cast<const T*>(a.residual) + token * a.ld_residual : nullptr;
+    T* out = static_cast<T*>(a.out) + token * a.ld_out;
+    if constexpr (kVec) {
+        if (i >= a.hidden / V::kN) return;
+        uint64_t s[V::kPairs];
+#pragma unroll
+        for (int q = 0; q < V::kPairs; ++q) s[q] = 0;
+        for (int j0 = 0; j0 < a.k; j0 += 8) {              // eight rows in flight
+            uint4 w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j0 + j < a.k && row[j0 + j] >= 0) w[j] = reinterpret_cast<const uint4*>(y + row[j0 + j] * a.ld_y)[i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j0 + j < a.k && row[j0 + j] >= 0) {
+                    const uint64_t f = f32x2::both(weight[j0 + j]);
+#pragma unroll
+                    for (int q = 0; q < V::kPairs; ++q) s[q] = f32x2::fma(V::pair(w[j], q), f, s[q]);
+                }
+        }
+        if (res) {
+            const uint4 w = reinterpret_cast<const uint4*>(res)[i];
+#pragma unroll
+            for (int q = 0; q < V::kPairs; ++q) s[q] = f32x2::add(s[q], V::pair(w, q));
+        }
+        reinterpret_cast<uint4*>(out)[i] = V::from_pairs(s);
+    } else {
+        if (i >= a.hidden) return;
+        float s = 0.0f;
+        for (int j = 0; j < a.k; ++j)
+            if (row[j] >= 0) s = fmaf(to_f32(y[row[j] * a.ld_y + i]), weight[j], s);
+        out[i] = from_f32<T>(res ? s + to_f32(res[i]) : s);
+    }
+}
+
+// dy[row[t][j]] = weight[t][j] dout[t],  dweight[t][j] = <dout[t], y[row[t][j]]>.  A
+// warp per slot, so that a row's product stays in the warp; the warps of a token read
+// its dout from L1.  dweight of a slot without a row is 0.
+constexpr int kSlotWarps = 8;
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kSlotWarps * 32)
+moe_combine_backward_kernel(const CombineArgs a, unsigned int* status) {
+    using V = Vec<T>;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t s = int64_t(blockIdx.x) * kSlotWarps + (threadIdx.x >> 5);
+    if (s >= a.tokens * a.k) return;
+    const int64_t token = s / a.k;
+    int64_t r = a.row[s];
+    if (r >= a.total_rows) {
+        set_device_status(status, kStatusBadArg);
+        r = -1;
+    }
+    if (r < 0) {
+        if (a.dweight && lane == 0) a.dweight[s] = 0.0f;
+        return;
+    }
+    const T* dout = static_cast<const T*>(a.dout) + token * a.ld_dout;
+    const T* y = static_cast<const T*>(a.y) + r * a.ld_y;
+    T* dy = a.dy ? static_cast<T*>(a.dy) + r * a.ld_dy : nullptr;
+    const float w = a.weight[s];
+    float dot = 0.0f;
+    if constexpr (kVec) {
+        const uint64_t w2 = f32x2::both(w);
+        const int64_t nvec = a.hidden / V::kN;
+        uint64_t sum = 0;
+        constexpr int kAhead = 4;                          // vectors in flight
+        for (int64_t i0 = lane; i0 < nvec; i0 += 32 * kAhead) {
+            uint4 d[kAhead], v[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int64_t i = i0 + 32 * q;
+                d[q] = i < nvec ? reinterpret_cast<const uint4*>(dout)[i] : make_uint4(0, 0, 0, 0);
+                if (a.dweight) v[q] = i < nvec ? reinterpret_cast<const uint4*>(y)[i] : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int64_t i = i0 + 32 * q;
+                if (i >= nvec) break;
+                uint64_t o[V::kPairs];
+#pragma unroll
+                for (int p = 0; p < V::kPairs; ++p) {
+                    const uint64_t dp = V::pair(d[q], p);
+                    o[p] = f32x2::mul(dp, w2);
+                    if (a.dweight) sum = f32x2::fma(dp, V::pair(v[q], p), sum);
+                }
+                if (dy) reinterpret_cast<uint4*>(dy)[i] = V::from_pairs(o);
+            }
+        }
+        dot = f32x2::lo(sum) + f32x2::hi(sum);
+    } else {
+        for (int64_t i = lane; i < a.hidden; i += 32) {
+            const float d = to_f32(dout[i]);
+            if (a.dweight) dot = fmaf(d, to_f32(y[i]), dot);
+            if (dy) dy[i] = from_f32<T>(d * w);
+        }
+    }
+    if (a.dweight) {
+        dot = warp_sum(dot);
+        if (lane == 0) a.dweight[s] = dot;
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+template <typename T, int kN>
+cudaError_t route_n(const RouteArgs& a, bool backward, cudaStream_t stream) {
+    const dim3 grid(unsigned((a.tokens + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
+    return backward ? launch_dependent(route_backward_kernel<T, kN>, grid, block, stream, a)
+                    : launch_dependent(route_kernel<T, kN>, grid, block, stream, a);
+}
+
+template <typename T>
+cudaError_t route_t(const RouteArgs& a, bool backward, cudaStream_t stream) {
+    if (a.experts <= 32) return route_n<T, 1>(a, backward, stream);
+    if (a.experts <= 64) return route_n<T, 2>(a, backward, stream);
+    if (a.experts <= 128) return route_n<T, 4>(a, backward, stream);
+    if (a.experts <= 256) return route_n<T, 8>(a, backward, stream);
+    if (a.experts <= 512) return route_n<T, 16>(a, backward, stream);
+    return route_n<T, 32>(a, backward, stream);
+}
+
+te_mx_status route_any(const RouteArgs& a, bool backward, cudaStream_t stream) {
+    cudaError_t e = a.dtype == TE_MX_FP32   ? route_t<float>(a, backward, stream)
+                    : a.dtype == TE_MX_FP16 ? route_t<__half>(a, backward, stream)
+                                            : route_t<__nv_bfloat16>(a, backward, stream);
+    return cuda_status(e, "router kernel launch");
+}
+
+template <int kBytes>
+cudaError_t dispatch_launch(const DispatchArgs& a, unsigned int* status, cudaStream_t stream) {
+    const int64_t per = int64_t(kCopyThreads) * kCopyPieces, pieces = a.row_bytes / kBytes;
+    const int64_t parts = pieces > per ? (pieces + per - 1) / per : 1;
+    return launch_dependent(moe_dispatch_kernel<kBytes>, dim3(unsigned(a.tokens * parts)), dim3(kCopyThreads), stream, a,
+                            int(parts), status);
+}
+
+template <typename T>
+cudaError_t combine(const CombineArgs& a, bool backward, unsigned int* status, cudaStream_t stream) {
+    auto fits = [&](const void* p, int64_t ld, int64_t rows) { return !p || rows_on16(p, ld, rows, sizeof(T)); };
+    const bool vec = a.hidden % Vec<T>::kN == 0 && fits(a.y, a.ld_y, a.total_rows) && fits(a.residual, a.ld_residual, a.tokens) &&
+                     fits(a.out, a.ld_out, a.tokens) && fits(a.dout, a.ld_dout, a.tokens) && fits(a.dy, a.ld_dy, a.total_rows);
+    if (backward) {
+        const dim3 grid(unsigned((a.tokens * a.k + kSlotWarps - 1) / kSlotWarps)), block(kSlotWarps * 32);
+        return vec ? launch_dependent(moe_combine_backward_kernel<T, true>, grid, block, stream, a, status)
+                   : launch_dependent(moe_combine_backward_kernel<T, false>, grid, block, stream, a, status);
+    }
+    const int64_t n = vec ? a.hidden / Vec<T>::kN : a.hidden, parts = (n + kCombineThreads - 1) / kCombineThreads;
+    const dim3 grid(unsigned(a.tokens * parts)), block(kCombineThreads);
+    return vec ? launch_dependent(moe_combine_kernel<T, true>, grid, block, stream, a, int(parts), status)
+               : launch_dependent(moe_combine_kernel<T, false>, grid, block, stream, a, int(parts), status);
+}
+
+te_mx_status combine_any(const CombineArgs& a, bool backward, cudaStream_t stream) {
+    unsigned int* status = nullptr;
+    te_mx_status st = device_status_ptr(&status);
+    if (st != TE_MX_OK) return st;
+    cudaError_t e = a.dtype == TE_MX_FP32   ? combine<float>(a, backward, status, stream)
+                    : a.dtype == TE_MX_FP16 ? combine<__half>(a, backward, status, stream)
+                                            : combine<__nv_bfloat16>(a, backward, status, stream);
+    return cuda_status(e, "combine kernel launch");
+}
+
+}  // namespace
+
+te_mx_status route_launch(const RouteArgs& a, cudaStream_t stream) { return route_any(a, false, stream); }
+te_mx_status route_backward_launch(const RouteArgs& a, cudaStream_t stream) { return route_any(a, true, stream); }
+
+te_mx_status moe_sort_launch(const int32_t* index, int64_t slots, int32_t experts, int32_t* group_m, int32_t* row,
+                             int32_t* slot, cudaStream_t stream) {
+    unsigned int* status = nullptr;
+    te_mx_status st = device_status_ptr(&status);
+    if (st != TE_MX_OK) return st;
+    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(moe_sort_kernel), kSortWarps * kMaxExperts * 4);
+    if (e != cudaSuccess) return cuda_status(e, "expert sort kernel attributes");
+    const int blocks = slots > 8 * kSortThreads ? kSortCluster : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = size_t(kSortWarps) * size_t(experts) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(blocks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, moe_sort_kernel, index, slots, experts, blocks, group_m, row, slot, status);
+    return cuda_status(e, "expert sort kernel launch");
+}
+
+te_mx_status moe_dispatch_launch(const DispatchArgs& a, cudaStream_t stream) {
+    unsigned int* status = nullptr;
+    te_mx_status st = device_status_ptr(&status);
+    if (st != TE_MX_OK) return st;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) | uintptr_t(a.row_bytes) |
+                          (a.tokens > 1 ? uintptr_t(a.ld_x) : 0) | (a.total_rows > 1 ? uintptr_t(a.ld_out) : 0);
+    cudaError_t e = all % 16 == 0  ? dispatch_launch<16>(a, status, stream)
+                    : all % 4 == 0 ? dispatch_launch<4>(a, status, stream)
+                    : all % 2 == 0 ? dispatch_launch<2>(a, status, stream)
+                                   : dispatch_launch<1>(a, status, stream);
+    return cuda_status(e, "dispatch kernel launch");
+}
+
+te_mx_status moe_combine_launch(const CombineArgs& a, cudaStream_t stream) { return combine_any(a, false, stream); }
+te_mx_status moe_combine_backward_launch(const CombineArgs& a, cudaStream_t stream) { return combine_any(a, true, stream); }
+
+}  // namespace temx

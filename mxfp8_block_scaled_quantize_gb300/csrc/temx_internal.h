@@ -104,6 +104,99 @@ constexpr int kLnMaxParts = 304;                 // partial sums per column, at 
 int ln_backward_parts(int64_t rows);
 te_mx_status ln_backward_launch(const LnBackwardArgs& a, cudaStream_t stream);
 
+struct RmsArgs {
+    const void* x;           // [rows x hidden] of `dtype`, pitch ld_x
+    int64_t rows, hidden, ld_x;
+    int32_t dtype, param_dtype;      // te_mx_dtype
+    const void* residual;    // [rows x hidden], pitch ld_residual, or null (then z is null too)
+    int64_t ld_residual;
+    const void* gamma;       // [hidden]
+    float eps;
+    void* z;                 // [rows x hidden], pitch ld_z
+    int64_t ld_z;
+    void* y;                 // [rows x hidden], pitch ld_y; null: quantised copies only
+    int64_t ld_y;
+    float* rsigma;           // fp32 [rows] or null (required with q_col)
+    uint8_t* q_row; uint8_t* s_row; int64_t ld_s_row;                       // quantising entry point only
+    uint8_t* q_col; uint8_t* s_col; int64_t ld_s_col;
+};
+te_mx_status rms_forward_launch(const RmsArgs& a, cudaStream_t stream);
+te_mx_status rms_quantize_launch(const RmsArgs& a, cudaStream_t stream);
+int64_t rms_quantize_max_hidden();
+
+struct RmsBackwardArgs {
+    const void* dy;          // [rows x hidden] of `dtype`, pitch ld_dy
+    int64_t ld_dy;
+    const void* z;
+    int64_t rows, hidden, ld_z;
+    int32_t dtype, param_dtype;
+    const void* gamma;
+    const float* rsigma;
+    const void* dz;          // [rows x hidden], pitch ld_dz, or null
+    int64_t ld_dz;
+    void* dx;                // [rows x hidden], pitch ld_dx, or null
+    int64_t ld_dx;
+    void* dgamma;            // [hidden] of `param_dtype`, or null
+    float* partial;          // fp32 [parts][hidden] (with dgamma)
+};
+constexpr int kRmsMaxParts = 304;                // partial sums per column, at most (two per SM)
+int rms_backward_parts(int64_t rows);
+te_mx_status rms_backward_launch(const RmsBackwardArgs& a, cudaStream_t stream);
+
+struct RouteArgs {
+    const void* logits;      // [tokens x experts] of `dtype`, pitch ld_logits
+    int64_t tokens, ld_logits;
+    int32_t experts, k, dtype;
+    const float* bias;       // fp32 [experts] or null (forward)
+    int32_t scoring;         // te_mx_scoring
+    bool renormalise;
+    float scale;
+    int32_t* index;          // [tokens x k]: written by the forward pass, read by the backward
+    float* weight;           // fp32 [tokens x k]: the weights, or their gradient
+    void* dlogits;           // [tokens x experts] of `dtype`, pitch ld_dlogits (backward)
+    int64_t ld_dlogits;
+};
+te_mx_status route_launch(const RouteArgs& a, cudaStream_t stream);
+te_mx_status route_backward_launch(const RouteArgs& a, cudaStream_t stream);
+
+te_mx_status moe_sort_launch(const int32_t* index, int64_t slots, int32_t experts, int32_t* group_m, int32_t* row,
+                             int32_t* slot, cudaStream_t stream);
+
+struct DispatchArgs {
+    const uint8_t* x;        // [tokens] rows of row_bytes, pitch ld_x bytes
+    int64_t ld_x, row_bytes;
+    const uint8_t* scales;   // [tokens] rows of scale_bytes, or null
+    int64_t ld_scales, scale_bytes;
+    const int32_t* row;      // [tokens x k]
+    int64_t tokens, total_rows;
+    int32_t k;
+    uint8_t* out;
+    int64_t ld_out;
+    uint8_t* out_scales;
+    int64_t ld_out_scales;
+};
+te_mx_status moe_dispatch_launch(const DispatchArgs& a, cudaStream_t stream);
+
+struct CombineArgs {
+    const void* y;           // [total_rows x hidden] of `dtype`, pitch ld_y
+    int64_t ld_y, total_rows, hidden;
+    int32_t dtype, k;
+    const int32_t* row;      // [tokens x k]
+    int64_t tokens;
+    const float* weight;     // fp32 [tokens x k] or null (all 1)
+    const void* residual;    // [tokens x hidden], pitch ld_residual, or null (forward)
+    int64_t ld_residual;
+    void* out;               // [tokens x hidden], pitch ld_out (forward)
+    int64_t ld_out;
+    const void* dout;        // backward
+    int64_t ld_dout;
+    void* dy;                // [total_rows x hidden], pitch ld_dy, or null
+    int64_t ld_dy;
+    float* dweight;          // fp32 [tokens x k] or null
+};
+te_mx_status moe_combine_launch(const CombineArgs& a, cudaStream_t stream);
+te_mx_status moe_combine_backward_launch(const CombineArgs& a, cudaStream_t stream);
+
 struct GatedBackwardArgs {
     const void* dh;          // bf16 [rows x F], pitch ld_dh
     int64_t ld_dh;
