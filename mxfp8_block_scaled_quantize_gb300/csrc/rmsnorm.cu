@@ -328,11 +328,16 @@ rms_colwise_kernel(const RmsArgs a, unsigned col_units) {
 
 // Rows on 16-byte boundaries: one pass over dy, z and dz, persistent.  A group of
 // threads owns the same columns (kV vectors per thread) of every row that it takes,
-// so the sums of dy xh over the rows stay in registers.  dy and z come through a
-// ring of rows in shared memory, one bulk copy each, and their words stay in
-// registers from the row's sum to its dx; dz is loaded while the sum crosses the
-// group.  The groups of a block are joined at the end, so that every block leaves
-// one partial sum per column.
+// so the sums of dy xh over the rows stay in registers.  The rows come through a ring
+// in shared memory, one bulk copy of each operand, and are read there twice: for the
+// row's sum, and for its dx once the sum is known, so that no word waits in registers.
+// The sum of the next row is taken before the dx of this one, so that its way across
+// the warp and the group is hidden behind that; a row's stage is filled again after
+// the next row's barrier, which every warp reaches past its last read of the row.
+// The groups of a block are joined at the end, so that every block leaves one partial
+// sum per column.
+// kOnce: a ring of one stage, for rows of which two do not fit: words stay in
+// registers from the sum to dx, and dz is loaded from global memory.
 constexpr int kBwdMaxGroups = 15;                // (named barriers)
 constexpr int kBwdMaxStages = 16;
 constexpr int kBwdSmem = 200 * 1024;             // the ring
@@ -342,19 +347,20 @@ struct RmsBwdShape {
     int group;       // threads per group
     int groups;      // groups per block
     int stages;      // rows of a group's ring
+    int streams;     // operands in the ring: dy, z and perhaps dz
 };
 
-template <typename T, bool kP32, int kV, int kMost>
+template <typename T, bool kP32, int kV, int kMost, bool kOnce>
 __global__ void __launch_bounds__(kMost, 1)
 rms_backward_vec_kernel(const RmsBackwardArgs a, const RmsBwdShape sh, unsigned int* status) {
     using V = Vec<T>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[kBwdMaxGroups][kBwdMaxStages];          // a row's dy and z landed
+    __shared__ __align__(8) uint64_t full[kBwdMaxGroups][kBwdMaxStages];          // a row's operands landed
     __shared__ float warp_part[2][kMost / 32];             // by parity of the row
 
     const int group = threadIdx.x / sh.group, t = threadIdx.x % sh.group, lane = threadIdx.x & 31;
-    const int gwarps = sh.group >> 5, gwarp0 = group * gwarps;
-    const uint32_t bytes = uint32_t(sh.nvec) * 16, stage_bytes = 2 * bytes;       // dy, then z
+    const int gwarps = sh.group >> 5;
+    const uint32_t bytes = uint32_t(sh.nvec) * 16, stage_bytes = uint32_t(sh.streams) * bytes;       // dy, z, dz
     const uint32_t ring = smem_u32(smem) + uint32_t(group * sh.stages) * stage_bytes;
     const int64_t first = int64_t(blockIdx.x) * sh.groups + group, step = int64_t(gridDim.x) * sh.groups;
     const int n_mine = first < a.rows ? int((a.rows - first + step - 1) / step) : 0;
@@ -371,94 +377,119 @@ rms_backward_vec_kernel(const RmsBackwardArgs a, const RmsBwdShape sh, unsigned 
         mbar_arrive_expect_tx(bar, stage_bytes);
         bulk_load_row(dst, static_cast<const T*>(a.dy) + row * a.ld_dy, bytes, bar);
         bulk_load_row(dst + bytes, static_cast<const T*>(a.z) + row * a.ld_z, bytes, bar);
+        if (sh.streams == 3) bulk_load_row(dst + 2 * bytes, static_cast<const T*>(a.dz) + row * a.ld_dz, bytes, bar);
     };
     if (t == 0)
         for (int i = 0; i < sh.stages && i < n_mine; ++i) load(i, i);
 
-    // (threads past the row's end work on its first vector with zeros in dy, so
-    // that nothing below branches; only their stores are left out)
     ParamVec<T, kP32> ga[kV];
     uint64_t dga[kV][V::kPairs];
     bool live[kV];
-    uint32_t at[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
         const int j = t + v * sh.group;
         live[v] = j < sh.nvec;
-        at[v] = ring + 16u * uint32_t(live[v] ? j : 0);
         ga[v].load(a.gamma, live[v] ? j : 0);
 #pragma unroll
         for (int k = 0; k < V::kPairs; ++k) dga[v][k] = 0;
     }
+    const uint32_t at = ring + 16u * uint32_t(t), apart = 16u * uint32_t(sh.group);          // of its vectors
+    constexpr bool kUnpackGamma = kV * V::kN > 16 || kMost > 512;      // (else it stays unpacked in registers)
     const float inv_h = 1.0f / float(a.hidden);
-    const float* rs_p = a.rsigma + first;
-    float rs = n_mine > 0 ? __ldg(rs_p) : 0.0f;
     bool ok = true;                                        // false once a wait gave up: no waits or copies from then on
-    int stage = 0;
-    uint32_t phase = 0;
-    for (int i = 0; i < n_mine; ++i) {
-        const int64_t row = first + i * step;
-        const float r = rs;
-        const uint64_t rs2 = f32x2::both(r);
-        uint4 wr[kV];
-        if (a.dz) {
-            const uint4* dz = reinterpret_cast<const uint4*>(static_cast<const T*>(a.dz) + row * a.ld_dz) + t;
-#pragma unroll
-            for (int v = 0; v < kV; ++v) wr[v] = live[v] ? dz[v * sh.group] : make_uint4(0, 0, 0, 0);
-        }
-        ok = ok && mbar_wait(smem_u32(&full[group][stage]), phase, status);
-        uint4 wd[kV], wz[kV];
+    uint4 wd[kOnce ? kV : 1], wz[kOnce ? kV : 1];
+    // a thread's part of a row's sum of g xh; its part of dgamma's
+    auto sum_of = [&](uint32_t here, uint64_t rs2) {
         uint64_t s = 0;
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            wd[v] = lds128(at[v] + uint32_t(stage) * stage_bytes);
-            wz[v] = lds128(at[v] + uint32_t(stage) * stage_bytes + bytes);
-            if (!live[v]) wd[v] = make_uint4(0, 0, 0, 0);
+            if (!live[v]) continue;
+            uint4& d4 = wd[kOnce ? v : 0];
+            uint4& z4 = wz[kOnce ? v : 0];
+            d4 = lds128(at + here + v * apart);
+            z4 = lds128(at + here + bytes + v * apart);
+            if constexpr (kUnpackGamma)
 #pragma unroll
-            for (int q = 0; q < ParamVec<T, kP32>::kWords; ++q) unpack_again(ga[v].w[q]);
+                for (int q = 0; q < ParamVec<T, kP32>::kWords; ++q) unpack_again(ga[v].w[q]);
 #pragma unroll
             for (int k = 0; k < V::kPairs; ++k) {
-                const uint64_t d = V::pair(wd[v], k), xh = f32x2::mul(V::pair(wz[v], k), rs2);
+                const uint64_t d = V::pair(d4, k), xh = f32x2::mul(V::pair(z4, k), rs2);
                 s = f32x2::fma(f32x2::mul(d, ga[v].pair(k)), xh, s);
                 dga[v][k] = f32x2::fma(d, xh, dga[v][k]);
             }
         }
-        rs_p += step;
-        if (i + 1 < n_mine) rs = __ldg(rs_p);              // a row ahead
-        // over the warp, then over the group's warps (every warp adds them up, lane =
-        // warp).  A parity's slots are read before the next row's barrier, and written
-        // again after it.
-        float total = warp_sum(f32x2::lo(s) + f32x2::hi(s));
-        if (gwarps > 1) {
-            float* part = &warp_part[i & 1][gwarp0];
-            if (lane == 0) part[t >> 5] = total;
-            group_barrier(1 + group, sh.group);
-            total = warp_sum(lane < gwarps ? part[lane] : 0.0f);
-        } else {
-            __syncwarp();                                  // every lane has read the stage
+        return f32x2::lo(s) + f32x2::hi(s);
+    };
+    // over the group's warps, in order (a parity's slots are read before the next row's
+    // barrier, and written again after it)
+    auto across_group = [&](float s, int i) {
+        if (gwarps == 1) {
+            __syncwarp();
+            return s;
         }
-        if (t == 0 && ok && i + sh.stages < n_mine) load(i + sh.stages, stage);      // (every warp has read it)
-        if (++stage == sh.stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
-        if (a.dx) {
-            // dx = rs g - rs c xh + dz, xh = z rs
-            const uint64_t k2 = f32x2::both(-r * r * (total * inv_h));
-            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.ld_dx) + t;
+        float* part = &warp_part[i & 1][group * gwarps];
+        if (lane == 0) part[t >> 5] = s;
+        group_barrier(1 + group, sh.group);
+        return warp_sum(lane < gwarps ? part[lane] : 0.0f);
+    };
+    // dx = rs g - rs c xh + dz, xh = z rs
+    auto dx_of = [&](int64_t row, uint32_t here, float r, float total) {
+        const uint64_t rs2 = f32x2::both(r), k2 = f32x2::both(-r * r * (total * inv_h));
+        const uint4* dz = a.dz ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.dz) + row * a.ld_dz) + t : nullptr;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.ld_dx) + t;
 #pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                uint64_t o[V::kPairs];
-                unpack_again(wd[v]);
-                unpack_again(wz[v]);
+        for (int v = 0; v < kV; ++v) {
+            if (!live[v]) continue;
+            uint4& d4 = wd[kOnce ? v : 0];
+            uint4& z4 = wz[kOnce ? v : 0];
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if constexpr (kOnce) {
+                unpack_again(d4);
+                unpack_again(z4);
+            } else {
+                d4 = lds128(at + here + v * apart);
+                z4 = lds128(at + here + bytes + v * apart);
+            }
+            if (!kOnce && sh.streams == 3) w = lds128(at + here + 2 * bytes + v * apart);
+            else if (dz) w = dz[v * sh.group];
+            if constexpr (kUnpackGamma)
 #pragma unroll
                 for (int q = 0; q < ParamVec<T, kP32>::kWords; ++q) unpack_again(ga[v].w[q]);
+            uint64_t o[V::kPairs];
 #pragma unroll
-                for (int k = 0; k < V::kPairs; ++k) {
-                    o[k] = f32x2::fma(f32x2::mul(V::pair(wd[v], k), ga[v].pair(k)), rs2, f32x2::mul(V::pair(wz[v], k), k2));
-                    if (a.dz) o[k] = f32x2::add(o[k], V::pair(wr[v], k));
-                }
-                if (live[v]) out[v * sh.group] = V::from_pairs(o);
+            for (int k = 0; k < V::kPairs; ++k) {
+                o[k] = f32x2::fma(f32x2::mul(V::pair(d4, k), ga[v].pair(k)), rs2, f32x2::mul(V::pair(z4, k), k2));
+                if (dz) o[k] = f32x2::add(o[k], V::pair(w, k));
+            }
+            out[v * sh.group] = V::from_pairs(o);
+        }
+    };
+    const float* rs_p = a.rsigma + first;
+    if constexpr (kOnce) {
+        for (int i = 0; i < n_mine; ++i) {
+            const float r = __ldg(rs_p + i * step);
+            ok = ok && mbar_wait(smem_u32(&full[group][0]), uint32_t(i & 1), status);
+            const float total = across_group(warp_sum(sum_of(0, f32x2::both(r))), i);
+            if (t == 0 && ok && i + 1 < n_mine) load(i + 1, 0);        // every warp has read the row
+            if (a.dx) dx_of(first + i * step, 0, r, total);
+        }
+    } else {
+        int stage = 0, before = 0;                         // of this row, of the row before
+        uint32_t phase = 0;
+        float rs = n_mine > 0 ? __ldg(rs_p) : 0.0f;
+        for (int i = 0; i < n_mine; ++i) {
+            const float r = rs;
+            const uint32_t here = uint32_t(stage) * stage_bytes;
+            if (i + 1 < n_mine) rs = __ldg(rs_p + (i + 1) * step);
+            ok = ok && mbar_wait(smem_u32(&full[group][stage]), phase, status);
+            const float total = across_group(warp_sum(sum_of(here, f32x2::both(r))), i);
+            // (every warp is past the row before)
+            if (t == 0 && ok && i > 0 && i - 1 + sh.stages < n_mine) load(i - 1 + sh.stages, before);
+            if (a.dx) dx_of(first + i * step, here, r, total);
+            before = stage;
+            if (++stage == sh.stages) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
     }
@@ -824,19 +855,22 @@ cudaError_t forward(const RmsArgs& a, int sms, cudaStream_t stream) {
     return forward_any<T, float>(a, sms, stream);
 }
 
-template <typename T, bool kP32, int kV, int kMost>
-cudaError_t backward_vec_launch(const RmsBackwardArgs& a, int nvec, int sms, unsigned int* status, int* parts, cudaStream_t stream) {
-    auto kern = rms_backward_vec_kernel<T, kP32, kV, kMost>;
+template <typename T, bool kP32, int kV, int kMost, bool kOnce>
+cudaError_t backward_vec_launch(const RmsBackwardArgs& a, int nvec, int streams, int sms, unsigned int* status, int* parts,
+                                cudaStream_t stream) {
+    auto kern = rms_backward_vec_kernel<T, kP32, kV, kMost, kOnce>;
     RmsBwdShape sh{};
     sh.nvec = nvec;
+    sh.streams = streams;
+    const int row_bytes = streams * nvec * 16, least = kOnce ? 1 : 2;
     sh.group = row_threads(nvec, kV);
     sh.groups = kMost / sh.group;
     if (sh.groups > kBwdMaxGroups) sh.groups = kBwdMaxGroups;
     if (sh.groups > a.rows) sh.groups = int(a.rows);
-    while (sh.groups > 1 && sh.groups * nvec * 32 > kBwdSmem) --sh.groups;
-    sh.stages = kBwdSmem / (sh.groups * nvec * 32);
+    while (sh.groups > 1 && least * sh.groups * row_bytes > kBwdSmem) --sh.groups;
+    sh.stages = kOnce ? 1 : kBwdSmem / (sh.groups * row_bytes);
     if (sh.stages > kBwdMaxStages) sh.stages = kBwdMaxStages;
-    const int ring = sh.groups * sh.stages * nvec * 32, sums = sh.groups * nvec * Vec<T>::kN * 4;
+    const int ring = sh.groups * sh.stages * row_bytes, sums = sh.groups * nvec * Vec<T>::kN * 4;
     cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), kBwdSmem);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.rows + sh.groups - 1) / sh.groups;
@@ -856,16 +890,22 @@ cudaError_t backward_vec_launch(const RmsBackwardArgs& a, int nvec, int sms, uns
     return cudaLaunchKernelEx(&cfg, kern, a, sh, status);
 }
 
-// Vectors of a row that the ring kernel takes: 2 of 16 bits (4 of fp32) in each of
-// 896 threads at 72 registers, or twice as many in each of 512.
+// Vectors of a row that the ring kernel takes: kBwdV<T> in each of up to 896 threads, or
+// twice as many in each of 512 (both hold their sums and gamma in registers); 128 KB of
+// dy and z at most.
 template <typename T> constexpr int kBwdV = sizeof(T) == 4 ? 4 : 2;
 template <typename T> constexpr int kBwdMostVectors = 2 * kBwdV<T> * 512;
 
 template <typename T, bool kP32>
 cudaError_t backward_vec(const RmsBackwardArgs& a, int sms, unsigned int* status, int* parts, cudaStream_t stream) {
+    constexpr int kV = kBwdV<T>;
     const int nvec = int(a.hidden / Vec<T>::kN);
-    if (nvec <= kBwdV<T> * 896) return backward_vec_launch<T, kP32, kBwdV<T>, 896>(a, nvec, sms, status, parts, stream);
-    return backward_vec_launch<T, kP32, 2 * kBwdV<T>, 512>(a, nvec, sms, status, parts, stream);
+    // (dz in the ring too where two rows then fit)
+    const int streams = a.dz && 2 * 3 * 16 * nvec <= kBwdSmem ? 3 : 2;
+    if (2 * streams * 16 * nvec > kBwdSmem) return backward_vec_launch<T, kP32, 2 * kV, 512, true>(a, nvec, 2, sms, status, parts, stream);
+    if (nvec <= kV * 512) return backward_vec_launch<T, kP32, kV, 512, false>(a, nvec, streams, sms, status, parts, stream);
+    if (nvec <= kV * 896) return backward_vec_launch<T, kP32, kV, 896, false>(a, nvec, streams, sms, status, parts, stream);
+    return backward_vec_launch<T, kP32, 2 * kV, 512, false>(a, nvec, streams, sms, status, parts, stream);
 }
 
 // One launch for dx and dgamma: see rms_backward_few_kernel.

@@ -176,7 +176,7 @@ def test_many_rows(rows, hidden, t):
 
 
 @pytest.mark.parametrize("rows,hidden", [(32, 32), (1, 64), (5, 4096), (64, 96), (160, 7168), (2048, 544), (3, 32768), (96, 16384),
-                                         (416, 8224), (33, 160), (1184, 1024)])
+                                         (416, 8224), (33, 160), (1184, 1024), (64, 32768), (32, 25600), (160, 25632)])
 @pytest.mark.parametrize("tp", ["bf16", "fp32"])
 def test_quantised(rows, hidden, tp):
     x, res, _, _, ga = make(rows, hidden, "bf16", tp, rows + hidden, pad=8)
