@@ -863,7 +863,9 @@ def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, stats: bool = True, stre
         assert _like(residual, shape, dtype, device)
         if "z" not in o:
             o["z"] = torch.empty_like(x, memory_format=torch.contiguous_format)
-        res, ld_res, z, ld_z = residual.data_ptr(), _pitch(residual), o["z"].data_ptr(), _pitch(o["z"])
+        v = o["z"]
+        res, ld_res = residual.data_ptr(), hidden if residual.is_contiguous() else _pitch(residual)
+        z, ld_z = v.data_ptr(), hidden if v.is_contiguous() else _pitch(v)
     else:
         assert "z" not in o                                    # (it would be left unwritten)
     if stats and "rsigma" not in o:
@@ -871,8 +873,9 @@ def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, stats: bool = True, stre
     if "rsigma" in o:
         rs = o["rsigma"].data_ptr()
     y = o["y"]
-    _check(lib().te_mx_rmsnorm(x.data_ptr(), rows, hidden, _pitch(x), _dtype_code[dtype], res, ld_res, gamma.data_ptr(),
-                               _dtype_code[gamma.dtype], eps, z, ld_z, y.data_ptr(), _pitch(y), rs, _raw_stream()))
+    _check(lib().te_mx_rmsnorm(x.data_ptr(), rows, hidden, hidden if x.is_contiguous() else _pitch(x), _dtype_code[dtype],
+                               res, ld_res, gamma.data_ptr(), _dtype_code[gamma.dtype], eps, z, ld_z, y.data_ptr(),
+                               hidden if y.is_contiguous() else _pitch(y), rs, _raw_stream()))
     return o
 
 
@@ -922,16 +925,19 @@ def rmsnorm_quantize(x, gamma, eps: float = 1e-5, residual=None, rowwise: bool =
         assert _like(residual, shape, bf16, device)
         if "z" not in o:
             o["z"] = torch.empty_like(x, memory_format=torch.contiguous_format)
-        res, ld_res, z, ld_z = residual.data_ptr(), _pitch(residual), o["z"].data_ptr(), _pitch(o["z"])
+        v = o["z"]
+        res, ld_res = residual.data_ptr(), hidden if residual.is_contiguous() else _pitch(residual)
+        z, ld_z = v.data_ptr(), hidden if v.is_contiguous() else _pitch(v)
     else:
         assert "z" not in o                                    # (it would be left unwritten)
     if "y" in o:
-        y, ld_y = o["y"].data_ptr(), _pitch(o["y"])
+        v = o["y"]
+        y, ld_y = v.data_ptr(), hidden if v.is_contiguous() else _pitch(v)
     if "q_row" in o:
         q_row, s_row, ld_row = o["q_row"].data_ptr(), o["s_row"].data_ptr(), _pitch(o["s_row"])
     if "q_col" in o:
         q_col, s_col, ld_col = o["q_col"].data_ptr(), o["s_col"].data_ptr(), _pitch(o["s_col"])
-    _check(lib().te_mx_rmsnorm_quantize(x.data_ptr(), rows, hidden, _pitch(x), res, ld_res, gamma.data_ptr(),
+    _check(lib().te_mx_rmsnorm_quantize(x.data_ptr(), rows, hidden, hidden if x.is_contiguous() else _pitch(x), res, ld_res, gamma.data_ptr(),
                                         _dtype_code[gamma.dtype], eps, z, ld_z, y, ld_y, q_row, s_row, ld_row, q_col,
                                         s_col, ld_col, o["rsigma"].data_ptr(), _raw_stream()))
     return o
@@ -972,10 +978,12 @@ def rmsnorm_backward(dy, z, gamma, rsigma, dz=None, dparams: bool = True, stream
         ws, size = workspace.data_ptr(), workspace.numel()
     dx, res, ld_res = o["dx"], 0, 0
     if dz is not None:
-        res, ld_res = dz.data_ptr(), _pitch(dz)
-    _check(lib().te_mx_rmsnorm_backward(dy.data_ptr(), _pitch(dy), z.data_ptr(), _pitch(z), rows, hidden, _dtype_code[dtype],
+        res, ld_res = dz.data_ptr(), hidden if dz.is_contiguous() else _pitch(dz)
+    _check(lib().te_mx_rmsnorm_backward(dy.data_ptr(), hidden if dy.is_contiguous() else _pitch(dy), z.data_ptr(),
+                                        hidden if z.is_contiguous() else _pitch(z), rows, hidden, _dtype_code[dtype],
                                         gamma.data_ptr(), _dtype_code[gamma.dtype], rsigma.data_ptr(), res, ld_res,
-                                        dx.data_ptr(), _pitch(dx), dga, ws, size, _raw_stream()))
+                                        dx.data_ptr(), hidden if dx.is_contiguous() else _pitch(dx), dga, ws, size,
+                                        _raw_stream()))
     return o
 
 
@@ -1001,7 +1009,8 @@ def route(logits, k: int, scoring: str = "softmax", renormalise: bool = True, sc
         o["index"] = torch.empty((tokens, k), dtype=torch.int32, device=logits.device)
     if "weight" not in o:
         o["weight"] = torch.empty((tokens, k), dtype=torch.float32, device=logits.device)
-    _check(lib().te_mx_route(logits.data_ptr(), tokens, experts, _pitch(logits), _dtype_code[logits.dtype],
+    ld = experts if logits.is_contiguous() else _pitch(logits)
+    _check(lib().te_mx_route(logits.data_ptr(), tokens, experts, ld, _dtype_code[logits.dtype],
                              0 if bias is None else bias.data_ptr(), k, SCORINGS[scoring], int(bool(renormalise)), scale,
                              o["index"].data_ptr(), o["weight"].data_ptr(), _raw_stream()))
     return o
@@ -1023,9 +1032,10 @@ def route_backward(dweight, logits, index, scoring: str = "softmax", renormalise
     assert _matrix(index, tokens, k, torch.int32, device) and _matrix(dweight, tokens, k, torch.float32, device)
     assert _like(out, logits.shape, logits.dtype, device)
     d = torch.empty_like(logits, memory_format=torch.contiguous_format) if out is None else out
-    _check(lib().te_mx_route_backward(dweight.data_ptr(), logits.data_ptr(), _pitch(logits), index.data_ptr(), tokens,
-                                      experts, _dtype_code[logits.dtype], k, SCORINGS[scoring], int(bool(renormalise)),
-                                      scale, d.data_ptr(), _pitch(d), _raw_stream()))
+    ld = experts if logits.is_contiguous() else _pitch(logits)
+    _check(lib().te_mx_route_backward(dweight.data_ptr(), logits.data_ptr(), ld, index.data_ptr(), tokens, experts,
+                                      _dtype_code[logits.dtype], k, SCORINGS[scoring], int(bool(renormalise)), scale,
+                                      d.data_ptr(), experts if d.is_contiguous() else _pitch(d), _raw_stream()))
     return d
 
 
@@ -1086,8 +1096,9 @@ def moe_dispatch(x, row, scales=None, total_rows=None, stream=None, out=None):
         assert _bytes(ds, m, width, device)
     if scales is not None:
         s, ld_s, d_s, ld_ds = scales.data_ptr(), _pitch(scales), ds.data_ptr(), _pitch(ds)
-    _check(lib().te_mx_moe_dispatch(x.data_ptr(), _pitch(x) * size, hidden * size, s, ld_s, width, row.data_ptr(), tokens, k,
-                                    m, d.data_ptr(), _pitch(d) * size, d_s, ld_ds, _raw_stream()))
+    ld_x, ld_d = hidden if x.is_contiguous() else _pitch(x), hidden if d.is_contiguous() else _pitch(d)
+    _check(lib().te_mx_moe_dispatch(x.data_ptr(), ld_x * size, hidden * size, s, ld_s, width, row.data_ptr(), tokens, k, m,
+                                    d.data_ptr(), ld_d * size, d_s, ld_ds, _raw_stream()))
     return d if scales is None else (d, ds)
 
 
@@ -1107,9 +1118,14 @@ def moe_combine(y, row, weight=None, residual=None, stream=None, out=None):
     assert _matrix(row, tokens, k, torch.int32, device) and _matrix(weight, tokens, k, torch.float32, device)
     assert _like(residual, (tokens, hidden), y.dtype, device) and _like(out, (tokens, hidden), y.dtype, device)
     d = torch.empty((tokens, hidden), dtype=y.dtype, device=y.device) if out is None else out
-    _check(lib().te_mx_moe_combine(y.data_ptr(), _pitch(y), rows, hidden, _dtype_code[y.dtype], row.data_ptr(), tokens, k,
-                                   0 if weight is None else weight.data_ptr(), 0 if residual is None else residual.data_ptr(),
-                                   0 if residual is None else _pitch(residual), d.data_ptr(), _pitch(d), _raw_stream()))
+    w = res = ld_res = 0
+    if weight is not None:
+        w = weight.data_ptr()
+    if residual is not None:
+        res, ld_res = residual.data_ptr(), hidden if residual.is_contiguous() else _pitch(residual)
+    _check(lib().te_mx_moe_combine(y.data_ptr(), hidden if y.is_contiguous() else _pitch(y), rows, hidden, _dtype_code[y.dtype],
+                                   row.data_ptr(), tokens, k, w, res, ld_res, d.data_ptr(),
+                                   hidden if d.is_contiguous() else _pitch(d), _raw_stream()))
     return d
 
 
@@ -1136,7 +1152,9 @@ def moe_combine_backward(dout, y, row, weight, dweight: bool = True, stream=None
     if dweight and "dweight" not in o:
         o["dweight"] = torch.empty_like(weight)
     dy = o["dy"]
-    _check(lib().te_mx_moe_combine_backward(dout.data_ptr(), _pitch(dout), y.data_ptr(), _pitch(y), rows, hidden,
-                                            _dtype_code[y.dtype], row.data_ptr(), weight.data_ptr(), tokens, k,
-                                            dy.data_ptr(), _pitch(dy), _ptr(o.get("dweight")), _raw_stream()))
+    _check(lib().te_mx_moe_combine_backward(dout.data_ptr(), hidden if dout.is_contiguous() else _pitch(dout), y.data_ptr(),
+                                            hidden if y.is_contiguous() else _pitch(y), rows, hidden, _dtype_code[y.dtype],
+                                            row.data_ptr(), weight.data_ptr(), tokens, k, dy.data_ptr(),
+                                            hidden if dy.is_contiguous() else _pitch(dy), _ptr(o.get("dweight")),
+                                            _raw_stream()))
     return o

@@ -90,8 +90,8 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             const int i = t + v * tx;
-            x[v] = i < nvec ? px[i] : make_uint4(0, 0, 0, 0);
-            if (a.residual) r[v] = i < nvec ? pr[i] : make_uint4(0, 0, 0, 0);
+            x[v] = i < nvec ? __ldcs(px + i) : make_uint4(0, 0, 0, 0);
+            if (a.residual) r[v] = i < nvec ? __ldcs(pr + i) : make_uint4(0, 0, 0, 0);
         }
     };
     if (first < a.rows) load(first);
@@ -260,48 +260,63 @@ rms_forward_long_kernel(const RmsArgs a) {
 // The column-wise MXFP8 copy of y = z rs gamma (z and rs from the kernel above; its
 // programmatic dependent).  A warp takes 32 rows x 64 columns, a lane two columns,
 // whose blocks are then its own; four warps stack 128 rows, so that a column's codes
-// leave as up to 128 contiguous bytes through shared memory.
+// leave as up to 128 contiguous bytes through shared memory.  A block's largest |y| is
+// fl(max fl(z rs) gamma): rounding keeps the order, so gamma enters after the maximum.
+// Blocks go from the last rows to the first: what the kernel above wrote last is still
+// in L2 (it reads x and the residual as data that is not read again).
 constexpr int kColWarps = 4;
 template <bool kP32>
-__global__ void __launch_bounds__(kColWarps * 32)
+__global__ void __launch_bounds__(kColWarps * 32, 4)
 rms_colwise_kernel(const RmsArgs a, unsigned col_units) {
     __shared__ __align__(16) uint8_t codes[64][kColWarps * 32 + 16];     // (rows 16 bytes longer: fewer bank conflicts)
+    __shared__ __align__(16) float2 rs[kColWarps * 32];    // twice each: a pair
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t c0 = int64_t(blockIdx.x % col_units) * 64, r00 = int64_t(blockIdx.x / col_units) * (kColWarps * 32);
+    const unsigned block = gridDim.x - 1 - blockIdx.x;
+    const int64_t c0 = int64_t(block % col_units) * 64, r00 = int64_t(block / col_units) * (kColWarps * 32);
     const int64_t r0 = r00 + warp * 32, c = c0 + 2 * lane;
     if (r0 < a.rows) {                                     // (rows and hidden are multiples of 32)
+        const float mine = a.rsigma[r0 + lane];
+        rs[threadIdx.x] = make_float2(mine, mine);
+        __syncwarp();
         const bool live = c < a.hidden;
-        const uint16_t* z = static_cast<const uint16_t*>(a.residual ? a.z : a.x) + c;
         const int64_t ld = a.residual ? a.ld_z : a.ld_x;
+        const uint16_t* z = static_cast<const uint16_t*>(a.residual ? a.z : a.x) + r0 * ld + (live ? c : 0);
         uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = live ? *reinterpret_cast<const uint32_t*>(z + (r0 + i) * ld) : 0u;
+        for (int i = 0; i < 32; ++i) w[i] = __ldcs(reinterpret_cast<const uint32_t*>(z + i * ld));
         using P = typename std::conditional<kP32, float, __nv_bfloat16>::type;
         const uint64_t g = live ? f32x2::pack(load_param<P>(a.gamma, c), load_param<P>(a.gamma, c + 1)) : 0;
-        const float rs_lane = a.rsigma[r0 + lane];
+        const uint32_t rs_at = smem_u32(rs + warp * 32);
         float lo = 0.0f, hi = 0.0f;
-        uint64_t y[32];
+        uint64_t y[32];                                    // z rs
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const uint64_t rs = f32x2::both(__shfl_sync(0xFFFFFFFFu, rs_lane, i));
-            y[i] = f32x2::mul(f32x2::mul(f32x2::pack(bf16_lo(w[i]), bf16_hi(w[i])), rs), g);
-            lo = maxabs(lo, f32x2::lo(y[i]));
-            hi = maxabs(hi, f32x2::hi(y[i]));
+        for (int i = 0; i < 32; i += 2) {
+            uint64_t rs_a, rs_b;
+            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(rs_a), "=l"(rs_b) : "r"(rs_at + 8u * i));
+            y[i] = f32x2::mul(f32x2::pack(bf16_lo(w[i]), bf16_hi(w[i])), rs_a);
+            y[i + 1] = f32x2::mul(f32x2::pack(bf16_lo(w[i + 1]), bf16_hi(w[i + 1])), rs_b);
+            lo = maxabs(lo, maxabs(f32x2::lo(y[i]), f32x2::lo(y[i + 1])));
+            hi = maxabs(hi, maxabs(f32x2::hi(y[i]), f32x2::hi(y[i + 1])));
         }
-        const uint32_t s_lo = mx_scale_byte(lo), s_hi = mx_scale_byte(hi);
+        const uint32_t s_lo = mx_scale_byte(lo * f32x2::lo(g)), s_hi = mx_scale_byte(hi * f32x2::hi(g));
         const uint64_t inv = f32x2::pack(inv_scale(s_lo), inv_scale(s_hi));
         uint32_t q_lo[8], q_hi[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint64_t p[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = f32x2::mul(y[4 * i + k], inv);
+            for (int k = 0; k < 4; ++k) p[k] = f32x2::mul(f32x2::mul(y[4 * i + k], g), inv);
             q_lo[i] = cvt_e4m3x2(f32x2::lo(p[0]), f32x2::lo(p[1])) | (cvt_e4m3x2(f32x2::lo(p[2]), f32x2::lo(p[3])) << 16);
             q_hi[i] = cvt_e4m3x2(f32x2::hi(p[0]), f32x2::hi(p[1])) | (cvt_e4m3x2(f32x2::hi(p[2]), f32x2::hi(p[3])) << 16);
-            if (s_lo == 0xFFu) q_lo[i] = 0x7F7F7F7Fu;
-            if (s_hi == 0xFFu) q_hi[i] = 0x7F7F7F7Fu;
+        }
+        if (__any_sync(0xFFFFFFFFu, s_lo == 0xFFu || s_hi == 0xFFu)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (s_lo == 0xFFu) q_lo[i] = 0x7F7F7F7Fu;
+                if (s_hi == 0xFFu) q_hi[i] = 0x7F7F7F7Fu;
+            }
         }
         uint4* to_lo = reinterpret_cast<uint4*>(&codes[2 * lane][warp * 32]);
         uint4* to_hi = reinterpret_cast<uint4*>(&codes[2 * lane + 1][warp * 32]);
