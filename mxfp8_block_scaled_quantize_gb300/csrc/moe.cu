@@ -4,7 +4,7 @@
 // combine without weights.)  Slot s = token * k + j is a token's j-th choice.
 #include <cuda_runtime.h>
 
-#include <cfloat>
+#include <mutex>
 
 #include "f32x2.cuh"
 #include "ptx.cuh"
@@ -208,16 +208,23 @@ route_backward_kernel(const RouteArgs a) {
 // ---------------------------------------------------------------- slots sorted by expert
 
 // A stable counting sort in one launch: a cluster of blocks, each with a contiguous
-// part of the slots, each warp with a contiguous part of its block's.  Every warp
-// counts its slots by expert (in shared memory of its own, so no atomic's order
-// matters); the counts are summed over the warps and, through distributed shared
-// memory, over the blocks; then every warp goes through its slots again, 32 at a time,
-// and gives each slot its expert's next row: the slots of one expert in a group of 32
-// find each other with a match, and their order among themselves is the lanes'.
+// part of the slots, each warp with a contiguous part of its block's.  A warp goes
+// through its slots 32 at a time: the slots of one expert find each other with a ballot
+// for each bit of its index, and each takes the warp's count of that expert (in shared
+// memory of the warp's own, so no atomic's order matters) and its place among them as
+// its rank.  The counts are then summed over the warps and, through distributed shared
+// memory, over the blocks, and a slot's row is its rank behind what comes before its
+// warp.  The inverse leaves through shared memory, where the block's slots are sorted,
+// so that an expert's slots are written side by side (scattered one by one from 8 SMs
+// 131072 slots took 2 us more).  A warp holds its slots in registers,
+// 16 groups of 32; more slots than all warps hold are sorted in rounds, after a pass
+// that counts the experts' slots in all of them.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 8;
+constexpr int kSortCluster = 16;                 // blocks at most (8 without the wide clusters)
 constexpr int kMaxExperts = 1024;
+constexpr int kSortHeld = 16;                    // groups of 32 slots in a warp's registers
+constexpr int kSortBlockSlots = kSortThreads * kSortHeld;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -235,91 +242,174 @@ __device__ __forceinline__ int32_t remote_load(const int32_t* p, uint32_t rank) 
     return v;
 }
 
+// Inclusive sum over the block's threads; `sums`: a slot for each warp.
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums, int warp, int lane) {
+    auto warp_scan = [&](int32_t x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    v = warp_scan(v);
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    const int32_t w = warp_scan(sums[lane]);               // (kSortWarps = 32)
+    const int32_t before = __shfl_sync(0xFFFFFFFFu, w, warp == 0 ? 0 : warp - 1);
+    return warp == 0 ? v : v + before;
+}
+
+template <int kBits>                             // of an expert's index
 __global__ void __launch_bounds__(kSortThreads, 1)
 moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t experts, int blocks, int32_t* __restrict__ group_m,
                 int32_t* __restrict__ row, int32_t* __restrict__ slot, unsigned int* status) {
-    extern __shared__ int32_t counts[];                    // [kSortWarps][experts]: counts, then next rows
-    __shared__ int32_t total[kMaxExperts];                 // of this block's slots (read by the other blocks)
-    __shared__ int32_t warp_total[kSortWarps];
+    extern __shared__ int32_t shared[];
+    uint32_t* sorted = reinterpret_cast<uint32_t*>(shared);            // [kSortBlockSlots]: expert << 16 | slot
+    int32_t* counts = shared + kSortBlockSlots;            // [kSortWarps][experts]: counts, then first places
+    __shared__ int32_t total[2][kMaxExperts];              // of this block's slots (read by the other blocks)
+    __shared__ int32_t to_row[kMaxExperts];                // from a place in `sorted` to a row
+    __shared__ int32_t sums[2][kSortWarps];
+    __shared__ int32_t here_kept, all_kept;
     grid_dependency_wait();
     grid_launch_dependents();
     const int t = int(threadIdx.x), lane = t & 31, warp = t >> 5;
     const uint32_t rank = blocks > 1 ? cluster_rank() : 0u;
-    // this warp's slots: whole groups of 32
-    const int64_t groups = (slots + 31) / 32, parts = int64_t(blocks) * kSortWarps;
-    const int64_t part = int64_t(rank) * kSortWarps + warp;
-    const int64_t s0 = 32 * (groups * part / parts), s1 = 32 * (groups * (part + 1) / parts);
-    for (int i = t; i < kSortWarps * experts; i += kSortThreads) counts[i] = 0;
-    __syncthreads();
-    int32_t* mine = counts + warp * experts;
-    for (int64_t s = s0 + lane; s < s1; s += 32) {
-        const int32_t e = s < slots ? index[s] : -1;
-        if (e >= experts) set_device_status(status, kStatusBadArg);
-        else if (e >= 0) atomicAdd(&mine[e], 1);
-    }
-    __syncthreads();
-    // over the warps: counts become the sums of the warps before
-    int32_t here = 0;
-    if (t < experts) {
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int32_t c = counts[w * experts + t];
-            counts[w * experts + t] = here;
-            here += c;
-        }
-        total[t] = here;
-    }
-    if (blocks > 1) cluster_sync_all();
-    else __syncthreads();
-    // over the blocks: this expert's slots in the blocks before, and in all
-    int32_t before = 0, all = here;
-    if (blocks > 1 && t < experts) {
-        all = 0;
-        for (int b = 0; b < blocks; ++b) {
-            const int32_t c = remote_load(&total[t], uint32_t(b));
-            if (b < int(rank)) before += c;
-            all += c;
-        }
-    }
-    // over the experts: an inclusive scan of `all`
-    int32_t upto = t < experts ? all : 0;
+    const int64_t per_round = int64_t(blocks) * kSortBlockSlots, rounds = slots > per_round ? (slots + per_round - 1) / per_round : 1;
+    auto sync_blocks = [&] {
+        if (blocks > 1) cluster_sync_all();
+        else __syncthreads();
+    };
+    // expert t's slots in the blocks before this one, and in all
+    auto across_blocks = [&](const int32_t* of_block, int32_t& before) {
+        int32_t v[kSortCluster], all = 0;
+        before = 0;
+        if (t >= experts) return all;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) warp_total[warp] = upto;
-    __syncthreads();
-    int32_t of_warps = lane < kSortWarps ? warp_total[lane] : 0;
+        for (int b = 0; b < kSortCluster; ++b) v[b] = b >= blocks ? 0 : blocks == 1 ? of_block[t] : remote_load(&of_block[t], uint32_t(b));
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, of_warps, o);
-        if (lane >= o) of_warps += v;
+        for (int b = 0; b < kSortCluster; ++b) {
+            if (b < int(rank)) before += v[b];
+            all += v[b];
+        }
+        return all;
+    };
+    int32_t all = 0, start = 0, done = 0;                  // expert t's slots, its first row, its slots in earlier rounds
+    if (rounds > 1) {
+        total[1][t] = 0;
+        __syncthreads();
+        for (int64_t s = int64_t(rank) * kSortThreads + t; s < slots; s += int64_t(blocks) * kSortThreads) {
+            const int32_t e = index[s];
+            if (e >= 0 && e < experts) atomicAdd(&total[1][e], 1);
+        }
+        sync_blocks();
+        int32_t before;
+        all = across_blocks(total[1], before);
+        const int32_t upto = block_scan(all, sums[0], warp, lane);
+        start = upto - all;
+        if (t == kSortThreads - 1) all_kept = upto;
     }
-    const int32_t kept = __shfl_sync(0xFFFFFFFFu, of_warps, 31);
-    upto += warp > 0 ? __shfl_sync(0xFFFFFFFFu, of_warps, warp - 1) : 0;
-    if (t < experts) {
-        const int32_t base = upto - all + before;
-        for (int w = 0; w < kSortWarps; ++w) counts[w * experts + t] += base;
-        if (rank == 0) group_m[t] = all;
-    }
-    __syncthreads();
-    for (int64_t s = s0 + lane; s < s1; s += 32) {         // (s1 - s0 is a multiple of 32: whole warps)
-        const int32_t e = s < slots ? index[s] : -1;
-        const bool live = e >= 0 && e < experts;
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, live ? e : -1);
-        int32_t r = -1;
-        if (live) r = mine[e] + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (live && lane == 31 - __clz(peers)) mine[e] = r + 1;
-        __syncwarp();
-        if (s < slots) {
-            row[s] = r;
-            if (live) slot[r] = int32_t(s);
+    for (int64_t round = 0; round < rounds; ++round) {
+        // this block's slots of the round, and this warp's, whole groups of 32
+        const int64_t first = round * per_round;
+        const int in_round = int(slots - first < per_round ? slots - first : per_round);
+        const int groups = (in_round + 31) / 32, parts = blocks * kSortWarps, part = int(rank) * kSortWarps + warp;
+        const int g0 = groups * part / parts, n = groups * (part + 1) / parts - g0;    // (at most 4096 x 256; at most kSortHeld)
+        const int of_block = 32 * (groups * (int(rank) * kSortWarps) / parts), s0 = 32 * g0 + lane;
+        const int32_t* from = index + first + s0;
+        int32_t of[kSortHeld];                             // expert << 16 | rank; -1: none
+#pragma unroll
+        for (int i = 0; i < kSortHeld; ++i) of[i] = i < n && s0 + 32 * i < in_round ? from[32 * i] : -1;
+        for (int i = t; i < kSortWarps * experts; i += kSortThreads) counts[i] = 0;
+        __syncthreads();
+        int32_t* mine = counts + warp * experts;
+#pragma unroll
+        for (int i = 0; i < kSortHeld; ++i) {
+            if (i < n) {
+                int32_t e = of[i];
+                if (e >= experts) {
+                    set_device_status(status, kStatusBadArg);
+                    e = -1;
+                }
+                uint32_t peers = __ballot_sync(0xFFFFFFFFu, e >= 0);   // the slots of the same expert
+#pragma unroll
+                for (int b = 0; b < kBits; ++b) {
+                    const bool one = e & (1 << b);
+                    const uint32_t set = __ballot_sync(0xFFFFFFFFu, one);
+                    peers &= one ? set : ~set;
+                }
+                int32_t r = 0;
+                if (e >= 0) r = mine[e] + __popc(peers & ((1u << lane) - 1u));
+                __syncwarp();
+                if (e >= 0 && lane == 31 - __clz(peers)) mine[e] = r + 1;
+                __syncwarp();
+                of[i] = e < 0 ? -1 : e << 16 | r;          // (r < 512)
+            }
+        }
+        __syncthreads();
+        // over the warps
+        int32_t here = 0;
+        if (t < experts) {
+            for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+                int32_t c[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) c[w] = counts[(w0 + w) * experts + t];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) here += c[w];
+            }
+        }
+        total[round & 1][t] = here;
+        // over the blocks, and over the experts
+        sync_blocks();
+        int32_t before;
+        const int32_t of_round = across_blocks(total[round & 1], before);
+        if (rounds == 1) {
+            all = of_round;
+            const int32_t upto = block_scan(all, sums[0], warp, lane);
+            start = upto - all;
+            if (t == kSortThreads - 1) all_kept = upto;
+        }
+        const int32_t place_upto = block_scan(here, sums[1], warp, lane);
+        if (t == kSortThreads - 1) here_kept = place_upto;
+        if (t < experts) {
+            int32_t p = place_upto - here;                 // the expert's first place in `sorted`
+            to_row[t] = start + done + before - p;
+            for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+                int32_t c[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) c[w] = counts[(w0 + w) * experts + t];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    counts[(w0 + w) * experts + t] = p;
+                    p += c[w];
+                }
+            }
+            done += of_round;
+        }
+        __syncthreads();
+        int32_t* to = row + first + s0;
+#pragma unroll
+        for (int i = 0; i < kSortHeld; ++i) {
+            if (i < n && s0 + 32 * i < in_round) {
+                int32_t r = -1;
+                if (of[i] >= 0) {
+                    const int32_t e = of[i] >> 16, p = (of[i] & 0xFFFF) + mine[e];
+                    sorted[p] = uint32_t(e) << 16 | uint32_t(s0 + 32 * i - of_block);
+                    r = p + to_row[e];
+                }
+                to[32 * i] = r;
+            }
+        }
+        __syncthreads();
+        const int32_t base = int32_t(first) + of_block;
+        for (int p = t; p < here_kept; p += kSortThreads) {
+            const uint32_t v = sorted[p];
+            slot[p + to_row[v >> 16]] = base + int32_t(v & 0xFFFFu);
         }
     }
+    if (rank == 0 && t < experts) group_m[t] = all;
     // rows without a slot
-    for (int64_t r = kept + int64_t(rank) * kSortThreads + t; r < slots; r += int64_t(blocks) * kSortThreads) slot[r] = -1;
+    for (int64_t r = all_kept + int64_t(rank) * kSortThreads + t; r < slots; r += int64_t(blocks) * kSortThreads) slot[r] = -1;
     if (blocks > 1) cluster_sync_all();                    // no block leaves while another may still read its counts
 }
 
@@ -372,7 +462,7 @@ moe_dispatch_kernel(const DispatchArgs a, int parts, unsigned int* status) {
 // out[t] = sum_j weight[t][j] y[row[t][j]] + residual[t], in fp32, the choices in
 // order, rounded once.  kVec: rows on 16-byte boundaries, a 16-byte vector per thread
 // and step; else an element.
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 128;
 constexpr int kMaxChoices = 32;
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kCombineThreads)
@@ -566,29 +656,61 @@ te_mx_status combine_any(const CombineArgs& a, bool backward, cudaStream_t strea
 te_mx_status route_launch(const RouteArgs& a, cudaStream_t stream) { return route_any(a, false, stream); }
 te_mx_status route_backward_launch(const RouteArgs& a, cudaStream_t stream) { return route_any(a, true, stream); }
 
+// Blocks of the sort: one up to where a cluster is faster (2048 slots: 6.3 us, 8 blocks
+// 6.4; 8192: 12, 6.7), eight, and sixteen, if the device takes such clusters, from where
+// those are faster (16384: 7.2, 7.4; 32768: 8.7, 8.0; 131072: 15.8, 11.3).
+constexpr int64_t kSortAlone = 2048, kSortEight = 16384;
+
+// Whether the device launches the kernel in clusters of 16 blocks; looked up once per
+// kernel and device, and the attribute for it set then.
+static bool wide_clusters(const void* kern, int which, const cudaLaunchConfig_t& cfg) {
+    static std::mutex mu;
+    static int8_t known[5][64];                            // 0: not looked up, 1: yes, -1: no
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    int8_t& k = known[which][dev];
+    if (k == 0) {
+        int n = 0;
+        const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+        if (!ok) (void)cudaGetLastError();
+        k = ok ? 1 : -1;
+    }
+    return k > 0;
+}
+
 te_mx_status moe_sort_launch(const int32_t* index, int64_t slots, int32_t experts, int32_t* group_m, int32_t* row,
                              int32_t* slot, cudaStream_t stream) {
     unsigned int* status = nullptr;
     te_mx_status st = device_status_ptr(&status);
     if (st != TE_MX_OK) return st;
-    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(moe_sort_kernel), kSortWarps * kMaxExperts * 4);
+    const int which = experts <= 32 ? 0 : experts <= 64 ? 1 : experts <= 128 ? 2 : experts <= 256 ? 3 : 4;
+    auto kern = which == 0 ? moe_sort_kernel<5> : which == 1 ? moe_sort_kernel<6> : which == 2 ? moe_sort_kernel<7>
+                : which == 3 ? moe_sort_kernel<8> : moe_sort_kernel<10>;
+    cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), (kSortBlockSlots + kSortWarps * kMaxExperts) * 4);
     if (e != cudaSuccess) return cuda_status(e, "expert sort kernel attributes");
-    const int blocks = slots > 8 * kSortThreads ? kSortCluster : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = size_t(kSortWarps) * size_t(experts) * 4;
+    cfg.dynamicSmemBytes = size_t(kSortBlockSlots + kSortWarps * experts) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(blocks);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = blocks > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, moe_sort_kernel, index, slots, experts, blocks, group_m, row, slot, status);
+    int blocks = 1;
+    auto clusters_of = [&](int n) {
+        blocks = n;
+        cfg.gridDim = dim3(unsigned(n));
+        attr[1].val.clusterDim.x = unsigned(n);
+        cfg.numAttrs = n > 1 ? 2 : 1;
+    };
+    clusters_of(slots <= kSortAlone ? 1 : slots <= kSortEight ? 8 : kSortCluster);
+    if (blocks == kSortCluster && !wide_clusters(reinterpret_cast<const void*>(kern), which, cfg)) clusters_of(8);
+    e = cudaLaunchKernelEx(&cfg, kern, index, slots, experts, blocks, group_m, row, slot, status);
     return cuda_status(e, "expert sort kernel launch");
 }
 
