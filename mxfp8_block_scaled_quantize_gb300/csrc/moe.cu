@@ -416,10 +416,10 @@ moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t expert
 // ---------------------------------------------------------------- dispatch
 
 // Every token's row is read once and written to the rows of its slots.  A block takes
-// a token's part of kCopyThreads pieces of kBytes bytes; the scales of MXFP8 rows go
+// a token's part of kCopyThreads * kCopyPieces pieces of kBytes bytes; the scales of MXFP8 rows go
 // byte by byte with the first part.
 constexpr int kCopyThreads = 128;
-constexpr int kCopyPieces = 4;                   // per thread
+template <int kBytes> constexpr int kCopyPieces = kBytes == 16 ? 4 : 8;      // per thread
 template <int kBytes> struct PieceOf;
 template <> struct PieceOf<16> { using Type = uint4; };
 template <> struct PieceOf<4> { using Type = uint32_t; };
@@ -434,11 +434,11 @@ moe_dispatch_kernel(const DispatchArgs a, int parts, unsigned int* status) {
     grid_launch_dependents();
     const int64_t token = int64_t(blockIdx.x) / parts;
     const int part = int(int64_t(blockIdx.x) % parts);
-    const int64_t pieces = a.row_bytes / kBytes, p0 = int64_t(part) * kCopyThreads * kCopyPieces + threadIdx.x;
+    const int64_t pieces = a.row_bytes / kBytes, p0 = int64_t(part) * kCopyThreads * kCopyPieces<kBytes> + threadIdx.x;
     const Piece* x = reinterpret_cast<const Piece*>(a.x + token * a.ld_x);
-    Piece v[kCopyPieces];
+    Piece v[kCopyPieces<kBytes>];
 #pragma unroll
-    for (int i = 0; i < kCopyPieces; ++i)
+    for (int i = 0; i < kCopyPieces<kBytes>; ++i)
         if (p0 + i * kCopyThreads < pieces) v[i] = x[p0 + i * kCopyThreads];
     for (int j = 0; j < a.k; ++j) {
         const int64_t r = a.row[token * a.k + j];
@@ -449,7 +449,7 @@ moe_dispatch_kernel(const DispatchArgs a, int parts, unsigned int* status) {
         }
         Piece* out = reinterpret_cast<Piece*>(a.out + r * a.ld_out);
 #pragma unroll
-        for (int i = 0; i < kCopyPieces; ++i)
+        for (int i = 0; i < kCopyPieces<kBytes>; ++i)
             if (p0 + i * kCopyThreads < pieces) out[p0 + i * kCopyThreads] = v[i];
         if (a.scales && part == 0)
             for (int64_t b = threadIdx.x; b < a.scale_bytes; b += kCopyThreads)
@@ -460,63 +460,90 @@ moe_dispatch_kernel(const DispatchArgs a, int parts, unsigned int* status) {
 // ---------------------------------------------------------------- combine
 
 // out[t] = sum_j weight[t][j] y[row[t][j]] + residual[t], in fp32, the choices in
-// order, rounded once.  kVec: rows on 16-byte boundaries, a 16-byte vector per thread
-// and step; else an element.
-constexpr int kCombineThreads = 128;
-constexpr int kMaxChoices = 32;
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kCombineThreads)
-moe_combine_kernel(const CombineArgs a, int parts, unsigned int* status) {
+// order, rounded once.  Persistent: a block's warps take parts of 32 kN pieces of a
+// token side by side, a piece a 16-byte vector (kVec: rows on 16-byte boundaries) or an element, from kJ rows at
+// a time; lane j holds the j-th row and weight, loaded a token ahead.  The loads in
+// flight are what it lives on, so few choices take more pieces (two of 2048 bf16, 4096
+// tokens: a block per token and part, one vector per thread, 20 us).
+constexpr int kCombineThreads = 256;             // at most
+template <typename T, bool kVec, int kN, int kJ>
+__global__ void __launch_bounds__(kCombineThreads, 3)
+moe_combine_kernel(const CombineArgs a, unsigned int* status) {
     using V = Vec<T>;
-    __shared__ int32_t row[kMaxChoices];
-    __shared__ float weight[kMaxChoices];
+    using Piece = typename std::conditional<kVec, uint4, T>::type;
+    constexpr int kPairs = kVec ? V::kPairs : 1;           // (an element: the low half)
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t token = int64_t(blockIdx.x) / parts;
-    const int64_t i = int64_t(int64_t(blockIdx.x) % parts) * kCombineThreads + threadIdx.x;
-    if (threadIdx.x < a.k) {
-        int32_t r = a.row[token * a.k + threadIdx.x];
-        if (r >= a.total_rows) {
+    const int lane = threadIdx.x & 31;
+    const int pieces = kVec ? int(a.hidden / V::kN) : int(a.hidden);
+    const int i0 = int(blockIdx.y * blockDim.x + threadIdx.x - lane) * kN + lane;
+    if (i0 - lane >= pieces) return;                       // (no part of the rows for this warp)
+    auto pair = [](const Piece& w, int q) {
+        if constexpr (kVec) return V::pair(w, q);
+        else return f32x2::pack(to_f32(w), 0.0f);
+    };
+    int32_t row = -1, row_next = -1;
+    float weight = 0.0f, weight_next = 0.0f;
+    auto load_side = [&](int64_t token) {
+        row_next = lane < a.k ? a.row[token * a.k + lane] : -1;
+        weight_next = lane < a.k && a.weight ? a.weight[token * a.k + lane] : 1.0f;
+    };
+    load_side(blockIdx.x);
+    for (int64_t token = blockIdx.x; token < a.tokens; token += gridDim.x) {
+        row = row_next;
+        weight = weight_next;
+        if (row >= a.total_rows) {
             set_device_status(status, kStatusBadArg);
-            r = -1;
+            row = -1;
         }
-        row[threadIdx.x] = r;
-        weight[threadIdx.x] = a.weight ? a.weight[token * a.k + threadIdx.x] : 1.0f;
-    }
-    __syncthreads();
-    const T* y = static_cast<const T*>(a.y);
-    const T* res = a.residual ? static_cast<const T*>(a.residual) + token * a.ld_residual : nullptr;
-    T* out = static_cast<T*>(a.out) + token * a.ld_out;
-    if constexpr (kVec) {
-        if (i >= a.hidden / V::kN) return;
-        uint64_t s[V::kPairs];
+        if (token + gridDim.x < a.tokens) load_side(token + gridDim.x);
+        const Piece* res = a.residual ? reinterpret_cast<const Piece*>(static_cast<const T*>(a.residual) + token * a.ld_residual) : nullptr;
+        Piece add[kN];
+        uint64_t s[kN][kPairs];
 #pragma unroll
-        for (int q = 0; q < V::kPairs; ++q) s[q] = 0;
-        for (int j0 = 0; j0 < a.k; j0 += 8) {              // eight rows in flight
-            uint4 w[8];
+        for (int n = 0; n < kN; ++n) {
+            if (res && i0 + 32 * n < pieces) add[n] = res[i0 + 32 * n];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j0 + j < a.k && row[j0 + j] >= 0) w[j] = reinterpret_cast<const uint4*>(y + row[j0 + j] * a.ld_y)[i];
+            for (int q = 0; q < kPairs; ++q) s[n][q] = 0;
+        }
+        for (int j0 = 0; j0 < a.k; j0 += kJ) {
+            Piece w[kJ][kN];
+            int32_t r[kJ];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j0 + j < a.k && row[j0 + j] >= 0) {
-                    const uint64_t f = f32x2::both(weight[j0 + j]);
+            for (int j = 0; j < kJ; ++j) {
+                r[j] = __shfl_sync(0xFFFFFFFFu, row, (j0 + j) & 31);
+                if (j0 + j >= a.k) r[j] = -1;
+                if (r[j] >= 0) {
+                    const Piece* y = reinterpret_cast<const Piece*>(static_cast<const T*>(a.y) + r[j] * a.ld_y) + i0;
 #pragma unroll
-                    for (int q = 0; q < V::kPairs; ++q) s[q] = f32x2::fma(V::pair(w[j], q), f, s[q]);
+                    for (int n = 0; n < kN; ++n)
+                        if (i0 + 32 * n < pieces) w[j][n] = y[32 * n];
                 }
-        }
-        if (res) {
-            const uint4 w = reinterpret_cast<const uint4*>(res)[i];
+            }
 #pragma unroll
-            for (int q = 0; q < V::kPairs; ++q) s[q] = f32x2::add(s[q], V::pair(w, q));
+            for (int j = 0; j < kJ; ++j) {
+                const uint64_t f = f32x2::both(__shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31));
+                if (r[j] >= 0) {
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+                        if (i0 + 32 * n < pieces) {
+#pragma unroll
+                            for (int q = 0; q < kPairs; ++q) s[n][q] = f32x2::fma(pair(w[j][n], q), f, s[n][q]);
+                        }
+                }
+            }
         }
-        reinterpret_cast<uint4*>(out)[i] = V::from_pairs(s);
-    } else {
-        if (i >= a.hidden) return;
-        float s = 0.0f;
-        for (int j = 0; j < a.k; ++j)
-            if (row[j] >= 0) s = fmaf(to_f32(y[row[j] * a.ld_y + i]), weight[j], s);
-        out[i] = from_f32<T>(res ? s + to_f32(res[i]) : s);
+        Piece* out = reinterpret_cast<Piece*>(static_cast<T*>(a.out) + token * a.ld_out) + i0;
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+            if (i0 + 32 * n < pieces) {
+                if (res) {
+#pragma unroll
+                    for (int q = 0; q < kPairs; ++q) s[n][q] = f32x2::add(s[n][q], pair(add[n], q));
+                }
+                if constexpr (kVec) out[32 * n] = V::from_pairs(s[n]);
+                else out[32 * n] = from_f32<T>(f32x2::lo(s[n][0]));
+            }
     }
 }
 
@@ -577,10 +604,22 @@ moe_combine_backward_kernel(const CombineArgs a, unsigned int* status) {
         }
         dot = f32x2::lo(sum) + f32x2::hi(sum);
     } else {
-        for (int64_t i = lane; i < a.hidden; i += 32) {
-            const float d = to_f32(dout[i]);
-            if (a.dweight) dot = fmaf(d, to_f32(y[i]), dot);
-            if (dy) dy[i] = from_f32<T>(d * w);
+        constexpr int kAhead = 8;                          // elements in flight
+        for (int64_t i0 = lane; i0 < a.hidden; i0 += 32 * kAhead) {
+            T d[kAhead], v[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const bool live = i0 + 32 * q < a.hidden;
+                d[q] = live ? dout[i0 + 32 * q] : from_f32<T>(0.0f);
+                if (a.dweight) v[q] = live ? y[i0 + 32 * q] : from_f32<T>(0.0f);
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                if (i0 + 32 * q >= a.hidden) break;
+                const float f = to_f32(d[q]);
+                if (a.dweight) dot = fmaf(f, to_f32(v[q]), dot);
+                if (dy) dy[i0 + 32 * q] = from_f32<T>(f * w);
+            }
         }
     }
     if (a.dweight) {
@@ -619,14 +658,23 @@ te_mx_status route_any(const RouteArgs& a, bool backward, cudaStream_t stream) {
 
 template <int kBytes>
 cudaError_t dispatch_launch(const DispatchArgs& a, unsigned int* status, cudaStream_t stream) {
-    const int64_t per = int64_t(kCopyThreads) * kCopyPieces, pieces = a.row_bytes / kBytes;
+    const int64_t per = int64_t(kCopyThreads) * kCopyPieces<kBytes>, pieces = a.row_bytes / kBytes;
     const int64_t parts = pieces > per ? (pieces + per - 1) / per : 1;
     return launch_dependent(moe_dispatch_kernel<kBytes>, dim3(unsigned(a.tokens * parts)), dim3(kCopyThreads), stream, a,
                             int(parts), status);
 }
 
+template <typename T, bool kVec, int kN, int kJ>
+cudaError_t combine_launch(const CombineArgs& a, int sms, unsigned int* status, cudaStream_t stream) {
+    const int64_t pieces = kVec ? a.hidden / Vec<T>::kN : a.hidden, parts = (pieces + 32 * kN - 1) / (32 * kN);
+    const int warps = int(parts < kCombineThreads / 32 ? parts : kCombineThreads / 32);
+    const int64_t rows_of_blocks = (parts + warps - 1) / warps, most = (int64_t(sms) * 24 / warps + rows_of_blocks - 1) / rows_of_blocks;
+    return launch_dependent(moe_combine_kernel<T, kVec, kN, kJ>, dim3(unsigned(a.tokens < most ? a.tokens : most), unsigned(rows_of_blocks)),
+                            dim3(unsigned(32 * warps)), stream, a, status);
+}
+
 template <typename T>
-cudaError_t combine(const CombineArgs& a, bool backward, unsigned int* status, cudaStream_t stream) {
+cudaError_t combine(const CombineArgs& a, bool backward, int sms, unsigned int* status, cudaStream_t stream) {
     auto fits = [&](const void* p, int64_t ld, int64_t rows) { return !p || rows_on16(p, ld, rows, sizeof(T)); };
     const bool vec = a.hidden % Vec<T>::kN == 0 && fits(a.y, a.ld_y, a.total_rows) && fits(a.residual, a.ld_residual, a.tokens) &&
                      fits(a.out, a.ld_out, a.tokens) && fits(a.dout, a.ld_dout, a.tokens) && fits(a.dy, a.ld_dy, a.total_rows);
@@ -635,19 +683,20 @@ cudaError_t combine(const CombineArgs& a, bool backward, unsigned int* status, c
         return vec ? launch_dependent(moe_combine_backward_kernel<T, true>, grid, block, stream, a, status)
                    : launch_dependent(moe_combine_backward_kernel<T, false>, grid, block, stream, a, status);
     }
-    const int64_t n = vec ? a.hidden / Vec<T>::kN : a.hidden, parts = (n + kCombineThreads - 1) / kCombineThreads;
-    const dim3 grid(unsigned(a.tokens * parts)), block(kCombineThreads);
-    return vec ? launch_dependent(moe_combine_kernel<T, true>, grid, block, stream, a, int(parts), status)
-               : launch_dependent(moe_combine_kernel<T, false>, grid, block, stream, a, int(parts), status);
+    if (!vec) return combine_launch<T, false, 8, 4>(a, sms, status, stream);
+    if (a.k <= 2) return combine_launch<T, true, 4, 2>(a, sms, status, stream);
+    if (a.k <= 4) return combine_launch<T, true, 2, 4>(a, sms, status, stream);
+    return combine_launch<T, true, 1, 8>(a, sms, status, stream);
 }
 
 te_mx_status combine_any(const CombineArgs& a, bool backward, cudaStream_t stream) {
     unsigned int* status = nullptr;
+    int sms = 0;
     te_mx_status st = device_status_ptr(&status);
-    if (st != TE_MX_OK) return st;
-    cudaError_t e = a.dtype == TE_MX_FP32   ? combine<float>(a, backward, status, stream)
-                    : a.dtype == TE_MX_FP16 ? combine<__half>(a, backward, status, stream)
-                                            : combine<__nv_bfloat16>(a, backward, status, stream);
+    if (st != TE_MX_OK || (st = device_sm_count(&sms)) != TE_MX_OK) return st;
+    cudaError_t e = a.dtype == TE_MX_FP32   ? combine<float>(a, backward, sms, status, stream)
+                    : a.dtype == TE_MX_FP16 ? combine<__half>(a, backward, sms, status, stream)
+                                            : combine<__nv_bfloat16>(a, backward, sms, status, stream);
     return cuda_status(e, "combine kernel launch");
 }
 
