@@ -24,7 +24,10 @@ namespace temx {
 
 namespace {
 
-constexpr int kThreads = 512;                    // of a block, at most, where a thread holds more than one vector
+// Threads of a block, at most, where a thread holds kV vectors (two: 72 registers each
+// for two blocks per SM).
+constexpr int kThreads = 512;
+template <int kV> constexpr int kMostThreads = kV == 1 ? 1024 : kV == 2 ? 448 : kThreads;
 
 // Sum over the block's warps of a value that each warp has summed (the same value
 // in each thread, in warp order).  `part`: a slot for each warp; one call between
@@ -62,47 +65,41 @@ __device__ __forceinline__ void unpack_again(uint4& w) { asm volatile("" : "+r"(
 
 // ---------------------------------------------------------------- forward
 
-// Rows on 16-byte boundaries; persistent.  blockDim.x threads hold a row, kV
-// vectors each, and the next row's words are in flight while this row's sum
-// crosses the block; blockDim.y rows per block where a warp holds a row (then no
-// warp waits for another).  The longest chain of a sum: 8 kV / 2 + 1 + 5 additions
-// in a warp, 5 over the warps.
+// Rows on 16-byte boundaries; persistent.  blockDim.x threads hold a row, kV vectors
+// each, and later rows' words are in flight while this row's sum crosses the block: the
+// next row's x and residual, or the next two rows' x where there is no residual (with
+// one row ahead, 28 KB in flight per SM, 8192 x 7168 bf16 took 41.3 us); blockDim.y rows
+// per block where a warp holds a row (then no warp waits for another).  The longest
+// chain of a sum: 8 kV / 2 + 1 + 5 additions in a warp, 5 over the warps.
 // kQuantise (T = bf16): four neighbouring lanes hold an MX block of 32 elements.
-template <typename T, bool kP32, int kV, bool kQuantise>
-__global__ void __launch_bounds__(kV == 1 ? 1024 : kThreads, kV == 2 ? 2 : 1)
+template <typename T, bool kP32, int kV, bool kQuantise, bool kResidual>
+__global__ void __launch_bounds__(kMostThreads<kV>, kV == 2 ? 2 : 1)
 rms_forward_vec_kernel(const RmsArgs a, int nvec) {
     using V = Vec<T>;
     __shared__ float part[2][32];                          // by parity of the row
     grid_dependency_wait();
     grid_launch_dependents();
     const int t = int(threadIdx.x), tx = int(blockDim.x), lane = t & 31, warp = t >> 5, warps = tx >> 5;
-    const int64_t first = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, step = int64_t(gridDim.x) * blockDim.y;
+    const int64_t step = int64_t(gridDim.x) * blockDim.y;
     constexpr bool kKeep = kV <= 2;                        // gamma in registers (of more vectors it comes from L1)
     ParamVec<T, kP32> g[kKeep ? kV : 1];
     if constexpr (kKeep) {
 #pragma unroll
         for (int v = 0; v < kV; ++v) g[v].load(a.gamma, t + v * tx < nvec ? t + v * tx : 0);
     }
-    uint4 x[kV], r[kV];
-    auto load = [&](int64_t row) {
-        const uint4* px = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + row * a.ld_x);
-        const uint4* pr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + row * a.ld_residual);
+    auto load = [&](uint4 (&w)[kV], const void* from, int64_t ld, int64_t row) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(from) + row * ld);
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            const int i = t + v * tx;
-            x[v] = i < nvec ? __ldcs(px + i) : make_uint4(0, 0, 0, 0);
-            if (a.residual) r[v] = i < nvec ? __ldcs(pr + i) : make_uint4(0, 0, 0, 0);
-        }
+        for (int v = 0; v < kV; ++v) w[v] = t + v * tx < nvec ? __ldcs(p + t + v * tx) : make_uint4(0, 0, 0, 0);
     };
-    if (first < a.rows) load(first);
-    int parity = 0;
-    for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
+    // the row of words x (and residual r), which then hold those of row `next`
+    auto one_row = [&](int64_t row, int64_t next, uint4 (&x)[kV], uint4 (&r)[kV], float* slots) {
         uint4 z[kV];
         uint64_t s = 0;
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             z[v] = x[v];
-            if (a.residual) {
+            if constexpr (kResidual) {
                 uint64_t o[V::kPairs];
 #pragma unroll
                 for (int k = 0; k < V::kPairs; ++k) o[k] = f32x2::add(V::pair(x[v], k), V::pair(r[v], k));
@@ -116,8 +113,11 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
                 s = f32x2::fma(p, p, s);
             }
         }
-        if (row + step < a.rows) load(row + step);
-        const float total = across_warps(warp_sum(f32x2::lo(s) + f32x2::hi(s)), part[parity], warps, warp, lane);
+        if (next < a.rows) {
+            load(x, a.x, a.ld_x, next);
+            if constexpr (kResidual) load(r, a.residual, a.ld_residual, next);
+        }
+        const float total = across_warps(warp_sum(f32x2::lo(s) + f32x2::hi(s)), slots, warps, warp, lane);
         const float rs = 1.0f / sqrtf(total / float(a.hidden) + a.eps);
         if (t == 0 && a.rsigma) a.rsigma[row] = rs;
         const uint64_t rs2 = f32x2::both(rs);
@@ -150,6 +150,19 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
                     if ((lane & 3) == 0) a.s_row[row * a.ld_s_row + (i >> 2)] = uint8_t(sb);
                 }
             }
+        }
+    };
+    uint4 x[kV], r[kV];                                    // (r: the residual, or the row after x's)
+    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (row < a.rows) load(x, a.x, a.ld_x, row);
+    if constexpr (kResidual) {
+        if (row < a.rows) load(r, a.residual, a.ld_residual, row);
+        for (int parity = 0; row < a.rows; row += step, parity ^= 1) one_row(row, row + step, x, r, part[parity]);
+    } else {
+        if (row + step < a.rows) load(r, a.x, a.ld_x, row + step);
+        for (; row < a.rows; row += 2 * step) {
+            one_row(row, row + 2 * step, x, x, part[0]);
+            if (row + step < a.rows) one_row(row + step, row + 3 * step, r, r, part[1]);
         }
     }
 }
@@ -812,8 +825,8 @@ rms_backward_reduce_kernel(const RmsBackwardArgs a, int parts) {
 
 // ---------------------------------------------------------------- launches
 
-// Blocks of `threads` threads that an SM holds at 64 registers each.
-int resident(int threads) { return threads > 1024 ? 1 : 1024 / threads > 32 ? 32 : 1024 / threads; }
+// Blocks of `threads` threads that an SM holds, if it holds `most` threads.
+int resident(int threads, int most) { return threads > most ? 1 : most / threads > 32 ? 32 : most / threads; }
 
 // Threads that hold a row of `n` pieces, `per` each.
 int row_threads(int64_t n, int64_t per) { return int((n + 32 * per - 1) / (32 * per) * 32); }
@@ -822,10 +835,11 @@ template <typename T, bool kP32, int kV, bool kQuantise>
 cudaError_t forward_vec_launch(const RmsArgs& a, int nvec, int sms, cudaStream_t stream) {
     const int tx = row_threads(nvec, kV), ty = tx == 32 ? 4 : 1;
     int64_t blocks = (a.rows + ty - 1) / ty;
-    const int64_t most = int64_t(sms) * (kV > 2 ? (tx * 2 > kThreads ? 1 : 2) : resident(tx * ty));
+    const int64_t most = int64_t(sms) * (kV > 2 ? (tx * 2 > kThreads ? 1 : 2) : resident(tx * ty, kV == 2 ? 896 : 1024));
     if (blocks > most) blocks = most;
-    return launch_dependent(rms_forward_vec_kernel<T, kP32, kV, kQuantise>, dim3(unsigned(blocks)),
-                            dim3(unsigned(tx), unsigned(ty)), stream, a, nvec);
+    const dim3 grid{unsigned(blocks)}, block{unsigned(tx), unsigned(ty)};
+    return a.residual ? launch_dependent(rms_forward_vec_kernel<T, kP32, kV, kQuantise, true>, grid, block, stream, a, nvec)
+                      : launch_dependent(rms_forward_vec_kernel<T, kP32, kV, kQuantise, false>, grid, block, stream, a, nvec);
 }
 
 // Vectors per thread: one while there are too few rows to fill the GPU with smaller
@@ -834,7 +848,7 @@ template <typename T, bool kP32, bool kQuantise>
 cudaError_t forward_vec(const RmsArgs& a, int sms, cudaStream_t stream) {
     const int nvec = int(a.hidden / Vec<T>::kN);
     if (nvec <= 32 || (a.rows <= 2 * sms && nvec <= 1024)) return forward_vec_launch<T, kP32, 1, kQuantise>(a, nvec, sms, stream);
-    if (nvec <= 2 * kThreads) return forward_vec_launch<T, kP32, 2, kQuantise>(a, nvec, sms, stream);
+    if (nvec <= 2 * kMostThreads<2>) return forward_vec_launch<T, kP32, 2, kQuantise>(a, nvec, sms, stream);
     if (nvec <= 4 * kThreads) return forward_vec_launch<T, kP32, 4, kQuantise>(a, nvec, sms, stream);
     return forward_vec_launch<T, kP32, 8, kQuantise>(a, nvec, sms, stream);
 }
@@ -843,7 +857,7 @@ template <typename T, typename P, int kE>
 cudaError_t forward_any_launch(const RmsArgs& a, int sms, cudaStream_t stream) {
     const int tx = row_threads(a.hidden, kE), ty = tx == 32 ? 4 : 1;
     int64_t blocks = (a.rows + ty - 1) / ty;
-    const int64_t most = int64_t(sms) * (kE > 8 ? 1 : resident(tx * ty));
+    const int64_t most = int64_t(sms) * (kE > 8 ? 1 : resident(tx * ty, 1024));
     if (blocks > most) blocks = most;
     return launch_dependent(rms_forward_any_kernel<T, P, kE>, dim3(unsigned(blocks)), dim3(unsigned(tx), unsigned(ty)), stream, a);
 }
