@@ -720,7 +720,6 @@ ln_backward_few_kernel(const LnBackwardArgs a, int nvec, int col_blocks) {
 // is loaded before the sums of this one cross the group.  Measured (us; this, a
 // pass for dx and one for the columns' sums): 4097 x 1023 fp16 with fp32
 // parameters 17.2, 30.5; 5000 x 3001 fp32 49, 141; 1000 x 7001 bf16 30, 56.
-constexpr int kAnyThreads = 512;
 template <int kE> constexpr int kAnyBlocks = kE <= 4 ? 2 : 1;          // per SM
 template <int kE> constexpr bool kAhead = kE <= 8;                     // (more would not fit in the registers)
 template <typename T, typename P, int kE>

@@ -105,7 +105,45 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
+// Sum over the block's warps of a value that each warp has summed (the same value
+// in each thread, in warp order).  `part`: a slot for each warp; one call between
+// two barriers of the block.
+__device__ __forceinline__ float across_warps(float v, float* part, int warps, int warp, int lane) {
+    if (warps == 1) return v;
+    if (lane == 0) part[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < warps ? part[lane] : 0.0f);
+}
+
+// The compiler takes the words for new ones from here on: what it unpacked of them
+// before is unpacked again rather than kept in registers.
+__device__ __forceinline__ void unpack_again(uint4& w) { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)); }
+
+// A thread's sum of term(i) over i = t, t + kAnyThreads, ... in a block of kAnyThreads:
+// up to 32768 terms (rows of 2^24 elements), 64 to a batch, the batches added 64 to a
+// batch of batches, so that a chain has at most 64 + 64 + 8 additions.
+constexpr int kAnyThreads = 512;                 // of the kernels for rows in any layout
+template <typename F> __device__ __forceinline__ float long_sum(int64_t hidden, F&& term) {
+    float total = 0.0f, outer = 0.0f;
+    int batches = 0;
+    for (int64_t i = threadIdx.x; i < hidden;) {
+        float batch = 0.0f;
+        for (int k = 0; k < 64 && i < hidden; ++k, i += kAnyThreads) batch += term(i);
+        outer += batch;
+        if (++batches == 64) {
+            total += outer;
+            outer = 0.0f;
+            batches = 0;
+        }
+    }
+    return total + outer;
+}
+
 // ---------------------------------------------------------------- launches
+
+// Threads that hold a row of `n` pieces, `per` each.
+inline int row_threads(int64_t n, int64_t per) { return int((n + 32 * per - 1) / (32 * per) * 32); }
+
 
 // Launch with programmatic stream serialisation: the blocks may start while
 // the previous kernel in the stream finishes (every kernel here waits for it
