@@ -52,7 +52,9 @@ template <typename T> __device__ __forceinline__ uint64_t rounded(uint64_t v) {
 // per block where a warp holds a row (then no warp waits for another).  The longest
 // chain of a sum: 8 kV / 2 + 1 + 5 additions in a warp, 5 over the warps.
 // kQuantise (T = bf16): four neighbouring lanes hold an MX block of 32 elements.
-template <typename T, bool kP32, int kV, bool kQuantise, bool kResidual>
+// kShift: rows of 16-bit elements off 16-byte boundaries, as ShiftedRows (nvec is
+// then not used); 14666 x 4001 bf16 with a residual 208 us element by element.
+template <typename T, bool kP32, int kV, bool kQuantise, bool kResidual, bool kShift>
 __global__ void __launch_bounds__(kMostThreads<kV>, kV == 2 ? 2 : 1)
 rms_forward_vec_kernel(const RmsArgs a, int nvec) {
     using V = Vec<T>;
@@ -61,16 +63,30 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
     grid_launch_dependents();
     const int t = int(threadIdx.x), tx = int(blockDim.x), lane = t & 31, warp = t >> 5, warps = tx >> 5;
     const int64_t step = int64_t(gridDim.x) * blockDim.y;
-    constexpr bool kKeep = kV <= 2;                        // gamma in registers (of more vectors it comes from L1)
+    ShiftedRow<T> sr{int(a.hidden), 0};
+    if constexpr (kShift) {
+        sr.shift = int((int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * a.ld_x % V::kN);
+        nvec = sr.vectors();
+    }
+    constexpr bool kKeep = kV <= 2 || kShift;              // gamma in registers (of more vectors it comes from L1)
     ParamVec<T, kP32> g[kKeep ? kV : 1];
     if constexpr (kKeep) {
 #pragma unroll
-        for (int v = 0; v < kV; ++v) g[v].load(a.gamma, t + v * tx < nvec ? t + v * tx : 0);
+        for (int v = 0; v < kV; ++v) {
+            if constexpr (kShift) sr.template load_params<kP32>(g[v], a.gamma, t + v * tx);
+            else g[v].load(a.gamma, t + v * tx < nvec ? t + v * tx : 0);
+        }
     }
     auto load = [&](uint4 (&w)[kV], const void* from, int64_t ld, int64_t row) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(from) + row * ld);
+        if constexpr (kShift) {
+            const T* p = static_cast<const T*>(from) + row * ld;
 #pragma unroll
-        for (int v = 0; v < kV; ++v) w[v] = t + v * tx < nvec ? __ldcs(p + t + v * tx) : make_uint4(0, 0, 0, 0);
+            for (int v = 0; v < kV; ++v) w[v] = t + v * tx < nvec ? sr.load(p, t + v * tx) : make_uint4(0, 0, 0, 0);
+        } else {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(from) + row * ld);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) w[v] = t + v * tx < nvec ? __ldcs(p + t + v * tx) : make_uint4(0, 0, 0, 0);
+        }
     };
     // the row of words x (and residual r), which then hold those of row `next`
     auto one_row = [&](int64_t row, int64_t next, uint4 (&x)[kV], uint4 (&r)[kV], float* slots) {
@@ -85,7 +101,11 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
                 for (int k = 0; k < V::kPairs; ++k) o[k] = f32x2::add(V::pair(x[v], k), V::pair(r[v], k));
                 z[v] = V::from_pairs(o);
                 const int i = t + v * tx;
-                if (i < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.z) + row * a.ld_z)[i] = z[v];
+                if constexpr (kShift) {
+                    if (i < nvec) sr.store(static_cast<T*>(a.z) + row * a.ld_z, i, z[v]);
+                } else {
+                    if (i < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.z) + row * a.ld_z)[i] = z[v];
+                }
             }
 #pragma unroll
             for (int k = 0; k < V::kPairs; ++k) {
@@ -109,7 +129,11 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
             uint64_t o[V::kPairs];
 #pragma unroll
             for (int k = 0; k < V::kPairs; ++k) o[k] = f32x2::mul(f32x2::mul(V::pair(z[v], k), rs2), gv.pair(k));
-            if (a.y && i < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.ld_y)[i] = V::from_pairs(o);
+            if constexpr (kShift) {
+                if (a.y && i < nvec) sr.store(static_cast<T*>(a.y) + row * a.ld_y, i, V::from_pairs(o));
+            } else {
+                if (a.y && i < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.ld_y)[i] = V::from_pairs(o);
+            }
             if constexpr (kQuantise) {
                 float m = maxabs(f32x2::lo(o[0]), f32x2::hi(o[0]));
 #pragma unroll
@@ -317,26 +341,29 @@ rms_colwise_kernel(const RmsArgs a, unsigned col_units) {
 // Blocks of `threads` threads that an SM holds, if it holds `most` threads.
 int resident(int threads, int most) { return threads > most ? 1 : most / threads > 32 ? 32 : most / threads; }
 
-template <typename T, bool kP32, int kV, bool kQuantise>
+template <typename T, bool kP32, int kV, bool kQuantise, bool kShift>
 cudaError_t forward_vec_launch(const RmsArgs& a, int nvec, int sms, cudaStream_t stream) {
     const int tx = row_threads(nvec, kV), ty = tx == 32 ? 4 : 1;
     int64_t blocks = (a.rows + ty - 1) / ty;
     const int64_t most = int64_t(sms) * (kV > 2 ? (tx * 2 > kThreads ? 1 : 2) : resident(tx * ty, kV == 2 ? 896 : 1024));
     if (blocks > most) blocks = most;
+    if (kShift) blocks = blocks_for_shifts(blocks, ty, a.rows);
     const dim3 grid{unsigned(blocks)}, block{unsigned(tx), unsigned(ty)};
-    return a.residual ? launch_dependent(rms_forward_vec_kernel<T, kP32, kV, kQuantise, true>, grid, block, stream, a, nvec)
-                      : launch_dependent(rms_forward_vec_kernel<T, kP32, kV, kQuantise, false>, grid, block, stream, a, nvec);
+    return a.residual ? launch_dependent(rms_forward_vec_kernel<T, kP32, kV, kQuantise, true, kShift>, grid, block, stream, a, nvec)
+                      : launch_dependent(rms_forward_vec_kernel<T, kP32, kV, kQuantise, false, kShift>, grid, block, stream, a, nvec);
 }
 
 // Vectors per thread: one while there are too few rows to fill the GPU with smaller
-// blocks, else two, four or eight as the row needs.
-template <typename T, bool kP32, bool kQuantise>
+// blocks, else two, four or eight as the row needs (eight not with kShift).
+template <typename T, bool kP32, bool kQuantise, bool kShift>
 cudaError_t forward_vec(const RmsArgs& a, int sms, cudaStream_t stream) {
-    const int nvec = int(a.hidden / Vec<T>::kN);
-    if (nvec <= 32 || (a.rows <= 2 * sms && nvec <= 1024)) return forward_vec_launch<T, kP32, 1, kQuantise>(a, nvec, sms, stream);
-    if (nvec <= 2 * kMostThreads<2>) return forward_vec_launch<T, kP32, 2, kQuantise>(a, nvec, sms, stream);
-    if (nvec <= 4 * kThreads) return forward_vec_launch<T, kP32, 4, kQuantise>(a, nvec, sms, stream);
-    return forward_vec_launch<T, kP32, 8, kQuantise>(a, nvec, sms, stream);
+    // (a shifted row's elements can begin and end within vectors)
+    const int nvec = int(kShift ? (a.hidden + 2 * (Vec<T>::kN - 1)) / Vec<T>::kN : a.hidden / Vec<T>::kN);
+    if (nvec <= 32 || (a.rows <= 2 * sms && nvec <= 1024)) return forward_vec_launch<T, kP32, 1, kQuantise, kShift>(a, nvec, sms, stream);
+    if (nvec <= 2 * kMostThreads<2>) return forward_vec_launch<T, kP32, 2, kQuantise, kShift>(a, nvec, sms, stream);
+    if (kShift || nvec <= 4 * kThreads) return forward_vec_launch<T, kP32, 4, kQuantise, kShift>(a, nvec, sms, stream);
+    if constexpr (!kShift) return forward_vec_launch<T, kP32, 8, kQuantise, false>(a, nvec, sms, stream);
+    return cudaErrorInvalidValue;                          // (not reached)
 }
 
 template <typename T, typename P, int kE>
@@ -356,6 +383,10 @@ cudaError_t forward_any(const RmsArgs& a, int sms, cudaStream_t stream) {
     return launch_dependent(rms_forward_long_kernel<T, P>, dim3(unsigned(a.rows)), dim3(kAnyThreads), stream, a);
 }
 
+// Elements of a row that four vectors in each of a block's threads hold, whatever its shift.
+constexpr int64_t kMostShifted = 4 * kThreads * 8 - 14;
+constexpr int64_t kLeastShifted = 192;          // (below, single elements are as fast)
+
 template <typename T>
 cudaError_t forward(const RmsArgs& a, int sms, cudaStream_t stream) {
     const int64_t nvec = a.hidden / Vec<T>::kN;
@@ -363,9 +394,14 @@ cudaError_t forward(const RmsArgs& a, int sms, cudaStream_t stream) {
     if (a.hidden % Vec<T>::kN == 0 && nvec <= 8 * kThreads && fits(a.x, a.ld_x) && fits(a.residual, a.ld_residual) &&
         fits(a.z, a.ld_z) && fits(a.y, a.ld_y) && on16(a.gamma)) {
         if constexpr (sizeof(T) == 2)
-            if (a.param_dtype != TE_MX_FP32) return forward_vec<T, false, false>(a, sms, stream);
-        return forward_vec<T, true, false>(a, sms, stream);
+            if (a.param_dtype != TE_MX_FP32) return forward_vec<T, false, false, false>(a, sms, stream);
+        return forward_vec<T, true, false, false>(a, sms, stream);
     }
+    if constexpr (sizeof(T) == 2)
+        if (a.rows > 1 && a.hidden >= kLeastShifted && a.hidden <= kMostShifted && shifts_alike<T>(a.x, a.ld_x, a.ld_x) && shifts_alike<T>(a.residual, a.ld_residual, a.ld_x) &&
+            shifts_alike<T>(a.z, a.ld_z, a.ld_x) && shifts_alike<T>(a.y, a.ld_y, a.ld_x))
+            return a.param_dtype != TE_MX_FP32 ? forward_vec<T, false, false, true>(a, sms, stream)
+                                               : forward_vec<T, true, false, true>(a, sms, stream);
     if (a.param_dtype == a.dtype) return forward_any<T, T>(a, sms, stream);
     return forward_any<T, float>(a, sms, stream);
 }
@@ -392,8 +428,8 @@ te_mx_status rms_quantize_launch(const RmsArgs& a, cudaStream_t stream) {
     const bool p32 = a.param_dtype == TE_MX_FP32;
     using B = __nv_bfloat16;
     cudaError_t e;
-    if (a.q_row) e = p32 ? forward_vec<B, true, true>(a, sms, stream) : forward_vec<B, false, true>(a, sms, stream);
-    else e = p32 ? forward_vec<B, true, false>(a, sms, stream) : forward_vec<B, false, false>(a, sms, stream);
+    if (a.q_row) e = p32 ? forward_vec<B, true, true, false>(a, sms, stream) : forward_vec<B, false, true, false>(a, sms, stream);
+    else e = p32 ? forward_vec<B, true, false, false>(a, sms, stream) : forward_vec<B, false, false, false>(a, sms, stream);
     if (e != cudaSuccess || !a.q_col) return cuda_status(e, "rmsnorm quantize kernel launch");
     const unsigned col_units = unsigned((a.hidden + 63) / 64);
     const int64_t bands = (a.rows + 32 * kColWarps - 1) / (32 * kColWarps);

@@ -93,6 +93,64 @@ template <typename T, bool kP32> struct ParamVec {
     }
 };
 
+// ---------------------------------------------------------------- rows off 16-byte boundaries
+
+// Rows of 16-bit elements whose pitch is no multiple of 8: the rows of a block that are
+// multiples of 8 apart start equally far behind a 16-byte boundary (the base lies on
+// one), so they are read and written in whole vectors all the same.  Vector i of a row
+// that starts `shift` elements behind a boundary holds its elements 8 i - shift ..
+// 8 i - shift + 7; of the first and the last vector, which reach into the neighbouring
+// rows, only the row's own elements are touched, one by one.
+template <typename T> struct ShiftedRow {
+    static constexpr int kN = Vec<T>::kN;
+    int hidden, shift;
+    __device__ __forceinline__ int vectors() const { return (hidden + shift + kN - 1) / kN; }
+    __device__ __forceinline__ bool whole(int i) const { return i * kN >= shift && i * kN - shift + kN <= hidden; }
+    __device__ __forceinline__ bool has(int i, int k) const { return unsigned(i * kN - shift + k) < unsigned(hidden); }
+    // The vector's elements, 0 outside the row.  `row`: its first element; read once.
+    __device__ __forceinline__ uint4 load(const T* row, int i) const {
+        if (whole(i)) return __ldcs(reinterpret_cast<const uint4*>(row - shift) + i);
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+            if (has(i, k)) w[k / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[i * kN - shift + k]) << (k % 2 * 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void store(T* row, int i, const uint4& v) const {
+        if (whole(i)) {
+            reinterpret_cast<uint4*>(row - shift)[i] = v;
+            return;
+        }
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+            if (has(i, k)) reinterpret_cast<uint16_t*>(row)[i * kN - shift + k] = uint16_t(w[k / 2] >> (k % 2 * 16));
+    }
+    // parameters of the vector's elements (0 outside the row)
+    template <bool kP32> __device__ __forceinline__ void load_params(ParamVec<T, kP32>& p, const void* from, int i) const {
+        float f[kN];
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            f[k] = 0.0f;
+            if (has(i, k)) {
+                if constexpr (kP32) f[k] = load_param<float>(from, i * kN - shift + k);
+                else f[k] = load_param<T>(from, i * kN - shift + k);
+            }
+        }
+        if constexpr (ParamVec<T, kP32>::kWords == 2) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                p.w[q] = make_uint4(__float_as_uint(f[4 * q]), __float_as_uint(f[4 * q + 1]), __float_as_uint(f[4 * q + 2]),
+                                    __float_as_uint(f[4 * q + 3]));
+        } else {
+            uint64_t o[kN / 2];
+#pragma unroll
+            for (int k = 0; k < kN / 2; ++k) o[k] = f32x2::pack(f[2 * k], f[2 * k + 1]);
+            p.w[0] = Vec<T>::from_pairs(o);                // (exact)
+        }
+    }
+};
+
 // ---------------------------------------------------------------- blocks
 
 // Sizes and both addresses are multiples of 16 bytes; counted on the mbarrier `bar`.
@@ -160,6 +218,17 @@ cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, cudaStre
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Whether a matrix's rows can be taken as ShiftedRows beside those of pitch `ld`.
+template <typename T> inline bool shifts_alike(const void* p, int64_t ld_p, int64_t ld) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld_p - ld) % Vec<T>::kN == 0);
+}
+// Blocks, so that the rows of a block (rows_per_block at a time) are multiples of 8 apart.
+inline int64_t blocks_for_shifts(int64_t blocks, int rows_per_block, int64_t rows) {
+    if (blocks * rows_per_block >= rows) return blocks;    // (one row each)
+    const int64_t unit = rows_per_block >= 8 ? 1 : 8 / rows_per_block;
+    return blocks < unit ? unit : blocks / unit * unit;
 }
 
 inline bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
