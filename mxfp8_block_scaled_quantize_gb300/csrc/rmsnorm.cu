@@ -125,6 +125,7 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
         for (int v = 0; v < kV; ++v) {
             const int i = t + v * tx;
             ParamVec<T, kP32>& gv = g[kKeep ? v : 0];
+            if constexpr (kQuantise && kResidual) unpack_again(z[v]);      // (8192 x 7168: 66.2 -> 65.2 us)
             if constexpr (!kKeep) gv.load(a.gamma, i < nvec ? i : 0);
             uint64_t o[V::kPairs];
 #pragma unroll
