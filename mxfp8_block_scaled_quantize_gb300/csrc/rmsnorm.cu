@@ -51,9 +51,12 @@ template <typename T> __device__ __forceinline__ uint64_t rounded(uint64_t v) {
 // one row ahead, 28 KB in flight per SM, 8192 x 7168 bf16 took 41.3 us); blockDim.y rows
 // per block where a warp holds a row (then no warp waits for another).  The longest
 // chain of a sum: 8 kV / 2 + 1 + 5 additions in a warp, 5 over the warps.
-// kQuantise (T = bf16): four neighbouring lanes hold an MX block of 32 elements.
+// HBM bounds it: 8192 x 7168 bf16 with a residual 74 us (floor 69.4), without 41 (34.7).
+// kQuantise (T = bf16): four neighbouring lanes hold an MX block of 32 elements; with a
+// residual 65 us (61), without, where instructions bound it, 43 (26).
 // kShift: rows of 16-bit elements off 16-byte boundaries, as ShiftedRows (nvec is
-// then not used); 14666 x 4001 bf16 with a residual 208 us element by element.
+// counted here); with a residual (us; this, element by element): 14676 x 4001 bf16 122,
+// 208; 16384 x 769 31, 55; 16384 x 257 17, 23; 16384 x 101 9.1, 8.3.
 template <typename T, bool kP32, int kV, bool kQuantise, bool kResidual, bool kShift>
 __global__ void __launch_bounds__(kMostThreads<kV>, kV == 2 ? 2 : 1)
 rms_forward_vec_kernel(const RmsArgs a, int nvec) {
@@ -173,7 +176,7 @@ rms_forward_vec_kernel(const RmsArgs a, int nvec) {
 }
 
 // Rows of up to 512 kE elements in any layout: persistent, element by element,
-// gamma in registers.
+// gamma in registers.  3001 x 1021 fp16 in pitch 1024, y in pitch 1021: 11.9 us (floor 3.6).
 template <typename T, typename P, int kE>
 __global__ void __launch_bounds__(kAnyThreads, kE <= 8 ? 2 : 1)
 rms_forward_any_kernel(const RmsArgs a) {
@@ -261,7 +264,11 @@ rms_forward_long_kernel(const RmsArgs a) {
 // leave as up to 128 contiguous bytes through shared memory.  A block's largest |y| is
 // fl(max fl(z rs) gamma): rounding keeps the order, so gamma enters after the maximum.
 // Blocks go from the last rows to the first: what the kernel above wrote last is still
-// in L2 (it reads x and the residual as data that is not read again).
+// in L2 (it reads x and the residual as data that is not read again).  8192 x 7168: 38 us
+// (floor 26), 60 % of the issue slots.  Tried: persistent with the next tile's words in
+// registers 40, TMA loads and stores in a ring per warp 40, both copies in one pass over
+// z in the shared memory of clusters (three blocks of 256 threads per SM) 145 to 168 for
+// all of it, against 104 with the two kernels.
 constexpr int kColWarps = 4;
 template <bool kP32>
 __global__ void __launch_bounds__(kColWarps * 32, 4)

@@ -21,9 +21,11 @@ namespace {
 // so the sums of dy xh over the rows stay in registers.  The rows come through a ring
 // in shared memory, one bulk copy of each operand, and are read there twice: for the
 // row's sum, and for its dx once the sum is known, so that no word waits in registers.
-// The sum of the next row is taken before the dx of this one, so that its way across
-// the warp and the group is hidden behind that; a row's stage is filled again after
-// the next row's barrier, which every warp reaches past its last read of the row.
+// A row's stage is filled again after the next row's barrier, which every warp reaches
+// past its last read of the row.  HBM bounds it: 8192 x 7168 bf16 with dz 74.8 us (floor
+// 69.4; with the words kept in registers, spilled, 147; two groups of 448 threads at 72
+// registers 94; the next row's sum taken before this row's dx 81), 1111 x 8200 fp32
+// without dz 25 (16.2), of which the join of the blocks' sums takes 5.
 // The groups of a block are joined at the end, so that every block leaves one partial
 // sum per column.
 // kOnce: a ring of one stage, for rows of which two do not fit: words stay in
@@ -209,9 +211,12 @@ rms_backward_vec_kernel(const RmsBackwardArgs a, const RmsBwdShape sh, unsigned 
 // Few rows on 16-byte boundaries: one launch.  dgamma needs no sum over a row's
 // elements (rs is given), so the first col_blocks blocks own 8 vectors of columns
 // each and add them over all rows, while a block per row computes dx; dy and z come
-// from L2 the second time.  (dx may not overlap dy or z here.)
+// from L2 the second time.  (dx may not overlap dy or z here.)  Measured, with dz (us;
+// this, the persistent kernel and the join of its blocks' sums): 1 x 7168 bf16 2.9, 6.5;
+// 304 x 7168 5.5, 8.8; 512 x 7168 8.6, 11.5; 1000 x 7168 16.5, 17.5; 2000 x 7168 29, 26;
+// 512 x 512 4.0, 4.9; 1000 x 512 6.0, 4.9; 512 x 16384 fp32 46, 53: so up to 512 rows.
 constexpr int kFewThreads = 512;
-constexpr int kFewRows = 304;
+constexpr int kFewRows = 512;
 constexpr int kFewVectors = 8;                   // of columns per column block: 128 bytes of a row
 template <typename T, bool kP32, int kV>
 __global__ void __launch_bounds__(kFewThreads, kV <= 4 ? 2 : 1)
@@ -316,7 +321,8 @@ rms_backward_few_kernel(const RmsBackwardArgs a, int nvec, int col_blocks) {
 // Rows of up to 512 kE elements in any layout: persistent.  blockDim.x threads own
 // the same columns (kE each, element by element) of every row that they take;
 // blockDim.y such groups per block, joined at the end.  The next row is loaded before
-// the sum of this one crosses the group.
+// the sum of this one crosses the group.  Loads and stores of single elements bound it:
+// 4097 x 1023 fp16 with dz 13.9 us (floor 5.0), 8192 x 7167 bf16 152 (69).
 template <int kE> constexpr int kAnyBlocks = kE <= 8 ? 2 : 1;          // per SM
 template <typename T, typename P, int kE>
 __global__ void __launch_bounds__(kAnyThreads, kAnyBlocks<kE>)
