@@ -291,9 +291,9 @@ TEMX_API te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, co
                                                void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
                                                void* stream);
 
-/* te_mx_rmsnorm — root-mean-square norm with the residual's addition (the pre-norm
- * blocks that scale by the root mean square alone; te.RMSNorm beside te.LayerNorm,
- * leeroopedia "FP8 Training Quickstart").  Per row r:
+/* te_mx_rmsnorm — root-mean-square norm with the residual's addition (the rmsnorm of
+ * "Experimental Triton Kernels on ROCm", ROCm/TransformerEngine README, with what a
+ * pre-norm block does in front of it).  Per row r:
  *   z[r] = x[r] + residual[r], rounded to `dtype` (z = x if residual is NULL),
  *   rsigma[r] = 1/sqrt(mean(z[r]^2) + eps),  y = (z rsigma) gamma,
  * in fp32, y rounded once.  z is what the next layer and the backward pass read.

@@ -1084,7 +1084,7 @@ def moe_dispatch(x, row, scales=None, total_rows=None, stream=None, out=None):
     s = ld_s = width = d_s = ld_ds = 0
     if scales is not None:
         width = hidden // 32
-        assert size == 1 and _bytes(scales, tokens, width, device)
+        assert size == 1 and hidden % 32 == 0 and _bytes(scales, tokens, width, device)
     if out is None:
         m = tokens * k if total_rows is None else total_rows
         d = torch.empty((m, hidden), dtype=x.dtype, device=x.device)

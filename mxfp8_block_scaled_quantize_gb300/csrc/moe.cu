@@ -220,12 +220,12 @@ route_backward_kernel(const RouteArgs a) {
 // 131072 slots took 2 us more).  A warp holds its slots in registers,
 // 16 groups of 32; more slots than all warps hold are sorted in rounds, after a pass
 // that counts the experts' slots in all of them.
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortWarps = 32;                   // of a block
+constexpr int kSortFewWarps = 8;                 // of a block alone, for few slots and experts
 constexpr int kSortCluster = 16;                 // blocks at most (8 without the wide clusters)
 constexpr int kMaxExperts = 1024;
 constexpr int kSortHeld = 16;                    // groups of 32 slots in a warp's registers
-constexpr int kSortBlockSlots = kSortThreads * kSortHeld;
+constexpr int kSortBlockSlots = 32 * kSortWarps * kSortHeld;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -244,7 +244,7 @@ __device__ __forceinline__ int32_t remote_load(const int32_t* p, uint32_t rank) 
 }
 
 // Inclusive sum over the block's threads; `sums`: a slot for each warp.
-__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums, int warp, int lane) {
+template <int kWarps> __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums, int warp, int lane) {
     auto warp_scan = [&](int32_t x) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -256,27 +256,28 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums, int warp
     v = warp_scan(v);
     if (lane == 31) sums[warp] = v;
     __syncthreads();
-    const int32_t w = warp_scan(sums[lane]);               // (kSortWarps = 32)
+    const int32_t w = warp_scan(lane < kWarps ? sums[lane] : 0);
     const int32_t before = __shfl_sync(0xFFFFFFFFu, w, warp == 0 ? 0 : warp - 1);
     return warp == 0 ? v : v + before;
 }
 
-template <int kBits>                             // of an expert's index
-__global__ void __launch_bounds__(kSortThreads, 1)
+template <int kBits, int kWarps>                 // of an expert's index, of a block
+__global__ void __launch_bounds__(32 * kWarps, 1)
 moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t experts, int blocks, int32_t* __restrict__ group_m,
                 int32_t* __restrict__ row, int32_t* __restrict__ slot, unsigned int* status) {
+    constexpr int kThreads = 32 * kWarps, kSlots = kThreads * kSortHeld;
     extern __shared__ int32_t shared[];
-    uint32_t* sorted = reinterpret_cast<uint32_t*>(shared);            // [kSortBlockSlots]: expert << 16 | slot
-    int32_t* counts = shared + kSortBlockSlots;            // [kSortWarps][experts]: counts, then first places
+    uint32_t* sorted = reinterpret_cast<uint32_t*>(shared);            // [kSlots]: expert << 16 | slot
+    int32_t* counts = shared + kSlots;                     // [kWarps][experts]: counts, then first places
     __shared__ int32_t total[2][kMaxExperts];              // of this block's slots (read by the other blocks)
     __shared__ int32_t to_row[kMaxExperts];                // from a place in `sorted` to a row
-    __shared__ int32_t sums[2][kSortWarps];
+    __shared__ int32_t sums[2][kWarps];
     __shared__ int32_t here_kept, all_kept;
     grid_dependency_wait();
     grid_launch_dependents();
     const int t = int(threadIdx.x), lane = t & 31, warp = t >> 5;
     const uint32_t rank = blocks > 1 ? cluster_rank() : 0u;
-    const int64_t per_round = int64_t(blocks) * kSortBlockSlots, rounds = slots > per_round ? (slots + per_round - 1) / per_round : 1;
+    const int64_t per_round = int64_t(blocks) * kSlots, rounds = slots > per_round ? (slots + per_round - 1) / per_round : 1;
     auto sync_blocks = [&] {
         if (blocks > 1) cluster_sync_all();
         else __syncthreads();
@@ -299,29 +300,29 @@ moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t expert
     if (rounds > 1) {
         total[1][t] = 0;
         __syncthreads();
-        for (int64_t s = int64_t(rank) * kSortThreads + t; s < slots; s += int64_t(blocks) * kSortThreads) {
+        for (int64_t s = int64_t(rank) * kThreads + t; s < slots; s += int64_t(blocks) * kThreads) {
             const int32_t e = index[s];
             if (e >= 0 && e < experts) atomicAdd(&total[1][e], 1);
         }
         sync_blocks();
         int32_t before;
         all = across_blocks(total[1], before);
-        const int32_t upto = block_scan(all, sums[0], warp, lane);
+        const int32_t upto = block_scan<kWarps>(all, sums[0], warp, lane);
         start = upto - all;
-        if (t == kSortThreads - 1) all_kept = upto;
+        if (t == kThreads - 1) all_kept = upto;
     }
     for (int64_t round = 0; round < rounds; ++round) {
         // this block's slots of the round, and this warp's, whole groups of 32
         const int64_t first = round * per_round;
         const int in_round = int(slots - first < per_round ? slots - first : per_round);
-        const int groups = (in_round + 31) / 32, parts = blocks * kSortWarps, part = int(rank) * kSortWarps + warp;
+        const int groups = (in_round + 31) / 32, parts = blocks * kWarps, part = int(rank) * kWarps + warp;
         const int g0 = groups * part / parts, n = groups * (part + 1) / parts - g0;    // (at most 4096 x 256; at most kSortHeld)
-        const int of_block = 32 * (groups * (int(rank) * kSortWarps) / parts), s0 = 32 * g0 + lane;
+        const int of_block = 32 * (groups * (int(rank) * kWarps) / parts), s0 = 32 * g0 + lane;
         const int32_t* from = index + first + s0;
         int32_t of[kSortHeld];                             // expert << 16 | rank; -1: none
 #pragma unroll
         for (int i = 0; i < kSortHeld; ++i) of[i] = i < n && s0 + 32 * i < in_round ? from[32 * i] : -1;
-        for (int i = t; i < kSortWarps * experts; i += kSortThreads) counts[i] = 0;
+        for (int i = t; i < kWarps * experts; i += kThreads) counts[i] = 0;
         __syncthreads();
         int32_t* mine = counts + warp * experts;
 #pragma unroll
@@ -351,7 +352,7 @@ moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t expert
         // over the warps
         int32_t here = 0;
         if (t < experts) {
-            for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+            for (int w0 = 0; w0 < kWarps; w0 += 8) {
                 int32_t c[8];
 #pragma unroll
                 for (int w = 0; w < 8; ++w) c[w] = counts[(w0 + w) * experts + t];
@@ -366,16 +367,16 @@ moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t expert
         const int32_t of_round = across_blocks(total[round & 1], before);
         if (rounds == 1) {
             all = of_round;
-            const int32_t upto = block_scan(all, sums[0], warp, lane);
+            const int32_t upto = block_scan<kWarps>(all, sums[0], warp, lane);
             start = upto - all;
-            if (t == kSortThreads - 1) all_kept = upto;
+            if (t == kThreads - 1) all_kept = upto;
         }
-        const int32_t place_upto = block_scan(here, sums[1], warp, lane);
-        if (t == kSortThreads - 1) here_kept = place_upto;
+        const int32_t place_upto = block_scan<kWarps>(here, sums[1], warp, lane);
+        if (t == kThreads - 1) here_kept = place_upto;
         if (t < experts) {
             int32_t p = place_upto - here;                 // the expert's first place in `sorted`
             to_row[t] = start + done + before - p;
-            for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+            for (int w0 = 0; w0 < kWarps; w0 += 8) {
                 int32_t c[8];
 #pragma unroll
                 for (int w = 0; w < 8; ++w) c[w] = counts[(w0 + w) * experts + t];
@@ -403,14 +404,14 @@ moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t expert
         }
         __syncthreads();
         const int32_t base = int32_t(first) + of_block;
-        for (int p = t; p < here_kept; p += kSortThreads) {
+        for (int p = t; p < here_kept; p += kThreads) {
             const uint32_t v = sorted[p];
             slot[p + to_row[v >> 16]] = base + int32_t(v & 0xFFFFu);
         }
     }
     if (rank == 0 && t < experts) group_m[t] = all;
     // rows without a slot
-    for (int64_t r = all_kept + int64_t(rank) * kSortThreads + t; r < slots; r += int64_t(blocks) * kSortThreads) slot[r] = -1;
+    for (int64_t r = all_kept + int64_t(rank) * kThreads + t; r < slots; r += int64_t(blocks) * kThreads) slot[r] = -1;
     if (blocks > 1) cluster_sync_all();                    // no block leaves while another may still read its counts
 }
 
@@ -710,7 +711,7 @@ te_mx_status route_launch(const RouteArgs& a, cudaStream_t stream) { return rout
 te_mx_status route_backward_launch(const RouteArgs& a, cudaStream_t stream) { return route_any(a, true, stream); }
 
 // Blocks of the sort: one up to where a cluster is faster (2048 slots: 6.3 us, 8 blocks
-// 6.4; 8192: 12, 6.7), eight, and sixteen, if the device takes such clusters, from where
+// 6.4; 8192: 12, 6.7; with up to 256 experts one of 8 warps: 400 slots 4.3 us, 32 warps 5.4), eight, and sixteen, if the device takes such clusters, from where
 // those are faster (16384: 7.2, 7.4; 32768: 8.7, 8.0; 131072: 15.8, 11.3).
 constexpr int64_t kSortAlone = 2048, kSortEight = 16384;
 
@@ -739,13 +740,19 @@ te_mx_status moe_sort_launch(const int32_t* index, int64_t slots, int32_t expert
     te_mx_status st = device_status_ptr(&status);
     if (st != TE_MX_OK) return st;
     const int which = experts <= 32 ? 0 : experts <= 64 ? 1 : experts <= 128 ? 2 : experts <= 256 ? 3 : 4;
-    auto kern = which == 0 ? moe_sort_kernel<5> : which == 1 ? moe_sort_kernel<6> : which == 2 ? moe_sort_kernel<7>
-                : which == 3 ? moe_sort_kernel<8> : moe_sort_kernel<10>;
+    auto kern = which == 0 ? moe_sort_kernel<5, kSortWarps> : which == 1 ? moe_sort_kernel<6, kSortWarps>
+                : which == 2 ? moe_sort_kernel<7, kSortWarps> : which == 3 ? moe_sort_kernel<8, kSortWarps>
+                                                                           : moe_sort_kernel<10, kSortWarps>;
+    int warps = kSortWarps;
+    if (slots <= kSortAlone && experts <= 32 * kSortFewWarps) {
+        kern = moe_sort_kernel<8, kSortFewWarps>;
+        warps = kSortFewWarps;
+    }
     cudaError_t e = set_smem_attribute_once(reinterpret_cast<const void*>(kern), (kSortBlockSlots + kSortWarps * kMaxExperts) * 4);
     if (e != cudaSuccess) return cuda_status(e, "expert sort kernel attributes");
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = size_t(kSortBlockSlots + kSortWarps * experts) * 4;
+    cfg.blockDim = dim3(unsigned(32 * warps));
+    cfg.dynamicSmemBytes = size_t(32 * warps * kSortHeld + warps * experts) * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -261,11 +261,12 @@ rms_forward_long_kernel(const RmsArgs a) {
 // The column-wise MXFP8 copy of y = z rs gamma (z and rs from the kernel above; its
 // programmatic dependent).  A warp takes 32 rows x 64 columns, a lane two columns,
 // whose blocks are then its own; four warps stack 128 rows, so that a column's codes
-// leave as up to 128 contiguous bytes through shared memory.  A block's largest |y| is
+// leave as up to 128 contiguous bytes through shared memory, and its scale bytes four
+// at a time (single bytes, a sector of L2 each, took 10 us more).  A block's largest |y| is
 // fl(max fl(z rs) gamma): rounding keeps the order, so gamma enters after the maximum.
 // Blocks go from the last rows to the first: what the kernel above wrote last is still
-// in L2 (it reads x and the residual as data that is not read again).  8192 x 7168: 38 us
-// (floor 26), 60 % of the issue slots.  Tried: persistent with the next tile's words in
+// in L2 (it reads x and the residual as data that is not read again).  8192 x 7168: 34 us
+// (floor 26; the loads alone 20.5, with the arithmetic 27).  Tried, with single bytes: persistent with the next tile's words in
 // registers 40, TMA loads and stores in a ring per warp 40, both copies in one pass over
 // z in the shared memory of clusters (three blocks of 256 threads per SM) 145 to 168 for
 // all of it, against 104 with the two kernels.
@@ -274,6 +275,7 @@ template <bool kP32>
 __global__ void __launch_bounds__(kColWarps * 32, 4)
 rms_colwise_kernel(const RmsArgs a, unsigned col_units) {
     __shared__ __align__(16) uint8_t codes[64][kColWarps * 32 + 16];     // (rows 16 bytes longer: fewer bank conflicts)
+    __shared__ __align__(4) uint8_t scales[64][kColWarps];
     __shared__ __align__(16) float2 rs[kColWarps * 32];    // twice each: a pair
     grid_dependency_wait();
     grid_launch_dependents();
@@ -329,13 +331,18 @@ rms_colwise_kernel(const RmsArgs a, unsigned col_units) {
         to_lo[1] = make_uint4(q_lo[4], q_lo[5], q_lo[6], q_lo[7]);
         to_hi[0] = make_uint4(q_hi[0], q_hi[1], q_hi[2], q_hi[3]);
         to_hi[1] = make_uint4(q_hi[4], q_hi[5], q_hi[6], q_hi[7]);
-        if (live) {
-            uint8_t* s = a.s_col + c * a.ld_s_col + (r0 >> 5);
-            s[0] = uint8_t(s_lo);
-            s[a.ld_s_col] = uint8_t(s_hi);
-        }
+        scales[2 * lane][warp] = uint8_t(s_lo);
+        scales[2 * lane + 1][warp] = uint8_t(s_hi);
     }
     __syncthreads();
+    if (threadIdx.x < 64 && c0 + threadIdx.x < a.hidden) {
+        uint8_t* s = a.s_col + (c0 + threadIdx.x) * a.ld_s_col + (r00 >> 5);
+        const int n = a.rows - r00 < kColWarps * 32 ? int(a.rows - r00) / 32 : kColWarps;
+        if (n == 4 && (reinterpret_cast<uintptr_t>(s) & 3u) == 0)
+            *reinterpret_cast<uint32_t*>(s) = *reinterpret_cast<const uint32_t*>(scales[threadIdx.x]);
+        else
+            for (int i = 0; i < n; ++i) s[i] = scales[threadIdx.x][i];
+    }
     for (int i = threadIdx.x; i < 64 * kColWarps * 2; i += kColWarps * 32) {
         const int col = i / (kColWarps * 2), chunk = i % (kColWarps * 2);
         const int64_t r = r00 + 16 * chunk;

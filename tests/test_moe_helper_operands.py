@@ -80,7 +80,7 @@ WRONG = {
              dict(out={"group_m": i32(E + 1)}), dict(out={"slot": i32(M, K)})],
     "dispatch": [dict(row=zeros(M, K, dtype=torch.int64)), dict(row=i32(M + 1, K)), dict(out=zeros(R, H + 1)), dict(out=f32(R, H)),
                  dict(scales=u8(M, 16)), dict(x=u8(M, H), scales=u8(M, 3)), dict(x=u8(M, H), scales=u8(M, 16), out=(u8(R, H), u8(R, 3))),
-                 dict(total_rows=R + 1, out=zeros(R, H)), dict(x=zeros(H, M).t())],
+                 dict(x=u8(M, H + 16), scales=u8(M, 16)), dict(total_rows=R + 1, out=zeros(R, H)), dict(x=zeros(H, M).t())],
     "combine": [dict(weight=zeros(M, K)), dict(weight=f32(M, K + 1)), dict(residual=zeros(M, H + 1)), dict(residual=f32(M, H)), dict(out=f32(M, H)),
                 dict(out=zeros(M + 1, H))],
     "combine_bwd": [dict(weight=None), dict(weight=zeros(M, K)), dict(dout=f32(M, H)), dict(dout=zeros(M + 1, H)), dict(out={"dy": x()}),

@@ -214,6 +214,36 @@ def test_repeats_in_a_graph_and_on_a_stream(tokens):
     assert all(torch.equal(a, b) for r in got for a, b in zip(want, r))
 
 
+def test_calls_on_two_streams_at_once():
+    # the whole way there and back, on two streams that overlap, each with inputs of its own
+    def step(seed, **kw):
+        index = choices(9000, 4, 96, seed, "skewed").cuda()
+        x, weight = matrix(9000, 512, "bf16", seed), torch.rand(9000, 4, generator=torch.Generator().manual_seed(seed)).cuda()
+        ga = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+
+        def run():
+            s = binding.moe_sort(index, 96)
+            n = binding.rmsnorm_quantize(x, ga, residual=x, dense=True)
+            d = binding.moe_dispatch(n["y"], s["row"])
+            b = binding.moe_combine_backward(x, d, s["row"], weight)
+            g = binding.rmsnorm_backward(binding.moe_combine(b["dy"], s["row"]), n["z"], ga, n["rsigma"], dz=x)
+            return s["row"], s["slot"], d, b["dweight"], g["dx"], g["dgamma"]
+        return run
+
+    runs = [step(1), step(2)]
+    want = [f() for f in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(6):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(runs[i]())
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(want[i], r))
+
+
 def test_gradient_of_dispatch_is_a_combine_without_weights():
     row, kept = rows_of(50, 3, 8, 4, "dropped")
     x, d = matrix(50, 96, "fp32", 1), matrix(150, 96, "fp32", 2)
