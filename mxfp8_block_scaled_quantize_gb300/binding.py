@@ -839,6 +839,11 @@ def _like(t, shape, dtype, device: int) -> bool:
     return t is None or (t.shape == shape and t.dtype == dtype and t.get_device() == device)
 
 
+def _vector(t, n: int, dtype, device: int) -> bool:
+    """Whether t, if given, is a contiguous vector of n elements of that type on that CUDA device."""
+    return t is None or (t.shape == (n,) and t.dtype == dtype and t.get_device() == device and t.is_contiguous())
+
+
 def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, stats: bool = True, stream=None, out=None):
     """RMSNorm over the last axis of a 2-D bf16, fp16 or fp32 CUDA tensor, of
     z = x + residual if one is given; gamma has its type or fp32.  Returns a dict
@@ -855,7 +860,7 @@ def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, stats: bool = True, stre
     o = {} if out is None else dict(out)
     if o:
         assert _like(o.get("y"), shape, dtype, device) and _like(o.get("z"), shape, dtype, device)
-        assert _vectors(o.get("rsigma"), None, rows, torch.float32, device)
+        assert _vector(o.get("rsigma"), rows, torch.float32, device)
     if "y" not in o:
         o["y"] = torch.empty_like(x, memory_format=torch.contiguous_format)
     res = ld_res = z = ld_z = rs = 0
@@ -905,7 +910,7 @@ def rmsnorm_quantize(x, gamma, eps: float = 1e-5, residual=None, rowwise: bool =
         assert q is None or (q.shape == (hidden, rows) and q.is_contiguous())
         assert _bytes(q, hidden, rows, device) and _bytes(o.get("s_col"), hidden, rows // 32, device)
         assert _like(o.get("y"), shape, bf16, device) and _like(o.get("z"), shape, bf16, device)
-        assert _vectors(o.get("rsigma"), None, rows, torch.float32, device)
+        assert _vector(o.get("rsigma"), rows, torch.float32, device)
     if rowwise:
         if "q_row" not in o:
             o["q_row"] = torch.empty(shape, dtype=u8, device=dev)
@@ -959,10 +964,10 @@ def rmsnorm_backward(dy, z, gamma, rsigma, dz=None, dparams: bool = True, stream
     device = z.get_device()
     assert device >= 0 and device == _current_device() and _like(dy, shape, dtype, device) and _like(dz, shape, dtype, device)
     assert gamma.shape == shape[1:] and gamma.is_contiguous() and gamma.get_device() == device
-    assert _vectors(rsigma, None, rows, torch.float32, device)
+    assert _vector(rsigma, rows, torch.float32, device)
     o = {} if out is None else dict(out)
     if o:
-        assert _like(o.get("dx"), shape, dtype, device) and _vectors(o.get("dgamma"), None, hidden, gamma.dtype, device)
+        assert _like(o.get("dx"), shape, dtype, device) and _vector(o.get("dgamma"), hidden, gamma.dtype, device)
     if "dx" not in o:
         o["dx"] = torch.empty_like(z, memory_format=torch.contiguous_format)
     if dparams and "dgamma" not in o:
@@ -1000,7 +1005,7 @@ def route(logits, k: int, scoring: str = "softmax", renormalise: bool = True, sc
     torch = _torch or _load_torch()
     tokens, experts = logits.shape
     device = logits.get_device()
-    assert device >= 0 and device == _current_device() and _vectors(bias, None, experts, torch.float32, device)
+    assert device >= 0 and device == _current_device() and _vector(bias, experts, torch.float32, device)
     o = {} if out is None else dict(out)
     if o:
         assert _matrix(o.get("index"), tokens, k, torch.int32, device)
@@ -1055,7 +1060,7 @@ def moe_sort(index, experts: int, stream=None, out=None):
     if o:
         r = o.get("row")
         assert r is None or (r.shape == index.shape and r.dtype == i32 and r.is_contiguous() and r.get_device() == device)
-        assert _vectors(o.get("group_m"), None, experts, i32, device) and _vectors(o.get("slot"), None, n, i32, device)
+        assert _vector(o.get("group_m"), experts, i32, device) and _vector(o.get("slot"), n, i32, device)
     if "group_m" not in o:
         o["group_m"] = torch.empty(experts, dtype=i32, device=index.device)
     if "row" not in o:

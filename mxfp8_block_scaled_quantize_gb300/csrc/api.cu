@@ -510,7 +510,7 @@ te_mx_status te_mx_rmsnorm(const void* x, int64_t rows, int64_t hidden, int64_t 
     if (!y) return set_error(TE_MX_ERR_INVALID_ARG, "y is NULL");
     RmsArgs a{x, rows, hidden, ld_x, dtype, param_dtype, residual, ld_residual, gamma, eps, z, ld_z, y, ld_y, rsigma,
               nullptr, nullptr, 0, nullptr, nullptr, 0};
-    if ((st = validate_rms(a)) != TE_MX_OK || (st = check_device(nullptr)) != TE_MX_OK) return st;
+    if ((st = validate_rms(a)) != TE_MX_OK) return st;
     return rms_forward_launch(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -583,7 +583,6 @@ te_mx_status te_mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* z
     } else if (!dgamma) {
         return TE_MX_OK;
     }
-    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
     RmsBackwardArgs a{dy, ld_dy, z, rows, hidden, ld_z, dtype, param_dtype, gamma, rsigma, dz, ld_dz, dx, ld_dx, dgamma,
                       static_cast<float*>(workspace)};
     return rms_backward_launch(a, static_cast<cudaStream_t>(stream));
@@ -650,8 +649,6 @@ te_mx_status te_mx_moe_sort(const int32_t* index, int64_t slots, int32_t experts
     if (!apart_or_same(row, 1, b, index, 1, b, b, false) || !apart_or_same(slot, 1, b, index, 1, b, b, false) ||
         !apart_or_same(row, 1, b, slot, 1, b, b, false))
         return set_error(TE_MX_ERR_INVALID_ARG, "index, row and slot overlap");
-    te_mx_status st = check_device(nullptr);
-    if (st != TE_MX_OK) return st;
     return moe_sort_launch(index, slots, experts, group_m, row, slot, static_cast<cudaStream_t>(stream));
 }
 
@@ -686,7 +683,6 @@ te_mx_status te_mx_moe_dispatch(const void* x, int64_t ld_x, int64_t row_bytes, 
     if (!apart_or_same(out, total_rows, ld_out, x, tokens, ld_x, row_bytes, false)) return overlap_error("out", "x");
     if (scales && !apart_or_same(out_scales, total_rows, ld_out_scales, scales, tokens, ld_scales, scale_bytes, false))
         return overlap_error("out_scales", "scales");
-    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
     DispatchArgs a{static_cast<const uint8_t*>(x), ld_x, row_bytes, scales, ld_scales, scale_bytes, row, tokens, total_rows, k,
                    static_cast<uint8_t*>(out), ld_out, out_scales, ld_out_scales};
     return moe_dispatch_launch(a, static_cast<cudaStream_t>(stream));
@@ -720,7 +716,6 @@ te_mx_status te_mx_moe_combine(const void* y, int64_t ld_y, int64_t total_rows, 
     if ((st = validate_ln_matrix(out, ld_out, hidden, dtype, "out")) != TE_MX_OK) return st;
     if (!apart_or_same(out, tokens, ld_out * b, y, total_rows, ld_y * b, w, false)) return overlap_error("out", "y");
     if (!apart_or_same(out, tokens, ld_out * b, residual, tokens, ld_residual * b, w, true)) return overlap_error("out", "residual");
-    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
     return moe_combine_launch(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -743,7 +738,6 @@ te_mx_status te_mx_moe_combine_backward(const void* dout, int64_t ld_dout, const
         if (!apart_or_same(dy, total_rows, ld_dy * b, a.y, total_rows, ld_y * b, w, true)) return overlap_error("dy", "y");
         if (!apart_or_same(dy, total_rows, ld_dy * b, dout, tokens, ld_dout * b, w, false)) return overlap_error("dy", "dout");
     }
-    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
     return moe_combine_backward_launch(a, static_cast<cudaStream_t>(stream));
 }
 
