@@ -715,9 +715,10 @@ te_mx_status route_backward_launch(const RouteArgs& a, cudaStream_t stream) { re
 // those are faster (16384: 7.2, 7.4; 32768: 8.7, 8.0; 131072: 15.8, 11.3).
 constexpr int64_t kSortAlone = 2048, kSortEight = 16384;
 
-// Whether the device launches the kernel in clusters of 16 blocks; looked up once per
-// kernel and device, and the attribute for it set then.
-static bool wide_clusters(const void* kern, int which, const cudaLaunchConfig_t& cfg) {
+// Whether the device launches the kernel in clusters of 16 blocks, with the shared memory
+// of the most experts that it takes; looked up once per kernel and device, and the
+// attribute for it set then.
+static bool wide_clusters(const void* kern, int which, cudaLaunchConfig_t cfg) {
     static std::mutex mu;
     static int8_t known[5][64];                            // 0: not looked up, 1: yes, -1: no
     int dev = 0;
@@ -726,6 +727,7 @@ static bool wide_clusters(const void* kern, int which, const cudaLaunchConfig_t&
     int8_t& k = known[which][dev];
     if (k == 0) {
         int n = 0;
+        cfg.dynamicSmemBytes = size_t(kSortBlockSlots + kSortWarps * (which == 4 ? kMaxExperts : 32 << which)) * 4;
         const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
                         cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
         if (!ok) (void)cudaGetLastError();
