@@ -340,7 +340,8 @@ TEMX_API te_mx_status te_mx_rmsnorm_quantize(const void* x, int64_t rows, int64_
  *           path, or NULL (zero);
  *   dx      [rows x hidden], pitch ld_dx, or NULL (not computed); may be dy, z or dz
  *           (the same pointer and pitch); other overlaps are refused;
- *   dgamma  [hidden] of `param_dtype`, or NULL.  With rows == 0 it is set to zero;
+ *   dgamma  [hidden] of `param_dtype`, or NULL; may not overlap gamma.  With rows == 0 it
+ *           is set to zero;
  *   workspace  device scratch of te_mx_rmsnorm_backward_workspace_size(rows, hidden)
  *           bytes, 16-byte aligned, for dgamma (else NULL); its contents on entry do
  *           not matter and it is clobbered.
@@ -368,8 +369,9 @@ typedef enum te_mx_scoring { TE_MX_SCORE_SOFTMAX = 0, TE_MX_SCORE_SIGMOID = 1 } 
  *   index   int32 [tokens x k];  weight  fp32 [tokens x k].
  * An expert masked with -inf has the score 0, and is chosen only after all others;
  * where the scores to divide by sum to 0 the weights are 0.  A NaN logit is chosen
- * last, and NaN or +inf logits give weights as the formula does.  The k indices of a
- * token always differ.  Rules: 1 <= k <= 32, k <= experts <= 1024, tokens * k < 2^31;
+ * last, and NaN or +inf logits give weights as the formula does, but with renormalise =
+ * 1 only those of the chosen count (the others' sum cancels).  The k indices of a token
+ * always differ.  Rules: 1 <= k <= 32, k <= experts <= 1024, tokens * k < 2^31;
  * pointers aligned to their elements; scale finite; tokens == 0 is a no-op. */
 TEMX_API te_mx_status te_mx_route(const void* logits, int64_t tokens, int32_t experts, int64_t ld_logits, int32_t dtype,
                                   const float* bias, int32_t k, int32_t scoring, int32_t renormalise, float scale,
@@ -414,7 +416,8 @@ TEMX_API te_mx_status te_mx_moe_sort(const int32_t* index, int64_t slots, int32_
  * written.  A row >= total_rows is skipped and makes te_mx_device_status() report
  * TE_MX_ERR_INVALID_ARG.  Any alignment (rows on 16-byte boundaries are copied 16
  * bytes at a time).  Its gradient is te_mx_moe_combine without weights.  Rules:
- * 1 <= k <= 32; tokens * k < 2^31; tokens * row_bytes <= 2^39; out does not overlap x. */
+ * 1 <= k <= 32; tokens * k < 2^31; tokens * row_bytes <= 2^39; out does not overlap x,
+ * nor out_scales scales; tokens == 0 or row_bytes == 0 is a no-op. */
 TEMX_API te_mx_status te_mx_moe_dispatch(const void* x, int64_t ld_x, int64_t row_bytes, const uint8_t* scales,
                                          int64_t ld_scales, int64_t scale_bytes, const int32_t* row, int64_t tokens,
                                          int32_t k, int64_t total_rows, void* out, int64_t ld_out, uint8_t* out_scales,

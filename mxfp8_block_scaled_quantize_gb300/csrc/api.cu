@@ -579,6 +579,8 @@ te_mx_status te_mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* z
                 return set_error(TE_MX_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0),
                                  te_mx_rmsnorm_backward_workspace_size(rows, hidden));
             if (!aligned(workspace, 16)) return set_error(TE_MX_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+            const int64_t pw = hidden * element_bytes(param_dtype);    // (blocks write dgamma while others read gamma)
+            if (!apart_or_same(dgamma, 1, pw, gamma, 1, pw, pw, false)) return overlap_error("dgamma", "gamma");
         }
     } else if (!dgamma) {
         return TE_MX_OK;
@@ -645,10 +647,14 @@ te_mx_status te_mx_moe_sort(const int32_t* index, int64_t slots, int32_t experts
         return set_error(TE_MX_ERR_INVALID_ARG, "index, group_m, row and slot are required");
     if (!aligned(index, 4) || !aligned(group_m, 4) || !aligned(row, 4) || !aligned(slot, 4))
         return set_error(TE_MX_ERR_MISALIGNED, "index, group_m, row or slot is not aligned to its elements");
-    const int64_t b = 4 * slots;
-    if (!apart_or_same(row, 1, b, index, 1, b, b, false) || !apart_or_same(slot, 1, b, index, 1, b, b, false) ||
-        !apart_or_same(row, 1, b, slot, 1, b, b, false))
-        return set_error(TE_MX_ERR_INVALID_ARG, "index, row and slot overlap");
+    const void* arrays[4] = {index, row, slot, group_m};
+    const int64_t sizes[4] = {4 * slots, 4 * slots, 4 * slots, 4 * int64_t(experts)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(arrays[i]), q = reinterpret_cast<uintptr_t>(arrays[j]);
+            if (slots > 0 && p < q + uintptr_t(sizes[j]) && q < p + uintptr_t(sizes[i]))
+                return set_error(TE_MX_ERR_INVALID_ARG, "index, group_m, row and slot overlap");
+        }
     return moe_sort_launch(index, slots, experts, group_m, row, slot, static_cast<cudaStream_t>(stream));
 }
 
@@ -728,7 +734,8 @@ te_mx_status te_mx_moe_combine_backward(const void* dout, int64_t ld_dout, const
                   dout, ld_dout, dy, ld_dy, dweight};
     te_mx_status st = validate_combine(a);
     if (st != TE_MX_OK || tokens == 0 || hidden == 0) return st;
-    if (!dy && !dweight) return set_error(TE_MX_ERR_INVALID_ARG, "dy and dweight are both NULL");
+    // (dy of no rows has no address)
+    if (!dy && !dweight && total_rows > 0) return set_error(TE_MX_ERR_INVALID_ARG, "dy and dweight are both NULL");
     if (!weight) return set_error(TE_MX_ERR_INVALID_ARG, "weight is NULL");
     const int64_t b = element_bytes(dtype), w = hidden * b;
     if ((st = validate_ln_matrix(dout, ld_dout, hidden, dtype, "dout")) != TE_MX_OK) return st;

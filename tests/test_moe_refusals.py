@@ -69,6 +69,7 @@ REFUSED = [
     ("rms_bwd", dict(dgamma=B[6] + 1), ALIGN), ("rms_bwd", dict(workspace=0), SPACE), ("rms_bwd", dict(workspace_bytes=100), SPACE),
     ("rms_bwd", dict(workspace=B[7] + 8), ALIGN), ("rms_bwd", dict(rows=1 << 31), SHAPE), ("rms_bwd", dict(dx=B[0] + 2), ARG),
     ("rms_bwd", dict(dx=B[1], ld_dx=80), ARG), ("rms_bwd", dict(dx=B[4] + 128), ARG),
+    ("rms_bwd", dict(dgamma=B[2]), ARG), ("rms_bwd", dict(dgamma=B[2] + 126, dx=0), ARG),
     ("route", dict(tokens=-1), ARG), ("route", dict(dtype=3), ARG), ("route", dict(scoring=2), ARG), ("route", dict(renormalise=2), ARG),
     ("route", dict(scale=INF), ARG), ("route", dict(scale=NAN), ARG), ("route", dict(k=0), SHAPE), ("route", dict(k=33, experts=64, ld_logits=64), SHAPE),
     ("route", dict(k=9), SHAPE), ("route", dict(experts=1025, ld_logits=1025), SHAPE), ("route", dict(tokens=1 << 30), SHAPE),
@@ -79,6 +80,7 @@ REFUSED = [
     ("sort", dict(slots=-1), ARG), ("sort", dict(slots=1 << 31), SHAPE), ("sort", dict(experts=0), SHAPE), ("sort", dict(experts=1025), SHAPE),
     ("sort", dict(group_m=0), ARG), ("sort", dict(index=0), ARG), ("sort", dict(row=0), ARG), ("sort", dict(slot=0), ARG),
     ("sort", dict(row=B[2] + 2), ALIGN), ("sort", dict(row=B[0]), ARG), ("sort", dict(slot=B[2] + 8), ARG),
+    ("sort", dict(group_m=B[0] + 396), ARG), ("sort", dict(group_m=B[2] - 28), ARG), ("sort", dict(group_m=B[3]), ARG),
     ("dispatch", dict(tokens=-1), ARG), ("dispatch", dict(total_rows=-1), ARG), ("dispatch", dict(row_bytes=-1), ARG), ("dispatch", dict(k=0), SHAPE),
     ("dispatch", dict(k=33), SHAPE), ("dispatch", dict(tokens=1 << 30), SHAPE), ("dispatch", dict(total_rows=1 << 31), SHAPE),
     ("dispatch", dict(row_bytes=1 << 38, ld_x=1 << 38, ld_out=1 << 38), SHAPE), ("dispatch", dict(scales=0), ARG),
@@ -126,7 +128,8 @@ def reaches_the_device(op, change):
     ("route_bwd", {}), ("sort", {}), ("sort", dict(slots=0)), ("dispatch", {}), ("dispatch", dict(scales=0, out_scales=0)),
     ("dispatch", dict(total_rows=0, out=0)), ("combine", {}), ("combine", dict(weight=0, residual=0)), ("combine", dict(out=B[3])),
     ("combine", dict(total_rows=0, y=0)), ("combine_bwd", {}), ("combine_bwd", dict(dy=B[1])), ("combine_bwd", dict(dy=0)),
-    ("combine_bwd", dict(dweight=0, y=0)),
+    ("combine_bwd", dict(dweight=0, y=0)), ("combine_bwd", dict(total_rows=0, y=0, dy=0, dweight=0)),
+    ("sort", dict(group_m=B[2] - 32)), ("rms_bwd", dict(dgamma=B[2] + 128)),
 ])
 def test_accepted(op, change):
     reaches_the_device(op, change)

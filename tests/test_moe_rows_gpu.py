@@ -294,3 +294,17 @@ def test_around_the_grouped_gemms():
             size[t] += np.abs(v) + 1e-5 * weight[t, j] * (np.abs(wo[e * hidden:(e + 1) * hidden]) @ np.abs(hv[r]))
     # each expert's row is rounded to bf16 once, the sum once
     assert np.all(np.abs(f64(out) - want) <= 2.0 ** -7 * size + 1e-3 * 2.0 ** -7)
+
+
+def test_no_rows_at_all():
+    # every choice dropped: the experts' rows are empty
+    row = torch.full((5, 3), -1, dtype=torch.int32, device="cuda")
+    y, weight = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(5, 3, device="cuda")
+    x = matrix(5, 64, "bf16", 1)
+    assert binding.moe_dispatch(x, row, total_rows=0).shape == (0, 64)
+    assert torch.equal(binding.moe_combine(y, row, weight=weight, residual=x), x)
+    assert torch.all(binding.moe_combine(y, row) == 0)
+    for dweight in (False, True):
+        o = binding.moe_combine_backward(x, y, row, weight, dweight=dweight)
+        assert o["dy"].shape == (0, 64) and torch.all(o["dweight"] == 0) if dweight else "dweight" not in o
+    binding.te_mx_device_status()
