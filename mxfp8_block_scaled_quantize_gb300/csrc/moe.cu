@@ -469,9 +469,10 @@ moe_dispatch_kernel(const DispatchArgs a, int parts, unsigned int* status) {
 // flight are what it lives on, so few choices take more pieces.  16384 x 8 x 4096 bf16
 // with a residual: 200 us (floor 198; a block of 256 threads per token and part, one
 // vector per thread, 231); 4096 x 2 x 2048 15.5 (9.9; 20); 4096 x 4 x 2047 27 (15; 87).
-constexpr int kCombineThreads = 256;             // at most
+constexpr int kCombineThreads = 128;             // at most
+constexpr int kCombineWarps = 24;                // of an SM, resident
 template <typename T, bool kVec, int kN, int kJ>
-__global__ void __launch_bounds__(kCombineThreads, 3)
+__global__ void __launch_bounds__(kCombineThreads, kCombineWarps * 32 / kCombineThreads)
 moe_combine_kernel(const CombineArgs a, unsigned int* status) {
     using V = Vec<T>;
     using Piece = typename std::conditional<kVec, uint4, T>::type;
@@ -672,8 +673,16 @@ cudaError_t dispatch_launch(const DispatchArgs& a, unsigned int* status, cudaStr
 template <typename T, bool kVec, int kN, int kJ>
 cudaError_t combine_launch(const CombineArgs& a, int sms, unsigned int* status, cudaStream_t stream) {
     const int64_t pieces = kVec ? a.hidden / Vec<T>::kN : a.hidden, parts = (pieces + 32 * kN - 1) / (32 * kN);
-    const int warps = int(parts < kCombineThreads / 32 ? parts : kCombineThreads / 32);
-    const int64_t rows_of_blocks = (parts + warps - 1) / warps, most = (int64_t(sms) * 24 / warps + rows_of_blocks - 1) / rows_of_blocks;
+    // All blocks resident (a second wave of persistent blocks would take as long as the
+    // first); a block is one warp, so that every warp has a part whatever their number, or up
+    // to four where all the work is resident at once (64 x 8 x 7168 bf16: 2.6 us, 2.8 with
+    // one; 9044 x 6 x 2816 59.8, 57.4; 8192 x 2 x 5120 62.5, 60.0) or the parts are so many
+    // that a few warps without one do not count (a grid has 65535 rows of blocks at most)
+    const int64_t resident = int64_t(sms) * kCombineWarps;
+    const int64_t most_warps = a.tokens * parts <= resident || parts > 1024 ? kCombineThreads / 32 : 1;
+    const int64_t rows_of_blocks = (parts + most_warps - 1) / most_warps;
+    const int warps = int((parts + rows_of_blocks - 1) / rows_of_blocks);
+    const int64_t most = resident / warps > rows_of_blocks ? resident / warps / rows_of_blocks : 1;
     return launch_dependent(moe_combine_kernel<T, kVec, kN, kJ>, dim3(unsigned(a.tokens < most ? a.tokens : most), unsigned(rows_of_blocks)),
                             dim3(unsigned(32 * warps)), stream, a, status);
 }

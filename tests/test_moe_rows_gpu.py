@@ -308,3 +308,15 @@ def test_no_rows_at_all():
         o = binding.moe_combine_backward(x, y, row, weight, dweight=dweight)
         assert o["dy"].shape == (0, 64) and torch.all(o["dweight"] == 0) if dweight else "dweight" not in o
     binding.te_mx_device_status()
+
+
+@pytest.mark.parametrize("k", [1, 5])
+@pytest.mark.parametrize("hidden", [1 << 24, (1 << 24) - 1])
+def test_the_longest_rows(k, hidden):
+    # one choice of each token has a row, so the sum is that row
+    y = torch.randn(3, hidden, device="cuda")
+    row = torch.full((2, k), -1, dtype=torch.int32, device="cuda")
+    row[0, k // 2], row[1, 0] = 2, 1
+    out = binding.moe_combine(y, row)
+    assert torch.equal(out[0], y[2]) and torch.equal(out[1], y[1])
+    binding.te_mx_device_status()
