@@ -407,7 +407,8 @@ rms_backward_any_kernel(const RmsBackwardArgs a) {
 }
 
 // Longer rows: a block per row for dx, which reads dy and z twice, and a pass for the
-// columns' sums.
+// columns' sums.  Loads of single elements, several in flight, bound them: 1749 x 12998 fp32
+// with dz 112 us (floor 54; a load at a time 156), 3000 x 20001 bf16 190 (53; 278).
 template <typename T, typename P>
 __global__ void __launch_bounds__(kAnyThreads)
 rms_backward_dx_kernel(const RmsBackwardArgs a) {
@@ -420,43 +421,63 @@ rms_backward_dx_kernel(const RmsBackwardArgs a) {
     const T* dz = a.dz ? static_cast<const T*>(a.dz) + row * a.ld_dz : nullptr;
     T* dx = static_cast<T*>(a.dx) + row * a.ld_dx;
     const float rs = a.rsigma[row];
-    const float s = long_sum(a.hidden, [&](int64_t i) {
-        return to_f32(dy[i]) * load_param<P>(a.gamma, i) * (to_f32(z[i]) * rs);
-    });
+    T d[kLongAhead], zs[kLongAhead], add[kLongAhead];
+    float ga[kLongAhead];
+    auto load = [&](int q, int64_t i) {
+        d[q] = dy[i];
+        zs[q] = z[i];
+        ga[q] = load_param<P>(a.gamma, i);
+    };
+    const float s = long_sum(a.hidden, load, [&](int q, int64_t) { return to_f32(d[q]) * ga[q] * (to_f32(zs[q]) * rs); });
     const float c = across_warps(warp_sum(s), part, kAnyThreads / 32, threadIdx.x >> 5, threadIdx.x & 31) / float(a.hidden);
-    for (int64_t i = threadIdx.x; i < a.hidden; i += kAnyThreads) {
-        float o = rs * (to_f32(dy[i]) * load_param<P>(a.gamma, i) - to_f32(z[i]) * rs * c);
-        if (dz) o += to_f32(dz[i]);
-        dx[i] = from_f32<T>(o);
-    }
+    for (int64_t i = threadIdx.x; i < a.hidden; i += kLongAhead * kAnyThreads)
+        long_batch(i, a.hidden, [&](int q, int64_t at) {
+            load(q, at);
+            if (dz) add[q] = dz[at];
+        }, [&](int q, int64_t at) {
+            float o = rs * (to_f32(d[q]) * ga[q] - to_f32(zs[q]) * rs * c);
+            if (dz) o += to_f32(add[q]);
+            dx[at] = from_f32<T>(o);
+        });
 }
 
 // Partial sums of dy xh over the rows blockIdx.y, blockIdx.y + parts, ...; a thread
-// owns one column.
-constexpr int kColThreads = 256;
+// owns kColsEach columns, kColThreads apart.
+constexpr int kColThreads = 256, kColsEach = 2;
 template <typename T>
 __global__ void __launch_bounds__(kColThreads)
 rms_backward_gamma_kernel(const RmsBackwardArgs a, int parts) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t c = int64_t(blockIdx.x) * kColThreads + threadIdx.x;
-    if (c >= a.hidden) return;
+    const int64_t c = int64_t(blockIdx.x) * (kColThreads * kColsEach) + threadIdx.x;
     const T* z = static_cast<const T*>(a.z) + c;
     const T* dy = static_cast<const T*>(a.dy) + c;
-    float s = 0.0f;
-    for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += 4 * int64_t(parts)) {         // four rows in flight
-        float d[4], xh[4];
+    float s[kColsEach];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+    for (int e = 0; e < kColsEach; ++e) s[e] = 0.0f;
+    constexpr int kAhead = 4;                              // rows in flight
+    for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += kAhead * int64_t(parts)) {
+        T d[kAhead][kColsEach], v[kAhead][kColsEach];
+        float rs[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
             const int64_t r = r0 + k * int64_t(parts);
-            const bool live = r < a.rows;
-            d[k] = live ? to_f32(dy[r * a.ld_dy]) : 0.0f;
-            xh[k] = live ? to_f32(z[r * a.ld_z]) * a.rsigma[r] : 0.0f;
+            rs[k] = r < a.rows ? a.rsigma[r] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < kColsEach; ++e) {
+                const bool live = r < a.rows && c + e * kColThreads < a.hidden;
+                d[k][e] = live ? dy[r * a.ld_dy + e * kColThreads] : from_f32<T>(0.0f);
+                v[k][e] = live ? z[r * a.ld_z + e * kColThreads] : from_f32<T>(0.0f);
+            }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s = fmaf(d[k], xh[k], s);
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int e = 0; e < kColsEach; ++e) s[e] = fmaf(to_f32(d[k][e]), to_f32(v[k][e]) * rs[k], s[e]);
     }
-    a.partial[int64_t(blockIdx.y) * a.hidden + c] = s;
+#pragma unroll
+    for (int e = 0; e < kColsEach; ++e)
+        if (c + e * kColThreads < a.hidden) a.partial[int64_t(blockIdx.y) * a.hidden + c + e * kColThreads] = s[e];
 }
 
 // dgamma from `parts` partial sums per column.  A block owns 32 columns (lane =
@@ -627,10 +648,13 @@ cudaError_t backward(const RmsBackwardArgs& a, int sms, unsigned int* status, cu
         if (e != cudaSuccess || !a.dgamma) return e;
         return launch_dependent(rms_backward_reduce_kernel, reduce_grid, dim3(kReduceWarps * 32), stream, a, n);
     }
+    const unsigned cols = unsigned((a.hidden + kColThreads * kColsEach - 1) / (kColThreads * kColsEach));
     n = rms_backward_parts(a.rows);
+    // (blocks for the whole GPU twice over; with as many parts as the workspace holds the
+    // partial sums themselves, of 3000 x 20001, cost 20 us)
+    if (n > 1 + 16 * sms / int(cols)) n = 1 + 16 * sms / int(cols);
     // (the columns' sums first: dx may overwrite dy or z)
     if (a.dgamma && n > 0) {
-        const unsigned cols = unsigned((a.hidden + kColThreads - 1) / kColThreads);
         e = launch_dependent(rms_backward_gamma_kernel<T>, dim3(cols, unsigned(n)), dim3(kColThreads), stream, a, n);
         if (e != cudaSuccess) return e;
     }

@@ -177,16 +177,30 @@ __device__ __forceinline__ float across_warps(float v, float* part, int warps, i
 // before is unpacked again rather than kept in registers.
 __device__ __forceinline__ void unpack_again(uint4& w) { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)); }
 
-// A thread's sum of term(i) over i = t, t + kAnyThreads, ... in a block of kAnyThreads:
-// up to 32768 terms (rows of 2^24 elements), 64 to a batch, the batches added 64 to a
-// batch of batches, so that a chain has at most 64 + 64 + 8 additions.
+// What a thread takes of a long row, i = t, t + kAnyThreads, ... in a block of
+// kAnyThreads, kLongAhead elements at a time: all loaded, load(q, i), before the first is
+// used, use(q, i), which may write (the compiler moves no load past such a write).
 constexpr int kAnyThreads = 512;                 // of the kernels for rows in any layout
-template <typename F> __device__ __forceinline__ float long_sum(int64_t hidden, F&& term) {
+constexpr int kLongAhead = 8;
+template <typename L, typename U>
+__device__ __forceinline__ void long_batch(int64_t i, int64_t hidden, L&& load, U&& use) {
+#pragma unroll
+    for (int q = 0; q < kLongAhead; ++q)
+        if (i + q * kAnyThreads < hidden) load(q, i + q * kAnyThreads);
+#pragma unroll
+    for (int q = 0; q < kLongAhead; ++q)
+        if (i + q * kAnyThreads < hidden) use(q, i + q * kAnyThreads);
+}
+// A thread's sum of the terms that use() returns: up to 32768 of them (rows of 2^24
+// elements), 64 to a batch, the batches added 64 to a batch of batches, so that a chain has
+// at most 64 + 64 + 8 additions.
+template <typename L, typename U> __device__ __forceinline__ float long_sum(int64_t hidden, L&& load, U&& use) {
     float total = 0.0f, outer = 0.0f;
     int batches = 0;
     for (int64_t i = threadIdx.x; i < hidden;) {
         float batch = 0.0f;
-        for (int k = 0; k < 64 && i < hidden; ++k, i += kAnyThreads) batch += term(i);
+        for (int k = 0; k < 64 && i < hidden; k += kLongAhead, i += kLongAhead * kAnyThreads)
+            long_batch(i, hidden, load, [&](int q, int64_t at) { batch += use(q, at); });
         outer += batch;
         if (++batches == 64) {
             total += outer;
