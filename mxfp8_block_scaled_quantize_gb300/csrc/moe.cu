@@ -27,6 +27,9 @@ namespace {
 // a bias: kPacked) shares a word with its index, so that one maximum over the warp
 // gives both, and the chosen logits are read again at the end (16384 x 128 bf16, k = 8,
 // both directions: 12.0 us; with two maxima over the warp and a shuffle per choice 16.2).
+// For enough choices a lane first sorts its words: a round then looks at one of them (11.3
+// us; 16384 x 256, forward: 10.1, 11.4).  Keys of 32 bits with their index are pairs, and
+// sorted as such were slower (16384 x 256 fp32, k = 4: 12.6, 11.0).
 constexpr int kRouteWarps = 8;
 
 __device__ __forceinline__ uint32_t ordered_key(float v) {
@@ -71,6 +74,21 @@ template <typename T> __device__ __forceinline__ uint32_t ordered_key16(float v)
     return (b & 0x8000u) ? ~b & 0xFFFFu : b | 0x8000u;
 }
 
+// A lane's keys in falling order (Batcher's merge exchange; kN a power of two).
+template <int kN> __device__ __forceinline__ void sort_falling(uint32_t (&key)[kN]) {
+#pragma unroll
+    for (int p = 1; p < kN; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int i = 0; i + k < kN; ++i)
+                if (i >= k % p && (i - k % p) / k % 2 == 0 && i / (2 * p) == (i + k) / (2 * p)) {
+                    const uint32_t x = key[i], y = key[i + k];
+                    key[i] = max(x, y);
+                    key[i + k] = min(x, y);
+                }
+}
+
 template <typename T, int kN, bool kPacked>
 __global__ void __launch_bounds__(kRouteWarps * 32)
 route_kernel(const RouteArgs a) {
@@ -90,27 +108,38 @@ route_kernel(const RouteArgs a) {
         if (e >= a.experts) key[i] = 0u;
     }
     int mine = 0;                                          // lane j: the j-th choice
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
+    if (kPacked && kN <= 16 && a.k >= kN / 2) {            // (sorted once, a lane's largest key is its first)
+        sort_falling(key);
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key[0]);
+            const bool won = key[0] == top;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) best = max(best, key[i]);
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-        uint32_t e;
-        if constexpr (kPacked) {
-            e = 0xFFFFu - (top & 0xFFFFu);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) key[i] = key[i] == top ? 0u : key[i];
-        } else {
-            uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-            for (int i = kN - 1; i >= 0; --i)
-                if (key[i] == top) at = uint32_t(lane + 32 * i);
-            e = __reduce_min_sync(0xFFFFFFFFu, at);
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-                if (e == uint32_t(lane + 32 * i)) key[i] = 0u;
+            for (int i = 0; i < kN; ++i) key[i] = !won ? key[i] : i + 1 < kN ? key[i + 1] : 0u;
+            if (lane == j) mine = int(0xFFFFu - (top & 0xFFFFu));
         }
-        if (lane == j) mine = int(e);
+    } else {
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) best = max(best, key[i]);
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+            uint32_t e;
+            if constexpr (kPacked) {
+                e = 0xFFFFu - (top & 0xFFFFu);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) key[i] = key[i] == top ? 0u : key[i];
+            } else {
+                uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+                for (int i = kN - 1; i >= 0; --i)
+                    if (key[i] == top) at = uint32_t(lane + 32 * i);
+                e = __reduce_min_sync(0xFFFFFFFFu, at);
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    if (e == uint32_t(lane + 32 * i)) key[i] = 0u;
+            }
+            if (lane == j) mine = int(e);
+        }
     }
     const float logit = lane < a.k ? to_f32((static_cast<const T*>(a.logits) + token * a.ld_logits)[mine]) : -INFINITY;
     const bool chosen = lane < a.k;
