@@ -368,7 +368,8 @@ typedef enum te_mx_scoring { TE_MX_SCORE_SOFTMAX = 0, TE_MX_SCORE_SIGMOID = 1 } 
  *   bias    fp32 [experts] or NULL;
  *   index   int32 [tokens x k];  weight  fp32 [tokens x k].
  * An expert masked with -inf has the score 0, and is chosen only after all others;
- * where the scores to divide by sum to 0 the weights are 0.  A NaN logit is chosen
+ * where all chosen are masked so, and renormalise = 1, the weights are 0 (of finite
+ * logits they are the scores' shares, however small the scores).  A NaN logit is chosen
  * last, and NaN or +inf logits give weights as the formula does, but with renormalise =
  * 1 only those of the chosen count (the others' sum cancels).  The k indices of a token
  * always differ.  Rules: 1 <= k <= 32, k <= experts <= 1024, tokens * k < 2^31;

@@ -66,6 +66,22 @@ __device__ __forceinline__ void softmax_sum(const float (&l)[kN], float& most, f
     sum = warp_sum(s);
 }
 
+// A chosen logit's share of the logistic scores of the chosen (-inf in lanes without a
+// choice); 0 where all are -inf.  A sum below 1/2 says that every chosen logit is
+// negative: the scores, which vanish below -88, are then taken relative to e^top with top
+// the largest of them, s e^-top = 1 / (e^top + e^(top - v)), the factor cancels, and the
+// largest is at least 1/2.  (A score that vanishes beside a sum of 1/2 or more is a share
+// below 2^-125.)
+__device__ __forceinline__ float logistic_share(float logit) {
+    float s = logistic(logit), sum = warp_sum(s);
+    if (sum < 0.5f) {
+        const float top = warp_max(logit);
+        s = logit == -INFINITY ? 0.0f : 1.0f / (expf(top) + expf(top - logit));
+        sum = warp_sum(s);
+    }
+    return sum == 0.0f ? 0.0f : s / sum;
+}
+
 // The bits of a 16-bit float in the order of the numbers, NaN last (1), -0 as 0.
 template <typename T> __device__ __forceinline__ uint32_t ordered_key16(float v) {
     if (v != v) return 1u;
@@ -157,11 +173,7 @@ route_kernel(const RouteArgs a) {
         }
         w = sum == 0.0f ? 0.0f : w / sum;
     } else {
-        w = chosen ? logistic(logit) : 0.0f;
-        if (a.renormalise) {
-            const float sum = warp_sum(w);
-            w = sum == 0.0f ? 0.0f : w / sum;
-        }
+        w = a.renormalise ? logistic_share(logit) : logistic(logit);
     }
     if (chosen) {
         a.index[token * a.k + lane] = mine;
@@ -217,13 +229,12 @@ route_backward_kernel(const RouteArgs a) {
             for (int i = 0; i < kN; ++i) d[i] = l[i] == -INFINITY ? 0.0f : -total * (expf(l[i] - most) * inv);
         }
     } else {
-        const float s = e < 0 ? 0.0f : logistic(logit), rest = logistic(-logit);
+        const float rest = logistic(-logit);
         if (a.renormalise) {
-            const float sum = warp_sum(s), w = sum == 0.0f ? 0.0f : s / sum;
-            const float total = warp_sum(w * g);
+            const float w = logistic_share(logit), total = warp_sum(w * g);
             mine = e < 0 ? 0.0f : w * rest * (g - total);
         } else {
-            mine = e < 0 ? 0.0f : s * rest * g;
+            mine = e < 0 ? 0.0f : logistic(logit) * rest * g;
         }
     }
     // the whole row, then the chosen experts' over it (the warp's stores in order)

@@ -95,12 +95,27 @@ def scores(logits, scoring):
         return np.where(s == 0, 0.0, p / np.where(s == 0, 1.0, s))
 
 
+def chosen_shares(logits, index, scoring):
+    """The chosen experts' shares of the sum of their scores, which are taken relative to
+    e^top (top the largest of the chosen logits, of logistic scores where it is negative):
+    the factor cancels, and no sum underflows.  0 for an index outside the experts, and where
+    all chosen logits are -inf."""
+    x = np.asarray(logits, np.float64)
+    live = (index >= 0) & (index < x.shape[1])
+    v = np.where(live, np.take_along_axis(x, np.where(live, index, 0).astype(np.int64), axis=1), -np.inf)
+    top = v.max(axis=1, keepdims=True)
+    top = np.where(top == -np.inf, 0.0, np.minimum(top, 0.0) if scoring == "sigmoid" else top)
+    with np.errstate(over="ignore", invalid="ignore"):
+        p = np.exp(v - top) if scoring == "softmax" else 1 / (np.exp(top) + np.exp(top - v))
+    p = np.where(v == -np.inf, 0.0, p)
+    s = p.sum(axis=1, keepdims=True)
+    return np.where(s == 0, 0.0, p / np.where(s == 0, 1.0, s))
+
+
 def route_weights(logits, index, scoring, renormalise, scale):
-    p = np.take_along_axis(scores(logits, scoring), index.astype(np.int64), axis=1)
     if renormalise:
-        s = p.sum(axis=1, keepdims=True)
-        p = np.where(s == 0, 0.0, p / np.where(s == 0, 1.0, s))
-    return scale * p
+        return scale * chosen_shares(logits, index, scoring)
+    return scale * np.take_along_axis(scores(logits, scoring), index.astype(np.int64), axis=1)
 
 
 def score_error(logits, scoring):
@@ -114,33 +129,46 @@ def score_error(logits, scoring):
     return MORE * FP32_U * 2 * (a + 4 + 37 + 3 + 5)
 
 
+def weight_error(logits, index, scoring, renormalise):
+    """Relative error of a weight, per row: that of a score; shares of logistic scores have a
+    difference in the exponent too (its rounding times its size) where the chosen logits are
+    all negative."""
+    e = score_error(logits, scoring)
+    if scoring == "sigmoid" and renormalise:
+        x = np.asarray(logits, np.float64)
+        live = (index >= 0) & (index < x.shape[1])
+        v = np.take_along_axis(x, np.where(live, index, 0).astype(np.int64), axis=1)
+        top = np.where(live, v, -np.inf).max(axis=1, keepdims=True)
+        low = np.where(live & np.isfinite(v), v, np.inf).min(axis=1, keepdims=True)
+        spread = np.where(np.isfinite(top) & np.isfinite(low) & (top < 0), top - low, 0.0)
+        e = e + MORE * FP32_U * 2 * np.minimum(spread, 104.0)
+    return e
+
+
 def route_weights_bound(logits, index, scoring, renormalise, scale):
-    return np.abs(route_weights(logits, index, scoring, renormalise, scale)) * score_error(logits, scoring) + 2.0 ** -125 * abs(scale)
+    w = np.abs(route_weights(logits, index, scoring, renormalise, scale))
+    return w * weight_error(logits, index, scoring, renormalise) + 2.0 ** -125 * abs(scale)
 
 
 def route_backward(dweight, logits, index, scoring, renormalise, scale):
-    """dlogits, by the chain rule through the scores (an index outside the experts takes no part)."""
+    """dlogits, by the chain rule through the scores.  An index outside the experts is a choice
+    that was never made: the others' shares are of their sum alone."""
     x = np.asarray(logits, np.float64)
     T, E = x.shape
     p = scores(x, scoring)
     live = (index >= 0) & (index < E)
     at = np.where(live, index, 0).astype(np.int64)
-    c = np.where(live, np.take_along_axis(p, at, axis=1), 0.0)
     g = np.where(live, np.asarray(dweight, np.float64) * scale, 0.0)
+    d = np.zeros((T, E))
     if renormalise:
-        s = c.sum(axis=1, keepdims=True)
-        safe = np.where(s == 0, 1.0, s)
-        g = np.where(s == 0, 0.0, (g - (g * c).sum(axis=1, keepdims=True) / safe) / safe)
-        g = np.where(live, g, 0.0)
-    dp = np.zeros((T, E))
+        # of w_i = c_i / s with c_i' = c_i (logistic: times 1 - c_i): w_i (g_i - sum w g) c_i' / c_i
+        w = chosen_shares(x, index, scoring)
+        g = np.where(live, w * (g - (w * g).sum(axis=1, keepdims=True)), 0.0)
     for j in range(index.shape[1]):
-        dp[np.arange(T)[live[:, j]], at[live[:, j], j]] += g[live[:, j], j]
+        d[np.arange(T)[live[:, j]], at[live[:, j], j]] += g[live[:, j], j]
     if scoring == "sigmoid":
-        return dp * p * scores(-x, "sigmoid")
-    if renormalise:
-        # the sum of dp p below is 0: sum_i c_i (g_i - sum(g c) / s) / s = (sum(g c) - s sum(g c) / s) / s
-        return p * dp
-    return p * (dp - (dp * p).sum(axis=1, keepdims=True))
+        return d * scores(-x, "sigmoid") * (1.0 if renormalise else p)
+    return d if renormalise else p * (d - (d * p).sum(axis=1, keepdims=True))
 
 
 def route_backward_bound(dweight, logits, index, scoring, renormalise, scale, t):
@@ -153,10 +181,7 @@ def route_backward_bound(dweight, logits, index, scoring, renormalise, scale, t)
     at = np.where(live, index, 0).astype(np.int64)
     c = np.where(live, np.take_along_axis(p, at, axis=1), 0.0)
     g = np.abs(np.where(live, np.asarray(dweight, np.float64) * scale, 0.0))
-    w = c
-    if renormalise:
-        s = c.sum(axis=1, keepdims=True)
-        w = np.where(s == 0, 0.0, c / np.where(s == 0, 1.0, s))
+    w = chosen_shares(x, index, scoring) if renormalise else c
     size = np.zeros(x.shape)
     for j in range(index.shape[1]):
         size[np.arange(len(x))[live[:, j]], at[live[:, j], j]] += w[live[:, j], j] * g[live[:, j], j]
@@ -167,7 +192,7 @@ def route_backward_bound(dweight, logits, index, scoring, renormalise, scale, t)
             of[np.arange(len(x))[live[:, j]], at[live[:, j], j]] = w[live[:, j], j]
     elif scoring == "softmax":
         of = p
-    e = (size + of * both) * (3 * score_error(x, scoring) + 20 * FP32_U) + 2.0 ** -125 * (1 + g.max(axis=1, keepdims=True))
+    e = (size + of * both) * (3 * weight_error(x, index, scoring, renormalise) + 20 * FP32_U) + 2.0 ** -125 * (1 + g.max(axis=1, keepdims=True))
     d = route_backward(dweight, logits, index, scoring, renormalise, scale)
     return e + round_half(np.abs(d) + e, t)
 
