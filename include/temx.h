@@ -381,10 +381,14 @@ TEMX_API te_mx_status te_mx_route(const void* logits, int64_t tokens, int32_t ex
 /* te_mx_route_backward — the gradient of te_mx_route's logits from that of its
  * weights (the choice itself has none).
  *   dweight  fp32 [tokens x k];  logits, index and the options as in the forward call;
- *            an index outside the experts (a choice dropped since) takes no part; the
- *            others of a token differ;
+ *            the indices of a token differ, but for those outside the experts;
  *   dlogits  [tokens x experts] of `dtype`, pitch ld_dlogits: every element is written;
- *            may not overlap logits. */
+ *            may not overlap logits.
+ * A choice dropped after the weights were made (its slot has no row) keeps its index
+ * here and has a dweight of 0, which te_mx_moe_combine_backward writes: with renormalise
+ * = 1 its score is part of the sum that divided the others, and its logit has a gradient.
+ * An index outside the experts is a choice that was never made: the gradient is that of
+ * weights renormalised over the others alone, which are not the forward call's. */
 TEMX_API te_mx_status te_mx_route_backward(const float* dweight, const void* logits, int64_t ld_logits,
                                            const int32_t* index, int64_t tokens, int32_t experts, int32_t dtype, int32_t k,
                                            int32_t scoring, int32_t renormalise, float scale, void* dlogits,

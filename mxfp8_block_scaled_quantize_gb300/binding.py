@@ -1025,7 +1025,9 @@ def route_backward(dweight, logits, index, scoring: str = "softmax", renormalise
                    stream=None, out=None):
     """The gradient of ``route``'s logits (their type, [tokens, experts]) from that
     of its weights (fp32 [tokens, k]); index and the options as in the forward
-    call (a negative index: a choice dropped since)."""
+    call.  A choice dropped after the weights were made keeps its index here, with
+    a dweight of 0 (``moe_combine_backward`` gives it that): its score is part of the
+    sum that divided the others.  A negative index is a choice that was never made."""
     if stream is not None:
         with _on(stream):
             return route_backward(dweight, logits, index, scoring=scoring, renormalise=renormalise, scale=scale, out=out)

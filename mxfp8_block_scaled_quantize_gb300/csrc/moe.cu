@@ -187,7 +187,8 @@ route_kernel(const RouteArgs a) {
 //   softmax                 dl_e = p_e ([e chosen] g_e - sum_j p_j g_j)
 //   logistic, renormalised  dl_i = w_i (1 - s_i) (g_i - sum_j w_j g_j)
 //   logistic                dl_i = s_i (1 - s_i) g_i
-// An index outside the experts (a dropped choice) takes no part.
+// An index outside the experts takes no part in any of it, the sums of w included: a choice
+// that was never made.  (One dropped after the weights were made has its index and g = 0.)
 template <typename T, int kN>
 __global__ void __launch_bounds__(kRouteWarps * 32)
 route_backward_kernel(const RouteArgs a) {
