@@ -303,7 +303,8 @@ TEMX_API te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, co
  *   y       [rows x hidden] of `dtype`, pitch ld_y;
  *   rsigma  fp32 [rows] or NULL: for the backward pass.
  * z may be x or residual, and y x or residual (the same pointer and pitch); other
- * overlaps of an output are refused (TE_MX_ERR_INVALID_ARG).  Pointers aligned to
+ * overlaps of an output (z, y, rsigma) with an operand or another output are refused
+ * (TE_MX_ERR_INVALID_ARG); rows side by side in one buffer (equal pitches) do not overlap.  Pointers aligned to
  * their elements; any hidden <= 2^24 and any pitches >= hidden (rows that start on
  * 16-byte boundaries are read and written 16 bytes at a time); rows == 0 or hidden
  * == 0 is a no-op.  Deterministic, as te_mx_layernorm. */
@@ -321,6 +322,7 @@ TEMX_API te_mx_status te_mx_rmsnorm(const void* x, int64_t rows, int64_t hidden,
  *           is given and q_col is, y may not be x;
  *   q_row/s_row, q_col/s_col  as te_mx_quantize (either pair may be NULL);
  *   rsigma  fp32 [rows] (required).
+ * Codes and scales over an operand or another output are refused, as the overlaps there.
  * Rules: hidden % 32 == 0 and hidden <= 32768; rows % 32 == 0 when q_col is given;
  * rows == 0 or hidden == 0 is a no-op. */
 TEMX_API te_mx_status te_mx_rmsnorm_quantize(const void* x, int64_t rows, int64_t hidden, int64_t ld_x,
@@ -339,9 +341,9 @@ TEMX_API te_mx_status te_mx_rmsnorm_quantize(const void* x, int64_t rows, int64_
  *   dz      [rows x hidden], pitch ld_dz: the gradient that reaches z by the residual
  *           path, or NULL (zero);
  *   dx      [rows x hidden], pitch ld_dx, or NULL (not computed); may be dy, z or dz
- *           (the same pointer and pitch); other overlaps are refused;
- *   dgamma  [hidden] of `param_dtype`, or NULL; may not overlap gamma.  With rows == 0 it
- *           is set to zero;
+ *           (the same pointer and pitch); other overlaps of an output or the workspace with
+ *           an operand or with each other are refused;
+ *   dgamma  [hidden] of `param_dtype`, or NULL.  With rows == 0 it is set to zero;
  *   workspace  device scratch of te_mx_rmsnorm_backward_workspace_size(rows, hidden)
  *           bytes, 16-byte aligned, for dgamma (else NULL); its contents on entry do
  *           not matter and it is clobbered.
@@ -366,7 +368,8 @@ typedef enum te_mx_scoring { TE_MX_SCORE_SOFTMAX = 0, TE_MX_SCORE_SIGMOID = 1 } 
  *           renormalise = 1: scale * p[index] / sum over the chosen of p.
  *   logits  [tokens x experts] of `dtype`, pitch ld_logits >= experts (device);
  *   bias    fp32 [experts] or NULL;
- *   index   int32 [tokens x k];  weight  fp32 [tokens x k].
+ *   index   int32 [tokens x k];  weight  fp32 [tokens x k]; they overlap neither each
+ *           other nor logits or bias.
  * An expert masked with -inf has the score 0, and is chosen only after all others;
  * where all chosen are masked so, and renormalise = 1, the weights are 0 (of finite
  * logits they are the scores' shares, however small the scores).  A NaN logit is chosen
@@ -383,7 +386,7 @@ TEMX_API te_mx_status te_mx_route(const void* logits, int64_t tokens, int32_t ex
  *   dweight  fp32 [tokens x k];  logits, index and the options as in the forward call;
  *            the indices of a token differ, but for those outside the experts;
  *   dlogits  [tokens x experts] of `dtype`, pitch ld_dlogits: every element is written;
- *            may not overlap logits.
+ *            may not overlap an operand.
  * A choice dropped after the weights were made (its slot has no row) keeps its index
  * here and has a dweight of 0, which te_mx_moe_combine_backward writes: with renormalise
  * = 1 its score is part of the sum that divided the others, and its logit has a gradient.
@@ -421,8 +424,8 @@ TEMX_API te_mx_status te_mx_moe_sort(const int32_t* index, int64_t slots, int32_
  * written.  A row >= total_rows is skipped and makes te_mx_device_status() report
  * TE_MX_ERR_INVALID_ARG.  Any alignment (rows on 16-byte boundaries are copied 16
  * bytes at a time).  Its gradient is te_mx_moe_combine without weights.  Rules:
- * 1 <= k <= 32; tokens * k < 2^31; tokens * row_bytes <= 2^39; out does not overlap x,
- * nor out_scales scales; tokens == 0 or row_bytes == 0 is a no-op. */
+ * 1 <= k <= 32; tokens * k < 2^31; tokens * row_bytes <= 2^39; out and out_scales overlap
+ * neither each other nor an operand; tokens == 0 or row_bytes == 0 is a no-op. */
 TEMX_API te_mx_status te_mx_moe_dispatch(const void* x, int64_t ld_x, int64_t row_bytes, const uint8_t* scales,
                                          int64_t ld_scales, int64_t scale_bytes, const int32_t* row, int64_t tokens,
                                          int32_t k, int64_t total_rows, void* out, int64_t ld_out, uint8_t* out_scales,
@@ -455,7 +458,7 @@ TEMX_API te_mx_status te_mx_moe_combine(const void* y, int64_t ld_y, int64_t tot
  *         same pointer and pitch), other overlaps are refused.  Rows that no slot has
  *         are not written;
  *   dweight  fp32 [tokens x k], or NULL (not computed; y may then be NULL); 0 for a slot
- *         without a row.
+ *         without a row; may be weight.
  * Rules and device-side errors as te_mx_moe_combine. */
 TEMX_API te_mx_status te_mx_moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y,
                                                  int64_t total_rows, int64_t hidden, int32_t dtype, const int32_t* row,

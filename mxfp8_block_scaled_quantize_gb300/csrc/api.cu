@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 
 #include "ptx.cuh"
@@ -453,25 +454,42 @@ te_mx_status te_mx_grouped_gemm_wgrad(int32_t num_groups, const int32_t* group_m
     return gemm_launch(a, static_cast<cudaStream_t>(stream));
 }
 
-// An output may be an input (the same pointer and pitch) or lie apart from it; rows
-// side by side in one buffer (equal pitches) are apart.
-static bool apart_or_same(const void* out, int64_t out_rows, int64_t ld_out, const void* in, int64_t in_rows, int64_t ld_in,
-                          int64_t width, bool may_be_same) {
-    if (!out || !in || out_rows <= 0 || in_rows <= 0 || width <= 0) return true;
-    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
-    if (may_be_same && o == i && (ld_out == ld_in || (out_rows == 1 && in_rows == 1))) return true;
-    const uintptr_t o_end = o + uintptr_t((out_rows - 1) * ld_out + width), i_end = i + uintptr_t((in_rows - 1) * ld_in + width);
-    if (o >= i_end || i >= o_end) return true;
-    if (ld_out != ld_in) return false;
-    const uintptr_t d = (o > i ? o - i : i - o) % uintptr_t(ld_out);
-    return d >= uintptr_t(width) && d + uintptr_t(width) <= uintptr_t(ld_out);
+// An array that a call reads or writes: rows of `width` bytes, `ld` bytes apart.
+struct Span {
+    const char* name;
+    const void* p;
+    int64_t rows, ld, width;
+};
+static Span vector_span(const char* name, const void* p, int64_t bytes) { return {name, p, 1, bytes, bytes}; }
+
+// Whether the arrays share no byte; rows side by side in one buffer (equal pitches, or one
+// row between the other's) are apart.
+static bool apart(const Span& a, const Span& b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return true;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    if (pa >= pb + uintptr_t(b.rows - 1) * uintptr_t(b.ld) + uintptr_t(b.width) ||
+        pb >= pa + uintptr_t(a.rows - 1) * uintptr_t(a.ld) + uintptr_t(a.width))
+        return true;
+    if (a.rows == 1 && b.rows == 1) return false;
+    const int64_t ld = a.rows == 1 ? b.ld : a.ld;
+    if (ld <= 0 || (a.rows > 1 && b.rows > 1 && a.ld != b.ld)) return false;
+    const uintptr_t l = uintptr_t(ld), d = pa >= pb ? (pa - pb) % l : (l - (pb - pa) % l) % l;     // of a's rows behind b's
+    return d >= uintptr_t(b.width) && d + uintptr_t(a.width) <= l;
+}
+static bool same(const Span& a, const Span& b) { return a.p == b.p && (a.ld == b.ld || (a.rows == 1 && b.rows == 1)); }
+
+// An output has to lie apart from `others`, and from `or_same` unless it is one of them
+// (the same pointer and pitch).
+static te_mx_status keeps_apart(const Span& out, std::initializer_list<Span> others, std::initializer_list<Span> or_same = {}) {
+    for (const Span& s : others)
+        if (!apart(out, s)) return set_error(TE_MX_ERR_INVALID_ARG, "%s overlaps %s", out.name, s.name);
+    for (const Span& s : or_same)
+        if (!apart(out, s) && !same(out, s))
+            return set_error(TE_MX_ERR_INVALID_ARG, "%s overlaps %s without being it (the same pointer and pitch)", out.name, s.name);
+    return TE_MX_OK;
 }
 
 static int64_t element_bytes(int32_t dtype) { return dtype == TE_MX_FP32 ? 4 : 2; }
-
-static te_mx_status overlap_error(const char* out, const char* in) {
-    return set_error(TE_MX_ERR_INVALID_ARG, "%s overlaps %s without being it (the same pointer and pitch), or may not be it", out, in);
-}
 
 // Checks of the RMSNorm forward entry points past sizes and types.
 static te_mx_status validate_rms(const RmsArgs& a) {
@@ -486,17 +504,22 @@ static te_mx_status validate_rms(const RmsArgs& a) {
     if (a.residual) {
         if ((st = validate_ln_matrix(a.residual, a.ld_residual, a.hidden, a.dtype, "residual")) != TE_MX_OK) return st;
         if ((st = validate_ln_matrix(a.z, a.ld_z, a.hidden, a.dtype, "z")) != TE_MX_OK) return st;
-        if (!apart_or_same(a.z, a.rows, a.ld_z * b, a.x, a.rows, a.ld_x * b, w, true)) return overlap_error("z", "x");
-        if (!apart_or_same(a.z, a.rows, a.ld_z * b, a.residual, a.rows, a.ld_residual * b, w, true)) return overlap_error("z", "residual");
     }
-    if (a.y) {
-        if ((st = validate_ln_matrix(a.y, a.ld_y, a.hidden, a.dtype, "y")) != TE_MX_OK) return st;
-        // (the column-wise copy is made of x after y is written, if there is no z)
-        if (!apart_or_same(a.y, a.rows, a.ld_y * b, a.x, a.rows, a.ld_x * b, w, a.residual || !a.q_col)) return overlap_error("y", "x");
-        if (!apart_or_same(a.y, a.rows, a.ld_y * b, a.residual, a.rows, a.ld_residual * b, w, true)) return overlap_error("y", "residual");
-        if (!apart_or_same(a.y, a.rows, a.ld_y * b, a.z, a.rows, a.ld_z * b, w, false)) return overlap_error("y", "z");
-    }
-    return TE_MX_OK;
+    if (a.y && (st = validate_ln_matrix(a.y, a.ld_y, a.hidden, a.dtype, "y")) != TE_MX_OK) return st;
+    const Span x{"x", a.x, a.rows, a.ld_x * b, w}, residual{"residual", a.residual, a.rows, a.ld_residual * b, w};
+    const Span z{"z", a.z, a.rows, a.ld_z * b, w}, y{"y", a.y, a.rows, a.ld_y * b, w};
+    const Span gamma = vector_span("gamma", a.gamma, a.hidden * element_bytes(a.param_dtype)), rsigma = vector_span("rsigma", a.rsigma, 4 * a.rows);
+    if ((st = keeps_apart(z, {gamma, y}, {x, residual})) != TE_MX_OK) return st;
+    // (the column-wise copy is made of x after y is written, if there is no z)
+    if (!a.residual && a.q_col) st = keeps_apart(y, {gamma, x});
+    else st = keeps_apart(y, {gamma}, {x, residual});
+    if (st != TE_MX_OK || (st = keeps_apart(rsigma, {x, residual, gamma, z, y})) != TE_MX_OK) return st;
+    const Span q_row{"q_row", a.q_row, a.rows, a.hidden, a.hidden}, s_row{"s_row", a.s_row, a.rows, a.ld_s_row, a.hidden / 32};
+    const Span q_col{"q_col", a.q_col, a.hidden, a.rows, a.rows}, s_col{"s_col", a.s_col, a.hidden, a.ld_s_col, a.rows / 32};
+    if ((st = keeps_apart(q_row, {x, residual, gamma, z, y, rsigma})) != TE_MX_OK) return st;
+    if ((st = keeps_apart(s_row, {x, residual, gamma, z, y, rsigma, q_row})) != TE_MX_OK) return st;
+    if ((st = keeps_apart(q_col, {x, residual, gamma, z, y, rsigma, q_row, s_row})) != TE_MX_OK) return st;
+    return keeps_apart(s_col, {x, residual, gamma, z, y, rsigma, q_row, s_row, q_col});
 }
 
 te_mx_status te_mx_rmsnorm(const void* x, int64_t rows, int64_t hidden, int64_t ld_x, int32_t dtype,
@@ -568,20 +591,19 @@ te_mx_status te_mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* z
         if ((st = validate_ln_matrix(dy, ld_dy, hidden, dtype, "dy")) != TE_MX_OK) return st;
         if ((st = validate_ln_matrix(z, ld_z, hidden, dtype, "z")) != TE_MX_OK) return st;
         if (dz && (st = validate_ln_matrix(dz, ld_dz, hidden, dtype, "dz")) != TE_MX_OK) return st;
-        if (dx) {
-            if ((st = validate_ln_matrix(dx, ld_dx, hidden, dtype, "dx")) != TE_MX_OK) return st;
-            if (!apart_or_same(dx, rows, ld_dx * b, dy, rows, ld_dy * b, w, true)) return overlap_error("dx", "dy");
-            if (!apart_or_same(dx, rows, ld_dx * b, z, rows, ld_z * b, w, true)) return overlap_error("dx", "z");
-            if (!apart_or_same(dx, rows, ld_dx * b, dz, rows, ld_dz * b, w, true)) return overlap_error("dx", "dz");
-        }
-        if (dgamma) {
-            if (!workspace || workspace_bytes < te_mx_rmsnorm_backward_workspace_size(rows, hidden))
-                return set_error(TE_MX_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0),
-                                 te_mx_rmsnorm_backward_workspace_size(rows, hidden));
-            if (!aligned(workspace, 16)) return set_error(TE_MX_ERR_MISALIGNED, "workspace is not 16-byte aligned");
-            const int64_t pw = hidden * element_bytes(param_dtype);    // (blocks write dgamma while others read gamma)
-            if (!apart_or_same(dgamma, 1, pw, gamma, 1, pw, pw, false)) return overlap_error("dgamma", "gamma");
-        }
+        if (dx && (st = validate_ln_matrix(dx, ld_dx, hidden, dtype, "dx")) != TE_MX_OK) return st;
+        const size_t need = dgamma ? te_mx_rmsnorm_backward_workspace_size(rows, hidden) : 0;
+        if (need && (!workspace || workspace_bytes < need))
+            return set_error(TE_MX_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0), need);
+        if (need && !aligned(workspace, 16)) return set_error(TE_MX_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+        const int64_t pw = hidden * element_bytes(param_dtype);
+        const Span s_dy{"dy", dy, rows, ld_dy * b, w}, s_z{"z", z, rows, ld_z * b, w}, s_dz{"dz", dz, rows, ld_dz * b, w};
+        const Span s_dx{"dx", dx, rows, ld_dx * b, w}, s_gamma = vector_span("gamma", gamma, pw), s_dgamma = vector_span("dgamma", dgamma, pw);
+        const Span s_rsigma = vector_span("rsigma", rsigma, 4 * rows), s_work = vector_span("workspace", workspace, int64_t(need));
+        // (blocks write dgamma while others read gamma)
+        if ((st = keeps_apart(s_dx, {s_gamma, s_rsigma, s_dgamma}, {s_dy, s_z, s_dz})) != TE_MX_OK) return st;
+        if ((st = keeps_apart(s_dgamma, {s_dy, s_z, s_dz, s_gamma, s_rsigma})) != TE_MX_OK) return st;
+        if ((st = keeps_apart(s_work, {s_dy, s_z, s_dz, s_gamma, s_rsigma, s_dx, s_dgamma})) != TE_MX_OK) return st;
     } else if (!dgamma) {
         return TE_MX_OK;
     }
@@ -616,7 +638,13 @@ te_mx_status te_mx_route(const void* logits, int64_t tokens, int32_t experts, in
     t_last_error[0] = '\0';
     RouteArgs a{logits, tokens, ld_logits, experts, k, dtype, bias, scoring, renormalise == 1, scale, index, weight, nullptr, 0};
     te_mx_status st = validate_route(a, renormalise);
-    if (st != TE_MX_OK || tokens == 0 || (st = check_device(nullptr)) != TE_MX_OK) return st;
+    if (st != TE_MX_OK || tokens == 0) return st;
+    const int64_t b = element_bytes(dtype);
+    const Span s_logits{"logits", logits, tokens, ld_logits * b, experts * b}, s_bias = vector_span("bias", bias, 4 * int64_t(experts));
+    const Span s_index = vector_span("index", index, 4 * tokens * k), s_weight = vector_span("weight", weight, 4 * tokens * k);
+    if ((st = keeps_apart(s_index, {s_logits, s_bias})) != TE_MX_OK) return st;
+    if ((st = keeps_apart(s_weight, {s_logits, s_bias, s_index})) != TE_MX_OK) return st;
+    if ((st = check_device(nullptr)) != TE_MX_OK) return st;
     return route_launch(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -631,8 +659,9 @@ te_mx_status te_mx_route_backward(const float* dweight, const void* logits, int6
     if (st != TE_MX_OK || tokens == 0) return st;
     const int64_t b = element_bytes(dtype);
     if ((st = validate_ln_matrix(dlogits, ld_dlogits, experts, dtype, "dlogits")) != TE_MX_OK) return st;
-    if (!apart_or_same(dlogits, tokens, ld_dlogits * b, logits, tokens, ld_logits * b, experts * b, false))
-        return overlap_error("dlogits", "logits");
+    const Span s_logits{"logits", logits, tokens, ld_logits * b, experts * b}, s_dweight = vector_span("dweight", dweight, 4 * tokens * k);
+    const Span s_index = vector_span("index", index, 4 * tokens * k), s_dlogits{"dlogits", dlogits, tokens, ld_dlogits * b, experts * b};
+    if ((st = keeps_apart(s_dlogits, {s_logits, s_dweight, s_index})) != TE_MX_OK) return st;
     if ((st = check_device(nullptr)) != TE_MX_OK) return st;
     return route_backward_launch(a, static_cast<cudaStream_t>(stream));
 }
@@ -686,9 +715,11 @@ te_mx_status te_mx_moe_dispatch(const void* x, int64_t ld_x, int64_t row_bytes, 
     if (ld_x < row_bytes || ld_out < row_bytes) return set_error(TE_MX_ERR_MISALIGNED, "a row pitch is less than row_bytes");
     if (scales && (ld_scales < scale_bytes || ld_out_scales < scale_bytes))
         return set_error(TE_MX_ERR_MISALIGNED, "a scale pitch is less than scale_bytes");
-    if (!apart_or_same(out, total_rows, ld_out, x, tokens, ld_x, row_bytes, false)) return overlap_error("out", "x");
-    if (scales && !apart_or_same(out_scales, total_rows, ld_out_scales, scales, tokens, ld_scales, scale_bytes, false))
-        return overlap_error("out_scales", "scales");
+    const Span s_x{"x", x, tokens, ld_x, row_bytes}, s_scales{"scales", scales, tokens, ld_scales, scale_bytes};
+    const Span s_row = vector_span("row", row, 4 * tokens * k), s_out{"out", out, total_rows, ld_out, row_bytes};
+    const Span s_out_scales{"out_scales", out_scales, total_rows, ld_out_scales, scale_bytes};
+    if ((st = keeps_apart(s_out, {s_x, s_scales, s_row})) != TE_MX_OK) return st;
+    if ((st = keeps_apart(s_out_scales, {s_x, s_scales, s_row, s_out})) != TE_MX_OK) return st;
     DispatchArgs a{static_cast<const uint8_t*>(x), ld_x, row_bytes, scales, ld_scales, scale_bytes, row, tokens, total_rows, k,
                    static_cast<uint8_t*>(out), ld_out, out_scales, ld_out_scales};
     return moe_dispatch_launch(a, static_cast<cudaStream_t>(stream));
@@ -720,8 +751,9 @@ te_mx_status te_mx_moe_combine(const void* y, int64_t ld_y, int64_t total_rows, 
     if (total_rows > 0 && (st = validate_ln_matrix(y, ld_y, hidden, dtype, "y")) != TE_MX_OK) return st;
     if (residual && (st = validate_ln_matrix(residual, ld_residual, hidden, dtype, "residual")) != TE_MX_OK) return st;
     if ((st = validate_ln_matrix(out, ld_out, hidden, dtype, "out")) != TE_MX_OK) return st;
-    if (!apart_or_same(out, tokens, ld_out * b, y, total_rows, ld_y * b, w, false)) return overlap_error("out", "y");
-    if (!apart_or_same(out, tokens, ld_out * b, residual, tokens, ld_residual * b, w, true)) return overlap_error("out", "residual");
+    const Span s_y{"y", y, total_rows, ld_y * b, w}, s_residual{"residual", residual, tokens, ld_residual * b, w};
+    const Span s_row = vector_span("row", row, 4 * tokens * k), s_weight = vector_span("weight", weight, 4 * tokens * k);
+    if ((st = keeps_apart(Span{"out", out, tokens, ld_out * b, w}, {s_y, s_row, s_weight}, {s_residual})) != TE_MX_OK) return st;
     return moe_combine_launch(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -742,9 +774,13 @@ te_mx_status te_mx_moe_combine_backward(const void* dout, int64_t ld_dout, const
     if (total_rows > 0) {
         if (dweight && (st = validate_ln_matrix(y, ld_y, hidden, dtype, "y")) != TE_MX_OK) return st;
         if (dy && (st = validate_ln_matrix(dy, ld_dy, hidden, dtype, "dy")) != TE_MX_OK) return st;
-        if (!apart_or_same(dy, total_rows, ld_dy * b, a.y, total_rows, ld_y * b, w, true)) return overlap_error("dy", "y");
-        if (!apart_or_same(dy, total_rows, ld_dy * b, dout, tokens, ld_dout * b, w, false)) return overlap_error("dy", "dout");
     }
+    const Span s_dout{"dout", dout, tokens, ld_dout * b, w}, s_y{"y", a.y, total_rows, ld_y * b, w}, s_dy{"dy", dy, total_rows, ld_dy * b, w};
+    const Span s_row = vector_span("row", row, 4 * tokens * k), s_weight = vector_span("weight", weight, 4 * tokens * k);
+    const Span s_dweight = vector_span("dweight", dweight, 4 * tokens * k);
+    if ((st = keeps_apart(s_dy, {s_dout, s_row, s_weight}, {s_y})) != TE_MX_OK) return st;
+    // (a slot's weight is read by the warp that writes its dweight)
+    if ((st = keeps_apart(s_dweight, {s_dout, s_y, s_row, s_dy}, {s_weight})) != TE_MX_OK) return st;
     return moe_combine_backward_launch(a, static_cast<cudaStream_t>(stream));
 }
 
