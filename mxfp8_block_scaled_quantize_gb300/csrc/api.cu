@@ -622,7 +622,7 @@ static te_mx_status validate_route(const RouteArgs& a, int32_t renormalise) {
     if (!std::isfinite(a.scale)) return set_error(TE_MX_ERR_INVALID_ARG, "scale must be finite");
     if (a.k < 1 || a.k > 32 || a.experts < a.k || a.experts > 1024)
         return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "k=%d must be 1 .. 32 and experts=%d k .. 1024", int(a.k), int(a.experts));
-    if (a.tokens >= (int64_t(1) << 31) / a.k) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "tokens * k reaches 2^31");
+    if (a.tokens > ((int64_t(1) << 31) - 1) / a.k) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "tokens * k reaches 2^31");
     if (a.tokens == 0) return TE_MX_OK;
     if (!a.logits || !a.index || !a.weight) return set_error(TE_MX_ERR_INVALID_ARG, "logits, index and the weights are required");
     if (a.ld_logits < a.experts)
@@ -692,7 +692,7 @@ static te_mx_status validate_slots(int64_t tokens, int32_t k, int64_t total_rows
     if (tokens < 0 || total_rows < 0)
         return set_error(TE_MX_ERR_INVALID_ARG, "negative size %lld or %lld", (long long)tokens, (long long)total_rows);
     if (k < 1 || k > 32) return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "k=%d must be 1 .. 32", int(k));
-    if (tokens >= (int64_t(1) << 31) / k || total_rows >= int64_t(1) << 31)
+    if (tokens > ((int64_t(1) << 31) - 1) / k || total_rows >= int64_t(1) << 31)
         return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "tokens * k or total_rows reaches 2^31");
     return TE_MX_OK;
 }
