@@ -707,9 +707,10 @@ te_mx_status te_mx_moe_dispatch(const void* x, int64_t ld_x, int64_t row_bytes, 
     if (row_bytes < 0 || (scales && scale_bytes < 0)) return set_error(TE_MX_ERR_INVALID_ARG, "negative row size");
     if (tokens > 0 && row_bytes > (int64_t(1) << 39) / tokens)
         return set_error(TE_MX_ERR_UNSUPPORTED_SHAPE, "tokens * row_bytes exceeds 2^39");
-    if ((scales == nullptr) != (out_scales == nullptr))
-        return set_error(TE_MX_ERR_INVALID_ARG, "scales and out_scales must both be given or both be NULL");
     if (tokens == 0 || row_bytes == 0) return TE_MX_OK;
+    // (out and out_scales of no rows have no address)
+    if ((scales == nullptr) != (out_scales == nullptr) && (!scales || total_rows > 0))
+        return set_error(TE_MX_ERR_INVALID_ARG, "scales and out_scales must both be given or both be NULL");
     if (!x || (!out && total_rows > 0) || !row) return set_error(TE_MX_ERR_INVALID_ARG, "x, row and out are required");
     if (!aligned(row, 4)) return set_error(TE_MX_ERR_MISALIGNED, "row is not aligned to its elements");
     if (ld_x < row_bytes || ld_out < row_bytes) return set_error(TE_MX_ERR_MISALIGNED, "a row pitch is less than row_bytes");
