@@ -124,9 +124,9 @@ rms_backward_vec_kernel(const RmsBackwardArgs a, const RmsBwdShape sh, unsigned 
         group_barrier(1 + group, sh.group);
         return warp_sum(lane < gwarps ? part[lane] : 0.0f);
     };
-    // dx = rs g - rs c xh + dz, xh = z rs
+    // dx = rs (g - z (rs c)) + dz  (rs rs would be no number for rows near 0 with a tiny eps)
     auto dx_of = [&](int64_t row, uint32_t here, float r, float total) {
-        const uint64_t rs2 = f32x2::both(r), k2 = f32x2::both(-r * r * (total * inv_h));
+        const uint64_t rs2 = f32x2::both(r), k2 = f32x2::both(-r * (total * inv_h));
         const uint4* dz = a.dz ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.dz) + row * a.ld_dz) + t : nullptr;
         uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.ld_dx) + t;
 #pragma unroll
@@ -150,8 +150,8 @@ rms_backward_vec_kernel(const RmsBackwardArgs a, const RmsBwdShape sh, unsigned 
             uint64_t o[V::kPairs];
 #pragma unroll
             for (int k = 0; k < V::kPairs; ++k) {
-                o[k] = f32x2::fma(f32x2::mul(V::pair(d4, k), ga[v].pair(k)), rs2, f32x2::mul(V::pair(z4, k), k2));
-                if (dz) o[k] = f32x2::add(o[k], V::pair(w, k));
+                const uint64_t q = f32x2::fma(V::pair(z4, k), k2, f32x2::mul(V::pair(d4, k), ga[v].pair(k)));
+                o[k] = dz ? f32x2::fma(q, rs2, V::pair(w, k)) : f32x2::mul(q, rs2);
             }
             out[v * sh.group] = V::from_pairs(o);
         }
@@ -298,7 +298,7 @@ rms_backward_few_kernel(const RmsBackwardArgs a, int nvec, int col_blocks) {
         }
     }
     const float c = across_warps(warp_sum(f32x2::lo(s) + f32x2::hi(s)), part, warps, warp, lane) / float(a.hidden);
-    const uint64_t k2 = f32x2::both(-rs * rs * c);
+    const uint64_t k2 = f32x2::both(-rs * c);                // (as in the kernel above)
     uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.ld_dx);
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
@@ -310,8 +310,8 @@ rms_backward_few_kernel(const RmsBackwardArgs a, int nvec, int col_blocks) {
             uint64_t o[V::kPairs];
 #pragma unroll
             for (int k = 0; k < V::kPairs; ++k) {
-                o[k] = f32x2::fma(f32x2::mul(V::pair(wd[v], k), g.pair(k)), rs2, f32x2::mul(V::pair(wz[v], k), k2));
-                if (dz) o[k] = f32x2::add(o[k], V::pair(w, k));
+                const uint64_t q = f32x2::fma(V::pair(wz[v], k), k2, f32x2::mul(V::pair(wd[v], k), g.pair(k)));
+                o[k] = dz ? f32x2::fma(q, rs2, V::pair(w, k)) : f32x2::mul(q, rs2);
             }
             out[i] = V::from_pairs(o);
         }
