@@ -67,18 +67,15 @@ __device__ __forceinline__ void softmax_sum(const float (&l)[kN], float& most, f
 }
 
 // A chosen logit's share of the logistic scores of the chosen (-inf in lanes without a
-// choice); 0 where all are -inf.  A sum below 1/2 says that every chosen logit is
-// negative: the scores, which vanish below -88, are then taken relative to e^top with top
-// the largest of them, s e^-top = 1 / (e^top + e^(top - v)), the factor cancels, and the
-// largest is at least 1/2.  (A score that vanishes beside a sum of 1/2 or more is a share
-// below 2^-125.)
-__device__ __forceinline__ float logistic_share(float logit) {
-    float s = logistic(logit), sum = warp_sum(s);
-    if (sum < 0.5f) {
-        const float top = warp_max(logit);
-        s = logit == -INFINITY ? 0.0f : 1.0f / (expf(top) + expf(top - logit));
-        sum = warp_sum(s);
-    }
+// choice); 0 where all are -inf.  Scores vanish below -88, so they are taken relative to
+// e^top, s e^-top = 1 / (e^top + e^(top - v)), with top the largest chosen logit if that is
+// negative, else 0: the factor cancels, and the largest is at least 1/2.  (-top is the least
+// of max(-v, 0), whose bits are in the order of the numbers: one reduction.)  `rest`: 1 - s,
+// e^(top - v) times s e^-top; 1 where that is 0.
+__device__ __forceinline__ float logistic_share(float logit, float& rest) {
+    const float top = -__uint_as_float(__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(-logit, 0.0f))));
+    const float e = expf(top - logit), s = logit == -INFINITY ? 0.0f : 1.0f / (expf(top) + e), sum = warp_sum(s);
+    rest = s == 0.0f ? 1.0f : e * s;
     return sum == 0.0f ? 0.0f : s / sum;
 }
 
@@ -173,7 +170,8 @@ route_kernel(const RouteArgs a) {
         }
         w = sum == 0.0f ? 0.0f : w / sum;
     } else {
-        w = a.renormalise ? logistic_share(logit) : logistic(logit);
+        float rest;
+        w = a.renormalise ? logistic_share(logit, rest) : logistic(logit);
     }
     if (chosen) {
         a.index[token * a.k + lane] = mine;
@@ -230,12 +228,12 @@ route_backward_kernel(const RouteArgs a) {
             for (int i = 0; i < kN; ++i) d[i] = l[i] == -INFINITY ? 0.0f : -total * (expf(l[i] - most) * inv);
         }
     } else {
-        const float rest = logistic(-logit);
         if (a.renormalise) {
-            const float w = logistic_share(logit), total = warp_sum(w * g);
+            float rest;
+            const float w = logistic_share(logit, rest), total = warp_sum(w * g);
             mine = e < 0 ? 0.0f : w * rest * (g - total);
         } else {
-            mine = e < 0 ? 0.0f : logistic(logit) * rest * g;
+            mine = e < 0 ? 0.0f : logistic(logit) * logistic(-logit) * g;
         }
     }
     // the whole row, then the chosen experts' over it (the warp's stores in order)
