@@ -442,8 +442,10 @@ rms_backward_dx_kernel(const RmsBackwardArgs a) {
 }
 
 // Partial sums of dy xh over the rows blockIdx.y, blockIdx.y + parts, ...; a thread
-// owns kColsEach columns, kColThreads apart.
-constexpr int kColThreads = 256, kColsEach = 2;
+// owns kColsEach columns, kColThreads apart.  Few parts (one, from 1.2 million columns on)
+// have many rows each, so a sum is made of batches of kGammaBatch rows, and these of as many
+// batches: chains of 64 + 64 + the rest.
+constexpr int kColThreads = 256, kColsEach = 2, kGammaBatch = 64;
 template <typename T>
 __global__ void __launch_bounds__(kColThreads)
 rms_backward_gamma_kernel(const RmsBackwardArgs a, int parts) {
@@ -452,32 +454,48 @@ rms_backward_gamma_kernel(const RmsBackwardArgs a, int parts) {
     const int64_t c = int64_t(blockIdx.x) * (kColThreads * kColsEach) + threadIdx.x;
     const T* z = static_cast<const T*>(a.z) + c;
     const T* dy = static_cast<const T*>(a.dy) + c;
-    float s[kColsEach];
+    float outer[kColsEach], total[kColsEach];
 #pragma unroll
-    for (int e = 0; e < kColsEach; ++e) s[e] = 0.0f;
+    for (int e = 0; e < kColsEach; ++e) outer[e] = total[e] = 0.0f;
     constexpr int kAhead = 4;                              // rows in flight
-    for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += kAhead * int64_t(parts)) {
-        T d[kAhead][kColsEach], v[kAhead][kColsEach];
-        float rs[kAhead];
+    int batches = 0;
+    for (int64_t r0 = blockIdx.y; r0 < a.rows;) {
+        float s[kColsEach];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int64_t r = r0 + k * int64_t(parts);
-            rs[k] = r < a.rows ? a.rsigma[r] : 0.0f;
+        for (int e = 0; e < kColsEach; ++e) s[e] = 0.0f;
+        const int64_t past = r0 + kGammaBatch * int64_t(parts), end = past < a.rows ? past : a.rows;
+        for (; r0 < end; r0 += kAhead * int64_t(parts)) {
+            T d[kAhead][kColsEach], v[kAhead][kColsEach];
+            float rs[kAhead];
 #pragma unroll
-            for (int e = 0; e < kColsEach; ++e) {
-                const bool live = r < a.rows && c + e * kColThreads < a.hidden;
-                d[k][e] = live ? dy[r * a.ld_dy + e * kColThreads] : from_f32<T>(0.0f);
-                v[k][e] = live ? z[r * a.ld_z + e * kColThreads] : from_f32<T>(0.0f);
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t r = r0 + k * int64_t(parts);
+                rs[k] = r < a.rows ? a.rsigma[r] : 0.0f;
+#pragma unroll
+                for (int e = 0; e < kColsEach; ++e) {
+                    const bool live = r < a.rows && c + e * kColThreads < a.hidden;
+                    d[k][e] = live ? dy[r * a.ld_dy + e * kColThreads] : from_f32<T>(0.0f);
+                    v[k][e] = live ? z[r * a.ld_z + e * kColThreads] : from_f32<T>(0.0f);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                for (int e = 0; e < kColsEach; ++e) s[e] = fmaf(to_f32(d[k][e]), to_f32(v[k][e]) * rs[k], s[e]);
+        }
+        const bool full = ++batches % kGammaBatch == 0;
+#pragma unroll
+        for (int e = 0; e < kColsEach; ++e) {
+            outer[e] += s[e];
+            if (full) {
+                total[e] += outer[e];
+                outer[e] = 0.0f;
             }
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-            for (int e = 0; e < kColsEach; ++e) s[e] = fmaf(to_f32(d[k][e]), to_f32(v[k][e]) * rs[k], s[e]);
     }
 #pragma unroll
     for (int e = 0; e < kColsEach; ++e)
-        if (c + e * kColThreads < a.hidden) a.partial[int64_t(blockIdx.y) * a.hidden + c + e * kColThreads] = s[e];
+        if (c + e * kColThreads < a.hidden) a.partial[int64_t(blockIdx.y) * a.hidden + c + e * kColThreads] = total[e] + outer[e];
 }
 
 // dgamma from `parts` partial sums per column.  A block owns 32 columns (lane =
