@@ -539,12 +539,12 @@ cudaError_t backward_vec_launch(const RmsBackwardArgs& a, int nvec, int streams,
     RmsBwdShape sh{};
     sh.nvec = nvec;
     sh.streams = streams;
-    const int row_bytes = streams * nvec * 16, least = kOnce ? 1 : 2;
+    const int row_bytes = streams * nvec * 16;
     sh.group = row_threads(nvec, kV);
     sh.groups = kMost / sh.group;
     if (sh.groups > kBwdMaxGroups) sh.groups = kBwdMaxGroups;
     if (sh.groups > a.rows) sh.groups = int(a.rows);
-    while (sh.groups > 1 && least * sh.groups * row_bytes > kBwdSmem) --sh.groups;
+    // (several groups hold 2048 vectors at most between them, so two rows each of three operands fit)
     sh.stages = kOnce ? 1 : kBwdSmem / (sh.groups * row_bytes);
     if (sh.stages > kBwdMaxStages) sh.stages = kBwdMaxStages;
     const int ring = sh.groups * sh.stages * row_bytes, sums = sh.groups * nvec * Vec<T>::kN * 4;
@@ -569,7 +569,7 @@ cudaError_t backward_vec_launch(const RmsBackwardArgs& a, int nvec, int streams,
 
 // Vectors of a row that the ring kernel takes: kBwdV<T> in each of up to 896 threads, or
 // twice as many in each of 512 (both hold their sums and gamma in registers); 128 KB of
-// dy and z at most.
+// dy and z at most (64 KB of 16-bit elements, so three operands' rows fit twice).
 template <typename T> constexpr int kBwdV = sizeof(T) == 4 ? 4 : 2;
 template <typename T> constexpr int kBwdMostVectors = 2 * kBwdV<T> * 512;
 
@@ -579,15 +579,19 @@ cudaError_t backward_vec(const RmsBackwardArgs& a, int sms, unsigned int* status
     const int nvec = int(a.hidden / Vec<T>::kN);
     // (dz in the ring too where two rows then fit)
     const int streams = a.dz && 2 * 3 * 16 * nvec <= kBwdSmem ? 3 : 2;
-    if (2 * streams * 16 * nvec > kBwdSmem) return backward_vec_launch<T, kP32, 2 * kV, 512, true>(a, nvec, 2, sms, status, parts, stream);
     if (nvec <= kV * 512) return backward_vec_launch<T, kP32, kV, 512, false>(a, nvec, streams, sms, status, parts, stream);
-    if (nvec <= kV * 896) return backward_vec_launch<T, kP32, kV, 896, false>(a, nvec, streams, sms, status, parts, stream);
-    return backward_vec_launch<T, kP32, 2 * kV, 512, false>(a, nvec, streams, sms, status, parts, stream);
+    if constexpr (sizeof(T) == 4) {
+        // (from 3201 vectors on two rows of dy and z do not fit)
+        if (2 * 2 * 16 * nvec <= kBwdSmem) return backward_vec_launch<T, kP32, kV, 896, false>(a, nvec, streams, sms, status, parts, stream);
+        return backward_vec_launch<T, kP32, 2 * kV, 512, true>(a, nvec, 2, sms, status, parts, stream);
+    } else {
+        if (nvec <= kV * 896) return backward_vec_launch<T, kP32, kV, 896, false>(a, nvec, streams, sms, status, parts, stream);
+        return backward_vec_launch<T, kP32, 2 * kV, 512, false>(a, nvec, streams, sms, status, parts, stream);
+    }
 }
 
-// One launch for dx and dgamma: see rms_backward_few_kernel.
-bool few_rows(int64_t rows, int64_t nvec) { return nvec <= 8 * kFewThreads && rows <= kFewRows; }
-
+// One launch for dx and dgamma: see rms_backward_few_kernel.  (Up to kBwdMostVectors: more
+// than four per thread are rows of fp32.)
 template <typename T, bool kP32>
 cudaError_t backward_few(const RmsBackwardArgs& a, cudaStream_t stream) {
     const int nvec = int(a.hidden / Vec<T>::kN);
@@ -598,8 +602,9 @@ cudaError_t backward_few(const RmsBackwardArgs& a, cudaStream_t stream) {
     const dim3 grid(unsigned(col_blocks + (a.dx ? a.rows : 0))), block{unsigned(threads)};
     if (v == 1) return launch_dependent(rms_backward_few_kernel<T, kP32, 1>, grid, block, stream, a, nvec, col_blocks);
     if (v == 2) return launch_dependent(rms_backward_few_kernel<T, kP32, 2>, grid, block, stream, a, nvec, col_blocks);
-    if (v == 4) return launch_dependent(rms_backward_few_kernel<T, kP32, 4>, grid, block, stream, a, nvec, col_blocks);
-    return launch_dependent(rms_backward_few_kernel<T, kP32, 8>, grid, block, stream, a, nvec, col_blocks);
+    if constexpr (sizeof(T) == 4)
+        if (v == 8) return launch_dependent(rms_backward_few_kernel<T, kP32, 8>, grid, block, stream, a, nvec, col_blocks);
+    return launch_dependent(rms_backward_few_kernel<T, kP32, 4>, grid, block, stream, a, nvec, col_blocks);
 }
 
 // dx shares memory with dy or z (then the columns' sums must not read after dx is written).
@@ -614,7 +619,7 @@ template <typename T, typename P, int kE>
 cudaError_t backward_any_launch(const RmsBackwardArgs& a, int sms, int* parts, cudaStream_t stream) {
     const int tx = row_threads(a.hidden, kE);
     int ty = kAnyThreads / tx;
-    if (ty > 15) ty = tx == 32 ? 16 : 15;                  // (named barriers; a warp alone needs none)
+    // (16 at most, a warp each, which need no named barrier; else 8 at most)
     if (ty > a.rows) ty = int(a.rows);
     const int64_t want = (a.rows + ty - 1) / ty;
     int64_t most = int64_t(kAnyBlocks<kE>) * sms;
@@ -649,7 +654,7 @@ cudaError_t backward(const RmsBackwardArgs& a, int sms, unsigned int* status, cu
     int n = 0;
     if (a.rows > 0 && a.hidden % Vec<T>::kN == 0 && nvec <= kBwdMostVectors<T> && fits(a.z, a.ld_z) && fits(a.dy, a.ld_dy) &&
         fits(a.dz, a.ld_dz) && fits(a.dx, a.ld_dx) && on16(a.gamma)) {
-        if (few_rows(a.rows, nvec) && !dx_overlaps<T>(a)) {
+        if (a.rows <= kFewRows && !dx_overlaps<T>(a)) {
             if constexpr (sizeof(T) == 2)
                 if (a.param_dtype != TE_MX_FP32) return backward_few<T, false>(a, stream);
             return backward_few<T, true>(a, stream);
