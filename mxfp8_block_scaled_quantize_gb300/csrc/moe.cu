@@ -265,6 +265,8 @@ constexpr int kSortCluster = 16;                 // blocks at most (8 without th
 constexpr int kMaxExperts = 1024;
 constexpr int kSortHeld = 16;                    // groups of 32 slots in a warp's registers
 constexpr int kSortBlockSlots = 32 * kSortWarps * kSortHeld;
+// (a round's groups times its warps: products of both are ints)
+static_assert(int64_t(kSortCluster) * kSortBlockSlots / 32 * (kSortCluster * kSortWarps) < int64_t(1) << 31);
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -355,7 +357,7 @@ moe_sort_kernel(const int32_t* __restrict__ index, int64_t slots, int32_t expert
         const int64_t first = round * per_round;
         const int in_round = int(slots - first < per_round ? slots - first : per_round);
         const int groups = (in_round + 31) / 32, parts = blocks * kWarps, part = int(rank) * kWarps + warp;
-        const int g0 = groups * part / parts, n = groups * (part + 1) / parts - g0;    // (at most 4096 x 256; at most kSortHeld)
+        const int g0 = groups * part / parts, n = groups * (part + 1) / parts - g0;    // (n: at most kSortHeld)
         const int of_block = 32 * (groups * (int(rank) * kWarps) / parts), s0 = 32 * g0 + lane;
         const int32_t* from = index + first + s0;
         int32_t of[kSortHeld];                             // expert << 16 | rank; -1: none
