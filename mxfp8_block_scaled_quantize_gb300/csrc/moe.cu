@@ -26,10 +26,13 @@ namespace {
 // bytes of 16384 x 128 bf16 take 0.6 us): a key of 16 bits (bf16 or fp16 logits without
 // a bias: kPacked) shares a word with its index, so that one maximum over the warp
 // gives both, and the chosen logits are read again at the end (16384 x 128 bf16, k = 8,
-// both directions: 12.0 us; with two maxima over the warp and a shuffle per choice 16.2).
-// For enough choices a lane first sorts its words: a round then looks at one of them (11.3
-// us; 16384 x 256, forward: 10.1, 11.4).  Keys of 32 bits with their index are pairs, and
-// sorted as such were slower (16384 x 256 fp32, k = 4: 12.6, 11.0).
+// both directions, unsorted: 12.0 us; with two maxima over the warp and a shuffle per choice 16.2).
+// For enough choices a lane first sorts its words: a round then looks at one of them (both
+// directions 11.1).  On either side of the rule, forward, 16384 tokens, us (this, without the
+// sorted path in the kernel): 128 experts k = 8 6.5, 7.6, k = 1 4.8, 5.3; 256 k = 4 8.4, 8.8,
+// k = 3 7.9, 8.1; 512 k = 8 16.7, 18.4, but below the rule k = 7 17.0, 16.4, k = 3 12.4, 11.8.
+// Keys of 32 bits with their index are pairs, and sorted as such were slower (16384 x 256
+// fp32, k = 4: 12.6, 11.0).
 constexpr int kRouteWarps = 8;
 
 __device__ __forceinline__ uint32_t ordered_key(float v) {
