@@ -304,10 +304,10 @@ TEMX_API te_mx_status te_mx_layernorm_backward(const void* dy, int64_t ld_dy, co
  *   rsigma  fp32 [rows] or NULL: for the backward pass.
  * z may be x or residual, and y x or residual (the same pointer and pitch); other
  * overlaps of an output (z, y, rsigma) with an operand or another output are refused
- * (TE_MX_ERR_INVALID_ARG); rows side by side in one buffer (equal pitches) do not overlap.  Pointers aligned to
- * their elements; any hidden <= 2^24 and any pitches >= hidden (rows that start on
- * 16-byte boundaries are read and written 16 bytes at a time); rows == 0 or hidden
- * == 0 is a no-op.  Deterministic, as te_mx_layernorm. */
+ * (TE_MX_ERR_INVALID_ARG); rows side by side in one buffer (equal pitches) do not
+ * overlap.  Pointers aligned to their elements; any hidden <= 2^24 and any pitches >=
+ * hidden (rows that start on 16-byte boundaries are read and written 16 bytes at a
+ * time); rows == 0 or hidden == 0 is a no-op.  Deterministic, as te_mx_layernorm. */
 TEMX_API te_mx_status te_mx_rmsnorm(const void* x, int64_t rows, int64_t hidden, int64_t ld_x, int32_t dtype,
                                     const void* residual, int64_t ld_residual, const void* gamma, int32_t param_dtype,
                                     float eps, void* z, int64_t ld_z, void* y, int64_t ld_y, float* rsigma,

@@ -275,13 +275,13 @@ rms_forward_long_kernel(const RmsArgs a) {
 // fl(max fl(z rs) gamma): rounding keeps the order, so gamma enters after the maximum.
 // Blocks go from the last rows to the first: what the kernel above wrote last is still
 // in L2 (it reads x and the residual as data that is not read again).  8192 x 7168: 30.5 us
-// (floor 26) with six blocks per SM, 80 registers each; with four, 100 registers, 34 (with the
-// row kernel, six and four: 16384 x 1024 26.9, 27.7; 2048 x 4096 15.4, 15.0; 512 x 4096 7.7,
-// 7.0; 160 x 7168 7.6, 7.4); with seven, spilled, 33; half the rows in each half of a warp, 48 registers, 32.5; four columns
-// x 16 rows per lane 33.  Tried, with four blocks and single bytes: persistent with the next
-// tile's words in registers 40, TMA loads and stores in a ring per warp 40, both copies in
-// one pass over z in the shared memory of clusters (three blocks of 256 threads per SM) 145
-// to 168 for all of it, against 104 with the two kernels.
+// (floor 26) with six blocks per SM, 80 registers each; with four, 100 registers, 34 (both
+// kernels, six and four: 16384 x 1024 26.9, 27.7; 2048 x 4096 15.4, 15.0; 512 x 4096 7.7, 7.0;
+// 160 x 7168 7.6, 7.4); with seven, spilled, 33; half the rows in each half of a warp, 48
+// registers, 32.5; four columns x 16 rows per lane 33.  Tried, with four blocks and single
+// bytes: persistent with the next tile's words in registers 40, TMA loads and stores in a ring
+// per warp 40, both copies in one pass over z in the shared memory of clusters (three blocks of
+// 256 threads per SM) 145 to 168 for all of it, against 104 with the two kernels.
 constexpr int kColWarps = 4;
 template <bool kP32>
 __global__ void __launch_bounds__(kColWarps * 32, 6)
